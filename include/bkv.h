@@ -278,6 +278,140 @@ bkv_status bkv_score_noalloc(const bkv_cache_desc *desc, const void *k,
                              const void *beacons, int32_t n_beacons, int32_t M,
                              float scale, float *scores, void *stream);
 
+/* ------------------------------------------------------------------------
+ * The 8-bit cache.  The pages have no counterpart: these entry points serve a
+ * decode loop that holds its KV cache in half the bytes and evicts by the
+ * attention the cached rows have received, next to the beacon scores above.
+ *
+ * Layout: codes are OCP FP8 E4M3 bytes (S.1111.111 is NaN, no infinities),
+ * [n_seqs][n_kv_heads][capacity][head_dim]; block b of a head (rows b*block ..
+ * b*block+block-1) has one f32 scale for K and one for V,
+ * [n_seqs][n_kv_heads][capacity / block].  The value held is code * scale.  A
+ * scale is a power of two: the smallest not under 2^-117 for which the
+ * largest finite magnitude of the block's rows is at most 448 scale, when
+ * bkv_cache8_append fills the block at once and after every bkv_cache8_evict;
+ * rows appended to a block that already holds some can only raise it, and the
+ * older codes are then rounded again to the new scale (exact, but for those
+ * that leave e4m3's normal range).  An element that is not finite is held as
+ * NaN.  Rows and scales past a sequence's length may hold anything.
+ *
+ * "Sequences" are independent caches served by one call: the sequences of a
+ * decode batch in one layer, or the layers (times sequences) of a whole cache.
+ * Their lengths are int32 [n_seqs] on the device (a captured graph replays
+ * with the lengths of the moment), read by every call as the length that
+ * includes the call's own new rows:
+ *
+ *   lens += 1                               (once per decode step)
+ *   per layer:  bkv_cache8_append(..., lens, k_new, v_new, T = 1, ...)
+ *               bkv_cache8_attend(..., lens, max_len, q, T = 1, ...)
+ *   when over budget:  bkv_cache8_evict(..., lens, ..., K, ..., new_lens = lens)
+ *
+ * A padded batch gives n_new, int32 [n_seqs] on the device: sequence s has
+ * n_new[s] <= T new tokens, the first rows of its [T] rows; NULL means T for
+ * all.  With n_new[s] == 0 nothing of the sequence is written.
+ * A length or count out of range (negative, past capacity or max_len,
+ * n_new > T, for an append n_new > length) leaves that sequence as it was and
+ * is reported by bkv_read_device_status as BKV_ERR_DEVICE_ASSERT.
+ *
+ * Supported: dtype (of new rows, queries and outputs) bf16 or f32, head_dim a
+ * multiple of 16 up to 128, block 16, 32, 64 or 128, capacity a multiple of
+ * block, n_seqs * n_kv_heads at most 65535.  Codes, new rows, queries and
+ * outputs are 16-byte aligned, the rest 4-byte.  Attention uses the tensor
+ * cores for bf16 with head_dim 64 or 128 and the CUDA cores otherwise. */
+typedef struct {
+  int32_t n_seqs;
+  int32_t n_q_heads;   /* multiple of n_kv_heads */
+  int32_t n_kv_heads;
+  int32_t head_dim;
+  int64_t capacity;    /* rows allocated per (sequence, KV head) */
+  int32_t block;       /* rows that share a scale */
+  int32_t dtype;       /* bkv_dtype of new rows, queries and outputs */
+} bkv_cache8_desc;
+
+/* Bytes of workspace for bkv_cache8_attend with T tokens (T = 0: not called;
+ * weights != 0: with weights_out) and bkv_cache8_evict with budget K (K = 0:
+ * not called) over lengths up to max_len.  0 for invalid arguments.  Calls
+ * that can overlap on the GPU need a workspace each. */
+size_t bkv_cache8_workspace_size(const bkv_cache8_desc *desc, int64_t max_len,
+                                 int32_t T, int64_t K, int32_t weights);
+
+/* Append: rows lens[s] - n .. lens[s] - 1 of every sequence (n = n_new[s] or
+ * T) are quantised from the first n of
+ *   k_new, v_new  device, [n_seqs][n_kv_heads][T][head_dim].
+ * A block whose first row is among them takes the scale of its new rows, one
+ * that holds older rows the larger of its own and the new rows'.
+ * Requires 1 <= T <= capacity. */
+bkv_status bkv_cache8_append(const bkv_cache8_desc *desc, void *k8, void *v8,
+                             float *k_scale, float *v_scale,
+                             const int32_t *lens, const void *k_new,
+                             const void *v_new, int32_t T, const int32_t *n_new,
+                             void *stream);
+
+/* Attention of the newest n tokens (n = n_new[s] or T) over the cache.  Token
+ * t < n of query head h sees the keys j < lens[s] - n + t + 1:
+ *   out[s][h][t] = sum_j p_j v_j,  p = softmax_j(scale q . k_j),
+ *   lse[s][h][t] = log sum_j exp(scale q . k_j);
+ * a token that sees no key gets zeros and -infinity.
+ *   q, out      device, [n_seqs][n_q_heads][T][head_dim]; rows t >= n are not
+ *               read, and left as they were
+ *   lse         device, f32 [n_seqs][n_q_heads][T], optional
+ *   scale       0 means 1/sqrt(head_dim)
+ *   max_len     host: an upper bound of lens (sizes the launches)
+ *   weights_out device, f32 [n_seqs][n_kv_heads][capacity], optional: the
+ *               attention weight of every row j < lens[s],
+ *                 decay * weights_in[j] + sum of p_j over the KV head's n * G
+ *                 query rows,
+ *               without the first term for the call's own rows
+ *               j >= lens[s] - n (a new row starts at zero); rows
+ *               j >= lens[s] are left as they were
+ *   weights_in  device, like weights_out, optional (NULL: zeros); may be
+ *               weights_out itself
+ * Products are summed in f32, f32 queries on the CUDA cores.  With bf16 the
+ * probabilities are rounded to f16 for the second product (2^-11); the
+ * weights and lse come from f32.  Results do not depend on timing: sums run
+ * in an order fixed by the lengths.
+ * Requires 1 <= max_len <= capacity, 1 <= T. */
+bkv_status bkv_cache8_attend(const bkv_cache8_desc *desc, const void *k8,
+                             const void *v8, const float *k_scale,
+                             const float *v_scale, const int32_t *lens,
+                             int64_t max_len, const void *q, int32_t T,
+                             const int32_t *n_new, float scale, void *out,
+                             float *lse, const float *weights_in,
+                             float *weights_out, float decay, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
+/* Eviction by accumulated attention weight.  Every (sequence, KV head) of
+ * length L = lens[s] > K keeps its first `sink` rows, its last `recent` rows
+ * and, of the rest, the K - sink - recent with the largest weights (ties: the
+ * lower position; a NaN weight ranks last); one of L <= K keeps every row.
+ * The kept rows move, in ascending order, to rows 0 .. min(K, L) - 1 of the
+ * destination, with their weights, and every block of the destination takes
+ * the scale of its rows (values are as before but for codes that leave
+ * e4m3's normal range under their new block's scale).
+ *   weights      device, f32 [n_seqs][n_kv_heads][capacity]
+ *   dst          geometry of the destination: n_seqs, n_kv_heads, head_dim and
+ *                block as in desc, capacity >= min(K, max_len)
+ *   *_dst        device; either all of the codes' and scales' buffers are the
+ *                source's (with dst's capacity equal: in place, ordered so
+ *                that no row is overwritten before it is read) or none
+ *                overlaps it.  weights_dst is optional, and may be weights in
+ *                place
+ *   idx          device out, optional int32 [n_seqs][n_kv_heads][K]: the kept
+ *                positions, the first min(K, L) of each row
+ *   new_lens     device out, optional int32 [n_seqs]: min(K, L); may be lens
+ * Requires 1 <= K, sink + recent <= K, 1 <= max_len <= capacity; max_len
+ * up to 786432 (BKV_ERR_UNSUPPORTED past that). */
+bkv_status bkv_cache8_evict(const bkv_cache8_desc *desc, const void *k8,
+                            const void *v8, const float *k_scale,
+                            const float *v_scale, const float *weights,
+                            const int32_t *lens, int64_t max_len, int64_t K,
+                            int32_t sink, int32_t recent,
+                            const bkv_cache8_desc *dst, void *k8_dst,
+                            void *v8_dst, float *k_scale_dst,
+                            float *v_scale_dst, float *weights_dst, int32_t *idx,
+                            int32_t *new_lens, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
 /* Device-side status.  Kernels never trap: a bounded wait that runs out or a
  * failed consistency check records BKV_ERR_TIMEOUT / BKV_ERR_DEVICE_ASSERT in
  * a status word of the library instead.  This call synchronises `stream`,

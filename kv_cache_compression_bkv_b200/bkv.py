@@ -29,7 +29,8 @@ STATUS = {0: "BKV_OK", 1: "BKV_ERR_INVALID_ARG", 2: "BKV_ERR_UNSUPPORTED",
 EXPORTS = ("bkv_workspace_size", "bkv_score", "bkv_select_topk", "bkv_compact",
            "bkv_update_beacons", "bkv_compress_step", "bkv_read_device_status",
            "bkv_status_string", "bkv_score_noalloc", "bkv_score_mean", "bkv_compact_inplace",
-           "bkv_selftest_wait_timeout")
+           "bkv_selftest_wait_timeout", "bkv_cache8_workspace_size", "bkv_cache8_append",
+           "bkv_cache8_attend", "bkv_cache8_evict")
 SCORE_NOALLOC_SCRATCH_BYTES = 32 << 20
 
 
@@ -43,6 +44,13 @@ class CacheDesc(ctypes.Structure):
     _fields_ = [("n_layers", ctypes.c_int32), ("n_q_heads", ctypes.c_int32),
                 ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("capacity", ctypes.c_int64), ("dtype", ctypes.c_int32)]
+
+
+class Cache8Desc(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int32), ("n_q_heads", ctypes.c_int32),
+                ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("capacity", ctypes.c_int64), ("block", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
 
 
 class StepArgs(ctypes.Structure):
@@ -72,6 +80,7 @@ def _load() -> ctypes.CDLL:
     P, I32, I64, SZ, F = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t,
                           ctypes.c_float)
     D = ctypes.POINTER(CacheDesc)
+    D8 = ctypes.POINTER(Cache8Desc)
     sig = {
         "bkv_workspace_size": ([D, I64, I32, I32, I32, I64], SZ),
         "bkv_score": ([D, P, I64, P, I32, P, I32, I32, F, P, P, SZ, P], ctypes.c_int),
@@ -87,6 +96,12 @@ def _load() -> ctypes.CDLL:
         "bkv_score_noalloc": ([D, P, I64, P, I32, P, I32, I32, F, P, P], ctypes.c_int),
         "bkv_score_mean": ([D, P, I64, P, I32, P, I32, I32, F, P, P, SZ, P], ctypes.c_int),
         "bkv_selftest_wait_timeout": ([I64, P, P], ctypes.c_int),
+        "bkv_cache8_workspace_size": ([D8, I64, I32, I64, I32], SZ),
+        "bkv_cache8_append": ([D8, P, P, P, P, P, P, P, I32, P, P], ctypes.c_int),
+        "bkv_cache8_attend": ([D8, P, P, P, P, P, I64, P, I32, P, F, P, P, P, P, F, P, SZ, P],
+                              ctypes.c_int),
+        "bkv_cache8_evict": ([D8, P, P, P, P, P, P, I64, I64, I32, I32, D8, P, P, P, P, P, P, P, P,
+                              SZ, P], ctypes.c_int),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -265,10 +280,80 @@ def bkv_compress_step(geom: Geometry, k, v, L: int, K: int, recent_q, R: int, be
     return nb.value, nl.value
 
 
+@dataclass(frozen=True)
+class Geometry8:
+    """Geometry of an 8-bit cache (bkv_cache8_desc)."""
+    n_seqs: int
+    n_q_heads: int
+    n_kv_heads: int
+    head_dim: int
+    capacity: int
+    block: int
+    dtype: torch.dtype   # of new rows, queries and outputs
+
+    def __post_init__(self):
+        d = Cache8Desc(self.n_seqs, self.n_q_heads, self.n_kv_heads, self.head_dim, self.capacity,
+                       self.block, dtype_code(self.dtype))
+        object.__setattr__(self, "_desc", d)
+        object.__setattr__(self, "_ref", ctypes.byref(d))
+
+    def desc(self) -> Cache8Desc:
+        return self._desc
+
+
+def geometry8_of(codes: torch.Tensor, scales: torch.Tensor, n_q_heads: int,
+                 dtype: torch.dtype) -> Geometry8:
+    """Geometry of codes [n_seqs, n_kv_heads, capacity, head_dim] (one byte each,
+    torch.float8_e4m3fn or uint8) with scales [n_seqs, n_kv_heads, capacity / block]."""
+    S, Hkv, cap, d = codes.shape
+    return Geometry8(S, n_q_heads, Hkv, d, cap, cap // scales.shape[2], dtype)
+
+
+def bkv_cache8_workspace_size(geom: Geometry8, max_len: int, T: int, K: int,
+                              weights: bool) -> int:
+    return int(LIB.bkv_cache8_workspace_size(geom._ref, max_len, T, K, int(weights)))
+
+
+def bkv_cache8_append(geom: Geometry8, k8, v8, k_scale, v_scale, lens, k_new, v_new, T: int,
+                      n_new=None, stream=None) -> None:
+    """Quantise the newest rows of every sequence into the cache (lens counts them)."""
+    _check(LIB.bkv_cache8_append(geom._ref, _ptr(k8), _ptr(v8), _ptr(k_scale), _ptr(v_scale),
+                                 _ptr(lens), _ptr(k_new), _ptr(v_new), T, _ptr(n_new),
+                                 _stream(stream)), "bkv_cache8_append")
+
+
+def bkv_cache8_attend(geom: Geometry8, k8, v8, k_scale, v_scale, lens, max_len: int, q, T: int,
+                      n_new, scale: float, out, lse, weights_in, weights_out, decay: float,
+                      workspace, stream=None) -> None:
+    """Attention of the newest tokens over the cache, with the rows' attention
+    weights where weights_out is given; lse, weights_in and weights_out may be None."""
+    _check(LIB.bkv_cache8_attend(geom._ref, _ptr(k8), _ptr(v8), _ptr(k_scale), _ptr(v_scale),
+                                 _ptr(lens), max_len, _ptr(q), T, _ptr(n_new), scale, _ptr(out),
+                                 _ptr(lse), _ptr(weights_in), _ptr(weights_out), decay,
+                                 _ptr(workspace),
+                                 0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                 _stream(stream)), "bkv_cache8_attend")
+
+
+def bkv_cache8_evict(geom: Geometry8, k8, v8, k_scale, v_scale, weights, lens, max_len: int,
+                     K: int, sink: int, recent: int, dst: Geometry8, k8_dst, v8_dst, k_scale_dst,
+                     v_scale_dst, weights_dst=None, idx=None, new_lens=None, workspace=None,
+                     stream=None) -> None:
+    """Keep the first sink, the last recent and the heaviest other rows, K in all,
+    in dst (in place when dst's buffers are the source's)."""
+    _check(LIB.bkv_cache8_evict(geom._ref, _ptr(k8), _ptr(v8), _ptr(k_scale), _ptr(v_scale),
+                                _ptr(weights), _ptr(lens), max_len, K, sink, recent, dst._ref,
+                                _ptr(k8_dst), _ptr(v8_dst), _ptr(k_scale_dst), _ptr(v_scale_dst),
+                                _ptr(weights_dst), _ptr(idx), _ptr(new_lens), _ptr(workspace),
+                                0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                _stream(stream)), "bkv_cache8_evict")
+
+
 def bkv_selftest_wait_timeout(limit_ns: int, outcome, stream=None) -> None:
     """Make one bounded device-side wait give up on purpose (diagnostic)."""
     _check(LIB.bkv_selftest_wait_timeout(limit_ns, _ptr(outcome), _stream(stream)),
-           "bkv_selftest_wait_timeout")
+           "bkv_selftest_wait_timeout", "bkv_cache8_workspace_size", "bkv_cache8_append",
+           "bkv_cache8_attend", "bkv_cache8_evict")
 
 
 def bkv_read_device_status(stream=None) -> tuple[int, int]:

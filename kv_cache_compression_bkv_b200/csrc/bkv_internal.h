@@ -135,6 +135,62 @@ bkv_status launch_fps_tc(const FpsGeom &g, const void *beacons_in, const void *w
 bkv_status launch_fps(const FpsGeom &g, const void *beacons_in, const void *window,
                       void *beacons_out, void *ws, size_t ws_bytes, cudaStream_t stream);
 
+// ---- the 8-bit cache (cache8.cuh): codes [n_seqs][n_kv_heads][cap][head_dim],
+// scales [n_seqs][n_kv_heads][cap / block], lengths and counts on the device
+struct Cache8AppendArgs {
+  uint8_t *k8, *v8;
+  float *k_scale, *v_scale;
+  const void *k_new, *v_new;   // [n_seqs][n_kv_heads][T][head_dim]
+  const int32_t *lens, *n_new; // lengths with the new rows; NULL n_new: T for all
+  int n_seqs, n_kv_heads, head_dim, block, T;
+  int blocks_per_seq;          // blocks that T rows can touch
+  long long cap;
+};
+bkv_status launch_cache8_append(const Cache8AppendArgs &a, int dtype, cudaStream_t stream);
+
+struct Cache8AttendArgs {
+  const uint8_t *k8, *v8;
+  const float *k_scale, *v_scale;
+  const int32_t *lens, *n_new;
+  const void *q;               // [n_seqs][n_q_heads][T][head_dim]
+  void *out;                   // like q
+  float *lse;                  // [n_seqs][n_q_heads][T] or NULL
+  const float *w_in;           // [n_seqs][n_kv_heads][cap] or NULL (zeros)
+  float *w_out;                // NULL: no weights
+  float decay, scale;          // scale of the logits
+  int n_seqs, n_q_heads, n_kv_heads, head_dim, block, T, group;
+  long long cap, max_len;
+};
+// what the launches of one call share: sizes and workspace sections, from the
+// host's sizes alone
+struct Cache8AttendPlan {
+  int nt;            // n-tiles of 8 query rows in a row block
+  int row_blocks;    // row blocks per (sequence, KV head)
+  int ctas;          // CTAs that share the key tiles
+  int x_cols;        // logits kept per key for the weights pass (0: none kept)
+  size_t part_off, lse_off, x_off, bytes;  // workspace sections
+};
+Cache8AttendPlan plan_cache8_attend(int n_seqs, int n_q_heads, int n_kv_heads, int head_dim,
+                                    int dtype, long long max_len, int T, bool weights);
+bkv_status launch_cache8_attend(const Cache8AttendArgs &a, const Cache8AttendPlan &plan, int dtype,
+                                void *ws, cudaStream_t stream);
+
+struct Cache8EvictArgs {
+  const uint8_t *k8, *v8;
+  const float *k_scale, *v_scale, *weights;
+  const int32_t *lens;
+  uint8_t *k8_dst, *v8_dst;
+  float *k_scale_dst, *v_scale_dst, *weights_dst;  // weights_dst may be NULL
+  int32_t *idx;                // [n_seqs][n_kv_heads][K]
+  int32_t *kept;               // [n_seqs], workspace: min(L, K), -1 for a bad length
+  int32_t *new_lens;           // [n_seqs] or NULL; may be lens
+  int n_seqs, n_kv_heads, head_dim, block, sink, recent;
+  long long cap, dst_cap, max_len, K;
+  int mask_words, ctas_per_head;  // filled by the launcher
+};
+constexpr long long kCache8EvictMaxLen = 786432;  // two position bitmasks in shared memory
+bkv_status launch_cache8_evict(Cache8EvictArgs a, bool in_place, cudaStream_t stream);
+
 // Fault injection for the host-side error paths: when the environment
 // variable BKV_INJECT_LAUNCH_FAILURE is set to a non-empty value other than
 // "0" when the library first checks it, every kernel launcher returns
@@ -164,5 +220,8 @@ int take_status_fps_tc(cudaStream_t, int *);
 int take_status_compact(cudaStream_t, int *);
 int take_status_fps(cudaStream_t, int *);
 int take_status_selftest(cudaStream_t, int *);
+int take_status_cache8_append(cudaStream_t, int *);
+int take_status_cache8_attend(cudaStream_t, int *);
+int take_status_cache8_evict(cudaStream_t, int *);
 
 }  // namespace bkv

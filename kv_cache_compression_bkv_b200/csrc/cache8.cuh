@@ -1,0 +1,98 @@
+// cache8.cuh -- what the kernels of the 8-bit cache share: the e4m3 codes, the
+// blocks' power-of-two scales, and the arguments each launcher takes.
+//
+// A cached value is code * scale: an e4m3 code per element and one scale for
+// each block of `block` consecutive rows of a head.  The scale of a block whose
+// largest magnitude is a is the smallest power of two s >= 2^-117 with
+// a <= 448 s, so dividing by it is exact and a code is the value rounded to
+// e4m3 (relative error at most 2^-4, absolute at most 2^-10 s below 2^-6 s);
+// moving a code to another block's scale is exact too, but for codes that
+// fall below e4m3's normal range.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace bkv {
+namespace cache8 {
+
+constexpr int kMinExp = -117;    // 448 * 2^-117 and 2^-9 * 2^-117 are normal floats
+constexpr uint32_t kNaN4 = 0x7f7f7f7fu;
+
+// The exponent of the scale of a block whose largest magnitude is `amax`
+// (finite, >= 0): 448 = 1.75 * 2^8, so with amax = m 2^k the exponent is k - 8
+// for m <= 1.75 and k - 7 above.
+__device__ __forceinline__ int scale_exp(float amax) {
+  const uint32_t b = __float_as_uint(amax);
+  const int e = static_cast<int>(b >> 23) - 127 - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return max(e, kMinExp);  // zeros and subnormals have exponent field 0
+}
+
+__device__ __forceinline__ float pow2f(int e) {  // -126 <= e <= 127
+  return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+
+__device__ __forceinline__ int exp_of(float pow2) {
+  return static_cast<int>(__float_as_uint(pow2) >> 23) - 127;
+}
+
+// two floats -> two e4m3 codes (lo in the low byte), round to nearest even
+__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// half pairs <-> code pairs; a code is exact in f16
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes16) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(codes16)));
+  return r;
+}
+__device__ __forceinline__ uint32_t f16x2_to_e4m3x2(uint32_t h2) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h2));
+  return r;
+}
+
+__device__ __forceinline__ __half2 as_half2(uint32_t x) {
+  return *reinterpret_cast<__half2 *>(&x);
+}
+__device__ __forceinline__ uint32_t as_u32(__half2 x) { return *reinterpret_cast<uint32_t *>(&x); }
+
+// Four codes moved from one block's scale to another's, multiplied by 2^k
+// (k = old exponent - new exponent).  In f16 the product is exact down to
+// 2^-21, far below the 2^-10 under which e4m3 rounds to zero; k > 15 takes a
+// second factor (a small old code under a far smaller new scale).
+__device__ __forceinline__ uint32_t rescale4(uint32_t codes, __half2 f1, __half2 f2) {
+  const uint32_t lo = as_u32(__hmul2(__hmul2(as_half2(e4m3x2_to_f16x2(codes)), f1), f2));
+  const uint32_t hi = as_u32(__hmul2(__hmul2(as_half2(e4m3x2_to_f16x2(codes >> 16)), f1), f2));
+  return f16x2_to_e4m3x2(lo) | (f16x2_to_e4m3x2(hi) << 16);
+}
+__device__ __forceinline__ void rescale_factors(int k, __half2 *f1, __half2 *f2) {
+  k = max(-24, min(k, 24));  // below 2^-24 every code becomes zero
+  const int a = max(-12, min(k, 12));
+  *f1 = __float2half2_rn(pow2f(a));
+  *f2 = __float2half2_rn(pow2f(k - a));
+}
+__device__ __forceinline__ uint4 rescale16(uint4 c, int k) {
+  __half2 f1, f2;
+  rescale_factors(k, &f1, &f2);
+  return make_uint4(rescale4(c.x, f1, f2), rescale4(c.y, f1, f2), rescale4(c.z, f1, f2),
+                    rescale4(c.w, f1, f2));
+}
+
+__device__ __forceinline__ __half2 absmax4(uint32_t codes, __half2 m) {
+  // __hmax2 returns the number where one operand is NaN, so NaN codes do not count
+  m = __hmax2(m, __habs2(as_half2(e4m3x2_to_f16x2(codes))));
+  return __hmax2(m, __habs2(as_half2(e4m3x2_to_f16x2(codes >> 16))));
+}
+__device__ __forceinline__ float absmax16(uint4 c) {
+  __half2 m = __float2half2_rn(0.f);
+  m = absmax4(c.w, absmax4(c.z, absmax4(c.y, absmax4(c.x, m))));
+  return fmaxf(__low2float(m), __high2float(m));
+}
+
+}  // namespace cache8
+}  // namespace bkv

@@ -1,0 +1,1126 @@
+// cache8_attend.cu -- attention over the 8-bit cache, and the sum of each
+// cached key's probabilities (its attention weight).
+//
+// For every (sequence, KV head) the query rows r = t * G + g (token t of the
+// newest n, query head g of the group) attend to the keys j < len - n + t + 1:
+//   x_rj = scale q_r . (code_j s_j),  p = softmax_j x,  o_r = sum_j p_rj v_j.
+//
+// Work split.  The unit is a tile of 128 keys of one (sequence, KV head, row
+// block); the tiles of the whole call, in that order, are cut into equal runs,
+// one per resident CTA, so a ragged batch leaves no CTA idle and a single long
+// sequence uses every SM.  A run can begin and end inside a (sequence, head,
+// row block), a "segment": a CTA that has a whole segment writes its output,
+// one that has a part writes (max, sum, unnormalised output) to its slot of
+// the workspace and attend_finish_kernel joins the parts in their order.  The
+// lengths are read on the device; the host needs only their upper bound.
+//
+// attend_mma_kernel (bf16, head_dim 64 or 128): decode is bound by the codes'
+// bytes, so each of the 8 warps streams its own 16 keys of every tile through
+// a private cp.async ring (no CTA barrier in the loop) and holds its own
+// softmax statistics and output.  Codes become f16, exactly, two at a time
+// (cvt.rn.f16x2.e4m3x2).  K is the A operand of mma.m16n8k16 and the 8 query
+// rows the B operand, so a group of up to 8 query heads costs no padding; V is
+// read transposed by ldmatrix.b8 and is the A operand of the second product.
+// Both products' reduction indices are permuted so that the four consecutive
+// bytes a lane holds are its fragment as they are: element order inside a
+// contraction is free.  Queries become f16 under a power-of-two factor per
+// row, exact but for elements 2^-24 and more below the row's largest.
+//   The probabilities are rounded to f16 (2^-11, summed in f32 before that),
+// multiplied by the block's V scale over the largest one met so far.
+//   The softmax reference of a row moves only when a logit exceeds it by more
+// than 8 (in log2): one vote per tile instead of a max over lanes.
+//
+// attend_simt_kernel (f32, and other head sizes): the same split with f32
+// products on the CUDA cores.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "bkv_device_status.cuh"
+#include "bkv_internal.h"
+#include "cache8.cuh"
+
+BKV_DEFINE_STATUS_ACCESSOR(take_status_cache8_attend)
+
+namespace bkv {
+namespace {
+
+using namespace cache8;
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kKeys = 16;                // keys per warp and tile
+constexpr int kTile = kWarps * kKeys;    // keys per tile
+constexpr int kSms = 148;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kMaxXRows = 32;  // query rows per KV head whose logits are kept for the weights
+
+struct AttendArgs {
+  Cache8AttendArgs a;
+  int row_blocks, ctas, x_cols;
+  long long x_len;   // keys per (sequence, KV head) in x
+  float *part;       // [ctas][2][rows][2 + head_dim]: max, sum, output
+  float *lse2;       // [n_seqs][n_kv_heads][group * T], log2 units
+  float *x;          // [n_seqs][n_kv_heads][x_len][x_cols], log2 units
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// ------------------------------------------------------------ the work split
+
+struct SeqInfo {
+  int len, n;   // cached rows, new tokens
+  int tiles;    // key tiles per segment (0: nothing to do, or refused)
+  bool bad;
+};
+
+__device__ __forceinline__ SeqInfo seq_info(const Cache8AttendArgs &a, int s) {
+  SeqInfo q;
+  q.len = a.lens[s];
+  q.n = a.n_new ? a.n_new[s] : a.T;
+  q.bad = q.len < 0 || q.len > a.max_len || q.n < 0 || q.n > a.T;
+  q.tiles = q.bad || q.n == 0 ? 0 : (q.len + kTile - 1) / kTile;
+  return q;
+}
+
+// Called by whole warps.  Tiles before sequence `seq` (seq = n_seqs: all).
+__device__ __forceinline__ long long tiles_before(const Cache8AttendArgs &a, int units, int seq) {
+  const int lane = threadIdx.x & 31;
+  long long sum = 0;
+  for (int s = lane; s < seq; s += 32) sum += seq_info(a, s).tiles;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return sum * units;
+}
+
+// CTAs with a run: none of theirs is empty.
+__device__ __forceinline__ int busy_ctas(long long total, int ctas) {
+  return static_cast<int>(min(total, static_cast<long long>(ctas)));
+}
+
+__device__ __forceinline__ long long run_start(long long total, int ctas, int cta) {
+  return total * cta / ctas;
+}
+
+// The CTA whose run holds tile x.
+__device__ __forceinline__ int cta_of(long long total, int ctas, long long x) {
+  int c = static_cast<int>(x * ctas / total);
+  while (c + 1 < ctas && run_start(total, ctas, c + 1) <= x) ++c;
+  return c;
+}
+
+// A position in the call's list of tiles.
+struct Cursor {
+  int seq, unit, tile;  // unit = KV head * row_blocks + row block
+  SeqInfo q;
+
+  // Called by whole warps: the position of tile x (x < total).
+  __device__ __forceinline__ void seek(const Cache8AttendArgs &a, int units, long long x) {
+    const int lane = threadIdx.x & 31;
+    long long before = 0;
+    for (int s0 = 0;; s0 += 32) {
+      const long long t =
+          s0 + lane < a.n_seqs ? static_cast<long long>(seq_info(a, s0 + lane).tiles) * units : 0;
+      long long sum = t;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += y;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, before + sum > x);
+      if (hit != 0 || s0 + 32 >= a.n_seqs) {
+        const int l = hit != 0 ? __ffs(hit) - 1 : 0;
+        seq = s0 + l;
+        x -= before + __shfl_sync(0xffffffffu, sum - t, l);
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    q = seq_info(a, seq);
+    unit = static_cast<int>(x / max(q.tiles, 1));
+    tile = static_cast<int>(x - static_cast<long long>(unit) * q.tiles);
+  }
+  // The next tile; `more`: there is one.
+  __device__ __forceinline__ void next(const Cache8AttendArgs &a, int units) {
+    if (++tile < q.tiles) return;
+    tile = 0;
+    if (++unit < units) return;
+    unit = 0;
+    do {
+      if (++seq >= a.n_seqs) return;
+      q = seq_info(a, seq);
+    } while (q.tiles == 0);
+  }
+};
+
+// Where row r of a (sequence, KV head) lives in q and out, in rows.
+__device__ __forceinline__ size_t q_row(const Cache8AttendArgs &a, int seq, int kvh, int r) {
+  const int t = r / a.group, g = r - t * a.group;
+  return (static_cast<size_t>(seq) * a.n_q_heads + kvh * a.group + g) * a.T + t;
+}
+
+__device__ __forceinline__ void store_out(__nv_bfloat16 *p, float v) { *p = __float2bfloat16(v); }
+__device__ __forceinline__ void store_out(float *p, float v) { *p = v; }
+
+// lse of a row from its max and sum (log2 units): log2 units for the weights
+// pass, natural for the caller.
+__device__ __forceinline__ void store_lse(const AttendArgs &p, int seq, int kvh, int r, float m,
+                                          float l) {
+  const Cache8AttendArgs &a = p.a;
+  const float z = l > 0.f || l != l ? m + log2f(l) : -INFINITY;
+  p.lse2[(static_cast<size_t>(seq) * a.n_kv_heads + kvh) * a.group * a.T + r] = z;
+  if (a.lse) a.lse[q_row(a, seq, kvh, r)] = z * kLn2;
+}
+
+// The end of a CTA's part of a segment: kBufs buffers of unnormalised outputs
+// (summed here; element (r, d) of a buffer at off(r, d)) and the row statistics
+// m, l.  A whole segment goes out, a part to the CTA's slot.
+template <int kRows, int kBufs, typename T, typename Off>
+__device__ __forceinline__ void write_segment(const AttendArgs &p, const float *buf, int buf_stride,
+                                              const float *m, const float *l, int seq, int unit,
+                                              int n, bool whole, int slot, Off &&off) {
+  const Cache8AttendArgs &a = p.a;
+  const int D = a.head_dim;
+  const int kvh = unit / p.row_blocks, r0 = (unit - kvh * p.row_blocks) * kRows;
+  const int rows = a.group * n;
+  float *part = p.part + (static_cast<size_t>(blockIdx.x) * 2 + slot) * (kRows * (2 + D));
+  for (int e = threadIdx.x; e < kRows * D; e += kThreads) {
+    const int r = e / D, d = e - r * D;
+    const int o = off(r, d);
+    float v = 0.f;
+#pragma unroll
+    for (int b = 0; b < kBufs; ++b) v += buf[b * buf_stride + o];
+    if (!whole) {
+      part[2 * kRows + e] = v;
+    } else if (r0 + r < rows) {
+      store_out(static_cast<T *>(a.out) + q_row(a, seq, kvh, r0 + r) * D + d,
+                l[r] > 0.f || l[r] != l[r] ? v / l[r] : 0.f);
+    }
+  }
+  if (threadIdx.x < kRows) {
+    const int r = threadIdx.x;
+    if (!whole) {
+      part[r] = m[r];
+      part[kRows + r] = l[r];
+    } else if (r0 + r < rows) {
+      store_lse(p, seq, kvh, r0 + r, m[r], l[r]);
+    }
+  }
+}
+
+// --------------------------------------------------- tensor-core kernel (bf16)
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool there) {
+  const int n = there ? 16 : 0;  // 0: the 16 bytes are filled with zeros, nothing is read
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int kPending>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+
+// The f16 B fragments of one query row n = lane / 4 for every k-step: lane
+// c = lane % 4 holds the elements of 16-byte code chunks c and c + 4, the four
+// of word w in k-step w (chunk c) or 4 + w (chunk c + 4).  Returns the row's
+// factor: f16 value * factor = q * scale * log2(e).
+template <int D>
+__device__ __forceinline__ float load_q_frags(const AttendArgs &p, int seq, int kvh, int r, int rows,
+                                              uint2 (&f)[D / 16]) {
+  const int c = threadIdx.x & 3;
+  uint4 raw[D / 64][2];
+  uint32_t amax = 0;
+#pragma unroll
+  for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      raw[h][i] = make_uint4(0, 0, 0, 0);
+      if (r < rows)
+        raw[h][i] = __ldg(reinterpret_cast<const uint4 *>(
+                              static_cast<const __nv_bfloat16 *>(p.a.q) +
+                              q_row(p.a, seq, kvh, r) * D + (c + 4 * h) * 16) + i);
+      const uint32_t w[4] = {raw[h][i].x, raw[h][i].y, raw[h][i].z, raw[h][i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t lo = (w[k] & 0x7fffu) << 16, hi = w[k] & 0x7fff0000u;
+        if (lo < 0x7f800000u) amax = max(amax, lo);
+        if (hi < 0x7f800000u) amax = max(amax, hi);
+      }
+    }
+  amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+  amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+  // largest element to [2^14, 2^15)
+  const int e = amax == 0 ? 0 : max(static_cast<int>(amax >> 23) - 127, -112);
+  const float up = pow2f(14 - e);
+#pragma unroll
+  for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t w[4] = {raw[h][i].x, raw[h][i].y, raw[h][i].z, raw[h][i].w};
+      uint32_t y[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        y[k] = as_u32(__floats2half2_rn(__uint_as_float(w[k] << 16) * up,
+                                        __uint_as_float(w[k] & 0xffff0000u) * up));
+      f[h * 4 + i * 2] = make_uint2(y[0], y[1]);
+      f[h * 4 + i * 2 + 1] = make_uint2(y[2], y[3]);
+    }
+  return pow2f(e - 14) * (p.a.scale * kLog2e);
+}
+
+template <int D, int NT>
+struct MmaCfg {
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kCtasPerSm = NT == 1 ? 2 : 1;
+  static constexpr int kStages = NT == 1 ? 3 : 4;
+  static constexpr int kStageBytes = 2 * kKeys * D + 16;  // K, V and the two scales
+  static constexpr int kRing = kWarps * kStages * kStageBytes;
+  static constexpr int kBuf = kRows * D;                  // floats per merge buffer
+  static constexpr int kQ = NT == 1 ? 0 : NT * (D / 16) * 32 * 8;
+  static constexpr int kStat = (2 * kWarps * kRows + kWarps + 3 * kRows) * 4;
+  static constexpr int kSmem = kRing + 4 * kBuf * 4 + kQ + kStat;
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, (MmaCfg<D, NT>::kCtasPerSm))
+    attend_mma_kernel(const AttendArgs p) {
+  using Cfg = MmaCfg<D, NT>;
+  constexpr int KS = D / 16;  // k-steps of the first product, m-tiles of the second
+  extern __shared__ __align__(128) uint8_t smem[];
+  float *s_buf = reinterpret_cast<float *>(smem + Cfg::kRing);
+  uint2 *s_q = reinterpret_cast<uint2 *>(s_buf + 4 * Cfg::kBuf);
+  float *s_m = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(s_q) + Cfg::kQ);
+  float *s_l = s_m + kWarps * Cfg::kRows;
+  float *s_vref = s_l + kWarps * Cfg::kRows;
+  float *s_M = s_vref + kWarps, *s_L = s_M + Cfg::kRows, *s_rs = s_L + Cfg::kRows;
+
+  const Cache8AttendArgs &a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, c = lane & 3;
+  const int units = a.n_kv_heads * p.row_blocks;
+  const long long total = tiles_before(a, units, a.n_seqs);
+  const int ctas = busy_ctas(total, p.ctas);
+  if (static_cast<int>(blockIdx.x) >= ctas) return;
+  const long long t0 = run_start(total, ctas, blockIdx.x);
+  const long long t1 = run_start(total, ctas, blockIdx.x + 1);
+
+  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) +
+                        warp * Cfg::kStages * Cfg::kStageBytes;
+  const int sub = warp * kKeys;  // this warp's keys within a tile
+
+  // one tile of this warp into a stage of its ring
+  auto issue = [&](const Cursor &k, int stage) {
+    const int j0 = k.tile * kTile + sub;
+    if (j0 < k.q.len) {
+      const uint32_t dst = ring + stage * Cfg::kStageBytes;
+      const int kvh = k.unit / p.row_blocks;
+      const size_t head = static_cast<size_t>(k.seq) * a.n_kv_heads + kvh;
+      const size_t off = (head * a.cap + j0) * D;
+      constexpr int CH = D / 16;  // 16-byte chunks per row
+#pragma unroll
+      for (int i = 0; i < kKeys * CH / 32; ++i) {
+        const int q = i * 32 + lane;
+        const int key = q / CH, ch = q % CH;
+        const bool there = j0 + key < k.q.len;
+        // swizzles: both reads below are then free of bank conflicts
+        const int kc = D == 128 ? ch ^ ((key & 1) << 2) : ch;
+        const int vc = D == 128 ? ch ^ (key & 7) : ch ^ ((key >> 1) & 3);
+        cp_async16(dst + key * D + kc * 16, a.k8 + off + q * 16, there);
+        cp_async16(dst + kKeys * D + key * D + vc * 16, a.v8 + off + q * 16, there);
+      }
+      if (lane < 2) {
+        const size_t b = head * (a.cap / a.block) + j0 / a.block;
+        cp_async4(dst + 2 * kKeys * D + lane * 4, (lane ? a.v_scale : a.k_scale) + b);
+      }
+    }
+    cp_async_commit();
+  };
+
+  Cursor load, cur;
+  cur.seek(a, units, t0);
+  load = cur;
+  long long issued = t0;
+#pragma unroll
+  for (int s = 0; s < Cfg::kStages - 1; ++s) {
+    if (issued < t1) {
+      issue(load, s);
+      load.next(a, units);
+    } else {
+      cp_async_commit();
+    }
+    ++issued;
+  }
+
+  uint2 qf[NT == 1 ? KS : 1];
+  float rs[NT][2];
+  float o[KS][NT][4];
+  float m[NT][2], l[NT][2];
+  float vref = 0.f;
+  bool fresh = true;
+  int stage = 0;
+
+  for (long long it = t0; it < t1; ++it) {
+    const int kvh = cur.unit / p.row_blocks;
+    const int r0 = (cur.unit - kvh * p.row_blocks) * Cfg::kRows;
+    if (fresh) {  // a new segment: its queries, empty statistics
+      fresh = false;
+      const int rows = a.group * cur.q.n;
+      if constexpr (NT == 1) {
+        const float f = load_q_frags<D>(p, cur.seq, kvh, r0 + g, rows, qf);
+        rs[0][0] = __shfl_sync(0xffffffffu, f, (2 * c) * 4);
+        rs[0][1] = __shfl_sync(0xffffffffu, f, (2 * c + 1) * 4);
+      } else {
+        if (warp < NT) {
+          uint2 f[KS];
+          const float r = load_q_frags<D>(p, cur.seq, kvh, r0 + warp * 8 + g, rows, f);
+#pragma unroll
+          for (int s = 0; s < KS; ++s) s_q[(warp * KS + s) * 32 + lane] = f[s];
+          if (c == 0) s_rs[warp * 8 + g] = r;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          rs[nt][0] = s_rs[nt * 8 + 2 * c];
+          rs[nt][1] = s_rs[nt * 8 + 2 * c + 1];
+        }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        m[nt][0] = m[nt][1] = -INFINITY;
+        l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+        for (int mt = 0; mt < KS; ++mt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[mt][nt][i] = 0.f;
+      }
+      vref = 0.f;
+    }
+    cp_async_wait<Cfg::kStages - 2>();
+    __syncwarp();
+    const int j0 = cur.tile * kTile + sub;
+    const int seen0 = cur.q.len - cur.q.n + 1;  // keys that token 0 sees
+    if (j0 < cur.q.len) {
+      const uint8_t *st = smem + (warp * Cfg::kStages + stage) * Cfg::kStageBytes;
+      const float ks = *reinterpret_cast<const float *>(st + 2 * kKeys * D);
+      const float vs = *reinterpret_cast<const float *>(st + 2 * kKeys * D + 4);
+      // ---- logits: rows of the tile (A) in the order that leaves lane c the
+      // probabilities of keys 4c .. 4c+3 after the transposition below
+      const int key0 = ((g >> 1) << 2) | (g & 1);  // and key0 + 2
+      float x[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.f;
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h) {
+        const int ch = D == 128 ? (c + 4 * h) ^ ((key0 & 1) << 2) : c;
+        const uint4 ka = *reinterpret_cast<const uint4 *>(st + key0 * D + ch * 16);
+        const uint4 kb = *reinterpret_cast<const uint4 *>(st + (key0 + 2) * D + ch * 16);
+        const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const uint32_t a0 = e4m3x2_to_f16x2(wa[w]), a2 = e4m3x2_to_f16x2(wa[w] >> 16);
+          const uint32_t a1 = e4m3x2_to_f16x2(wb[w]), a3 = e4m3x2_to_f16x2(wb[w] >> 16);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const uint2 b = NT == 1 ? qf[NT == 1 ? h * 4 + w : 0]
+                                    : s_q[(nt * KS + h * 4 + w) * 32 + lane];
+            mma16816(x[nt], a0, a1, a2, a3, b.x, b.y);
+          }
+        }
+      }
+      const bool masked = j0 + kKeys > seen0 + r0 / a.group;
+      bool grow = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float f0 = ks * rs[nt][0], f1 = ks * rs[nt][1];
+        x[nt][0] *= f0, x[nt][2] *= f0;
+        x[nt][1] *= f1, x[nt][3] *= f1;
+        if (masked) {
+          const int r = r0 + nt * 8 + 2 * c;
+          const int v0 = seen0 + r / a.group, v1 = seen0 + (r + 1) / a.group;
+          if (j0 + key0 >= v0) x[nt][0] = -INFINITY;
+          if (j0 + key0 >= v1) x[nt][1] = -INFINITY;
+          if (j0 + key0 + 2 >= v0) x[nt][2] = -INFINITY;
+          if (j0 + key0 + 2 >= v1) x[nt][3] = -INFINITY;
+        }
+        grow |= fmaxf(x[nt][0], x[nt][2]) > m[nt][0] + 8.f;
+        grow |= fmaxf(x[nt][1], x[nt][3]) > m[nt][1] + 8.f;
+        if (p.x_cols > 0) {
+          const int col = r0 + nt * 8 + 2 * c;
+          if (col < p.x_cols) {
+            float *xs = p.x + ((static_cast<size_t>(cur.seq) * a.n_kv_heads + kvh) * p.x_len + j0 +
+                               key0) * p.x_cols + col;
+            *reinterpret_cast<float2 *>(xs) = make_float2(x[nt][0], x[nt][1]);
+            *reinterpret_cast<float2 *>(xs + 2 * p.x_cols) = make_float2(x[nt][2], x[nt][3]);
+          }
+        }
+      }
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float t = fmaxf(x[nt][i], x[nt][i + 2]);
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+            if (t > m[nt][i]) {
+              const float f = ex2(m[nt][i] - t);
+              m[nt][i] = t;
+              l[nt][i] *= f;
+#pragma unroll
+              for (int mt = 0; mt < KS; ++mt) {
+                o[mt][nt][i] *= f;
+                o[mt][nt][i + 2] *= f;
+              }
+            }
+          }
+      }
+      if (vs > vref) {  // the outputs are held in units of the largest V scale
+        const float f = vref / vs;
+        vref = vs;
+#pragma unroll
+        for (int mt = 0; mt < KS; ++mt)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[mt][nt][i] *= f;
+      }
+      const float vr = vs / vref;
+      uint32_t b[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
+        const float m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+        const float p0 = ex2(x[nt][0] - m0), p1 = ex2(x[nt][1] - m1);
+        const float p2 = ex2(x[nt][2] - m0), p3 = ex2(x[nt][3] - m1);
+        l[nt][0] += p0 + p2;
+        l[nt][1] += p1 + p3;
+        b[nt][0] = transpose8x8(as_u32(__floats2half2_rn(p0 * vr, p1 * vr)));
+        b[nt][1] = transpose8x8(as_u32(__floats2half2_rn(p2 * vr, p3 * vr)));
+      }
+      // ---- outputs: V^T (A) by ldmatrix, 16 keys x 16 elements a matrix
+      const uint32_t vbase = ring + stage * Cfg::kStageBytes + kKeys * D;
+      const int vkey = lane & 15;
+#pragma unroll
+      for (int mt = 0; mt < KS; mt += 2) {
+        const int ch = mt + (lane >> 4);
+        const int vc = D == 128 ? ch ^ (vkey & 7) : ch ^ ((vkey >> 1) & 3);
+        uint32_t w0, w1, w2, w3;
+        asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(w0), "=r"(w1), "=r"(w2), "=r"(w3)
+                     : "r"(vbase + vkey * D + vc * 16)
+                     : "memory");
+        const uint32_t a0 = e4m3x2_to_f16x2(w0), a2 = e4m3x2_to_f16x2(w0 >> 16);
+        const uint32_t a1 = e4m3x2_to_f16x2(w1), a3 = e4m3x2_to_f16x2(w1 >> 16);
+        const uint32_t c0 = e4m3x2_to_f16x2(w2), c2 = e4m3x2_to_f16x2(w2 >> 16);
+        const uint32_t c1 = e4m3x2_to_f16x2(w3), c3 = e4m3x2_to_f16x2(w3 >> 16);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma16816(o[mt][nt], a0, a1, a2, a3, b[nt][0], b[nt][1]);
+          mma16816(o[mt + 1][nt], c0, c1, c2, c3, b[nt][0], b[nt][1]);
+        }
+      }
+    }
+    __syncwarp();  // every lane has read its stage
+    if (issued < t1) {
+      issue(load, (stage + Cfg::kStages - 1) % Cfg::kStages);
+      load.next(a, units);
+    } else {
+      cp_async_commit();
+    }
+    ++issued;
+    stage = stage + 1 == Cfg::kStages ? 0 : stage + 1;
+
+    if (cur.tile + 1 == cur.q.tiles || it + 1 == t1) {  // the segment ends here
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float t = l[nt][i];
+          t += __shfl_xor_sync(0xffffffffu, t, 4);
+          t += __shfl_xor_sync(0xffffffffu, t, 8);
+          t += __shfl_xor_sync(0xffffffffu, t, 16);
+          if (g == 0) {
+            s_m[warp * Cfg::kRows + nt * 8 + 2 * c + i] = m[nt][i];
+            s_l[warp * Cfg::kRows + nt * 8 + 2 * c + i] = t;
+          }
+        }
+      __syncthreads();
+      // this warp's factor to the CTA's reference, with its V scale
+      float f[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = nt * 8 + 2 * c + i;
+          float M = -INFINITY;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w * Cfg::kRows + r]);
+          f[nt][i] = (m[nt][i] == -INFINITY ? (l[nt][i] != l[nt][i] ? 1.f : 0.f) : ex2(m[nt][i] - M)) * vref;
+          if (warp == 0 && g == 0) {
+            float L = 0.f;
+            for (int w = 0; w < kWarps; ++w) {
+              const float mw = s_m[w * Cfg::kRows + r], lw = s_l[w * Cfg::kRows + r];
+              L += mw == -INFINITY ? lw : ex2(mw - M) * lw;
+            }
+            s_M[r] = M;
+            s_L[r] = L;
+          }
+        }
+      auto at = [&](int mt, int nt, int i) { return ((mt * NT + nt) * 4 + i) * 32 + lane; };
+      if (warp >= kWarps / 2) {
+        float *bf = s_buf + (warp - kWarps / 2) * Cfg::kBuf;
+#pragma unroll
+        for (int mt = 0; mt < KS; ++mt)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) bf[at(mt, nt, i)] = o[mt][nt][i] * f[nt][i & 1];
+      }
+      __syncthreads();
+      if (warp < kWarps / 2) {
+        float *bf = s_buf + warp * Cfg::kBuf;
+#pragma unroll
+        for (int mt = 0; mt < KS; ++mt)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) bf[at(mt, nt, i)] += o[mt][nt][i] * f[nt][i & 1];
+      }
+      __syncthreads();
+      // tiles of the segment before this one in the CTA's run
+      const bool from_start = it - cur.tile >= t0;
+      const bool to_end = cur.tile + 1 == cur.q.tiles;
+      using T = __nv_bfloat16;
+      write_segment<Cfg::kRows, 4, T>(
+          p, s_buf, Cfg::kBuf, s_M, s_L, cur.seq, cur.unit, cur.q.n, from_start && to_end,
+          from_start ? 1 : 0, [](int r, int d) {
+            return (((d >> 4) * NT + (r >> 3)) * 4 + ((d >> 3) & 1) * 2 + (r & 1)) * 32 +
+                   (d & 7) * 4 + ((r & 7) >> 1);
+          });
+      __syncthreads();
+      fresh = true;
+    }
+    cur.next(a, units);
+  }
+}
+
+// ------------------------------------------------------ CUDA-core kernel (f32)
+
+__device__ __forceinline__ float load_q(const float *p) { return __ldg(p); }
+__device__ __forceinline__ float load_q(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
+
+// the four values of a word of codes
+__device__ __forceinline__ void values4(uint32_t w, float (&v)[4]) {
+  const float2 lo = __half22float2(as_half2(e4m3x2_to_f16x2(w)));
+  const float2 hi = __half22float2(as_half2(e4m3x2_to_f16x2(w >> 16)));
+  v[0] = lo.x, v[1] = lo.y, v[2] = hi.x, v[3] = hi.y;
+}
+
+constexpr int kSimtRows = 8;
+constexpr int kMaxD = 128;
+
+// The logits of 8 query rows (in shared memory, [8][D]) for one key: two lanes
+// a key, each half of the elements; both lanes get the sums.
+__device__ __forceinline__ void simt_logits(const uint8_t *key_row, int D, int half,
+                                            const float *s_q, float (&x)[kSimtRows]) {
+#pragma unroll
+  for (int r = 0; r < kSimtRows; ++r) x[r] = 0.f;
+  const int n = D / 8;  // words per half
+  for (int w = 0; w < n; ++w) {
+    float v[4];
+    values4(__ldg(reinterpret_cast<const uint32_t *>(key_row) + half * n + w), v);
+    const float *q = s_q + (half * n + w) * 4;
+#pragma unroll
+    for (int r = 0; r < kSimtRows; ++r) {
+      const float4 y = *reinterpret_cast<const float4 *>(q + r * D);
+      x[r] = fmaf(v[0], y.x, fmaf(v[1], y.y, fmaf(v[2], y.z, fmaf(v[3], y.w, x[r]))));
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < kSimtRows; ++r) x[r] += __shfl_xor_sync(0xffffffffu, x[r], 1);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) attend_simt_kernel(const AttendArgs p) {
+  __shared__ __align__(16) float s_q[kSimtRows * kMaxD];
+  __shared__ __align__(16) float s_buf[kWarps * kSimtRows * kMaxD];
+  __shared__ float s_p[kWarps][kKeys][kSimtRows];
+  __shared__ float s_m[kWarps][kSimtRows], s_l[kWarps][kSimtRows];
+  __shared__ float s_M[kSimtRows], s_L[kSimtRows];
+  const Cache8AttendArgs &a = p.a;
+  const int D = a.head_dim;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int units = a.n_kv_heads * p.row_blocks;
+  const long long total = tiles_before(a, units, a.n_seqs);
+  const int ctas = busy_ctas(total, p.ctas);
+  if (static_cast<int>(blockIdx.x) >= ctas) return;
+  const long long t0 = run_start(total, ctas, blockIdx.x);
+  const long long t1 = run_start(total, ctas, blockIdx.x + 1);
+  Cursor cur;
+  cur.seek(a, units, t0);
+  float o[kSimtRows][4], m[kSimtRows], l[kSimtRows];
+  bool fresh = true;
+  for (long long it = t0; it < t1; ++it) {
+    const int kvh = cur.unit / p.row_blocks;
+    const int r0 = (cur.unit - kvh * p.row_blocks) * kSimtRows;
+    const size_t head = static_cast<size_t>(cur.seq) * a.n_kv_heads + kvh;
+    if (fresh) {
+      fresh = false;
+      for (int e = threadIdx.x; e < kSimtRows * D; e += kThreads) {
+        const int r = r0 + e / D;
+        s_q[e] = r < a.group * cur.q.n
+                     ? load_q(static_cast<const T *>(a.q) + q_row(a, cur.seq, kvh, r) * D + e % D)
+                     : 0.f;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int r = 0; r < kSimtRows; ++r) {
+        m[r] = -INFINITY;
+        l[r] = 0.f;
+        o[r][0] = o[r][1] = o[r][2] = o[r][3] = 0.f;
+      }
+    }
+    const int j0 = cur.tile * kTile + warp * kKeys;
+    const int seen0 = cur.q.len - cur.q.n + 1;
+    if (j0 < cur.q.len) {
+      const int j = min(j0 + (lane >> 1), cur.q.len - 1);  // rows past the end are not read
+      const size_t blk = head * (a.cap / a.block) + j0 / a.block;
+      const float f = __ldg(a.k_scale + blk) * a.scale * kLog2e, vs = __ldg(a.v_scale + blk);
+      float x[kSimtRows];
+      simt_logits(a.k8 + (head * a.cap + j) * D, D, lane & 1, s_q, x);
+#pragma unroll
+      for (int r = 0; r < kSimtRows; ++r) {
+        x[r] = j0 + (lane >> 1) < seen0 + (r0 + r) / a.group && j0 + (lane >> 1) < cur.q.len
+                   ? x[r] * f
+                   : -INFINITY;
+        if (p.x_cols > r0 + r && (lane & 1) == 0 && j0 + (lane >> 1) < cur.q.len)
+          p.x[(head * p.x_len + j) * p.x_cols + r0 + r] = x[r];
+        float t = x[r];
+#pragma unroll
+        for (int s = 2; s < 32; s <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, s));
+        if (t > m[r]) {
+          const float g = exp2f(m[r] - t);
+          m[r] = t;
+          l[r] *= g;
+          o[r][0] *= g, o[r][1] *= g, o[r][2] *= g, o[r][3] *= g;
+        }
+        const float e = exp2f(x[r] - (m[r] == -INFINITY ? 0.f : m[r]));
+        if ((lane & 1) == 0) {
+          s_p[warp][lane >> 1][r] = e * vs;
+          l[r] += e;
+        }
+      }
+      __syncwarp();
+      if (lane * 4 < D) {
+        const int keys = min(kKeys, cur.q.len - j0);
+        for (int k = 0; k < keys; ++k) {
+          float v[4];
+          values4(__ldg(reinterpret_cast<const uint32_t *>(a.v8 + (head * a.cap + j0 + k) * D) + lane), v);
+#pragma unroll
+          for (int r = 0; r < kSimtRows; ++r) {
+            const float e = s_p[warp][k][r];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[r][i] = fmaf(e, v[i], o[r][i]);
+          }
+        }
+      }
+      __syncwarp();
+    }
+    if (cur.tile + 1 == cur.q.tiles || it + 1 == t1) {
+#pragma unroll
+      for (int r = 0; r < kSimtRows; ++r) {
+        float t = l[r];
+#pragma unroll
+        for (int s = 1; s < 32; s <<= 1) t += __shfl_xor_sync(0xffffffffu, t, s);
+        if (lane == 0) {
+          s_m[warp][r] = m[r];
+          s_l[warp][r] = t;
+        }
+        l[r] = t;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int r = 0; r < kSimtRows; ++r) {
+        float M = -INFINITY, L = 0.f;
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][r]);
+        const float f = m[r] == -INFINITY ? (l[r] != l[r] ? 1.f : 0.f) : exp2f(m[r] - M);
+        if (lane * 4 < D)
+          *reinterpret_cast<float4 *>(s_buf + (warp * kSimtRows + r) * D + lane * 4) =
+              make_float4(o[r][0] * f, o[r][1] * f, o[r][2] * f, o[r][3] * f);
+        if (threadIdx.x == 0) {
+          for (int w = 0; w < kWarps; ++w)
+            L += s_m[w][r] == -INFINITY ? s_l[w][r] : exp2f(s_m[w][r] - M) * s_l[w][r];
+          s_M[r] = M;
+          s_L[r] = L;
+        }
+      }
+      __syncthreads();
+      const bool from_start = it - cur.tile >= t0;
+      const bool to_end = cur.tile + 1 == cur.q.tiles;
+      write_segment<kSimtRows, kWarps, T>(p, s_buf, kSimtRows * D, s_M, s_L, cur.seq, cur.unit,
+                                          cur.q.n, from_start && to_end, from_start ? 1 : 0,
+                                          [D](int r, int d) { return r * D + d; });
+      __syncthreads();
+      fresh = true;
+    }
+    cur.next(a, units);
+  }
+}
+
+// ------------------------------------------------------------------- the join
+
+// One CTA per (sequence, KV head, row block) row: joins the parts of a segment
+// that several CTAs computed, and writes the empty rows of sequences without
+// cached keys.  Each warp takes every eighth part, in order; the warps' sums
+// are added in order, so results do not depend on timing.
+template <int kRows, typename T>
+__global__ void __launch_bounds__(kThreads) attend_finish_kernel(const AttendArgs p) {
+  __shared__ float s_o[kWarps][kMaxD];
+  __shared__ float s_red[2][kWarps];
+  const Cache8AttendArgs &a = p.a;
+  const int D = a.head_dim;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int units = a.n_kv_heads * p.row_blocks;
+  const int row = blockIdx.x % kRows;
+  const int u = blockIdx.x / kRows;
+  const int seq = u / units, unit = u - seq * units;
+  const int kvh = unit / p.row_blocks;
+  const int r = (unit - kvh * p.row_blocks) * kRows + row;
+  const SeqInfo q = seq_info(a, seq);
+  if (q.bad) {
+    if (threadIdx.x == 0) record_device_status(BKV_DEV_ASSERT, 611);
+    return;
+  }
+  if (r >= a.group * q.n) return;
+  T *out = static_cast<T *>(a.out) + q_row(a, seq, kvh, r) * D;
+  if (q.tiles == 0) {
+    if (threadIdx.x < D) store_out(out + threadIdx.x, 0.f);
+    if (threadIdx.x == 0) store_lse(p, seq, kvh, r, -INFINITY, 0.f);
+    return;
+  }
+  const long long total = tiles_before(a, units, a.n_seqs);
+  const long long b = tiles_before(a, units, seq) + static_cast<long long>(unit) * q.tiles;
+  const int ctas = busy_ctas(total, p.ctas);
+  const int c0 = cta_of(total, ctas, b), c1 = cta_of(total, ctas, b + q.tiles - 1);
+  if (c0 == c1) return;  // written by its CTA
+  const int parts = c1 - c0 + 1;
+  const int stride = kRows * (2 + D);
+  // part i: CTA c0 + i; slot 1 of the CTA the segment starts in, slot 0 after it
+  auto part = [&](int i) {
+    return p.part + (static_cast<size_t>(c0 + i) * 2 + (i == 0 ? 1 : 0)) * stride;
+  };
+  float M = -INFINITY;
+  for (int i = threadIdx.x; i < parts; i += kThreads) M = fmaxf(M, part(i)[row]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  if (lane == 0) s_red[0][warp] = M;
+  __syncthreads();
+  M = s_red[0][0];
+#pragma unroll
+  for (int w = 1; w < kWarps; ++w) M = fmaxf(M, s_red[0][w]);
+  float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int i = warp; i < parts; i += kWarps) {
+    const float *s = part(i);
+    const float mi = s[row], li = s[kRows + row];
+    const float f = mi == -INFINITY ? 0.f : exp2f(mi - M);
+    l += mi == -INFINITY ? li : f * li;
+    if (lane * 4 < D) {
+      const float4 v = *reinterpret_cast<const float4 *>(s + 2 * kRows + row * D + lane * 4);
+      if (f > 0.f || mi != mi) {
+        o[0] = fmaf(f, v.x, o[0]), o[1] = fmaf(f, v.y, o[1]);
+        o[2] = fmaf(f, v.z, o[2]), o[3] = fmaf(f, v.w, o[3]);
+      } else if (li != li) {
+        o[0] = o[1] = o[2] = o[3] = li;  // NaN logits
+      }
+    }
+  }
+  if (lane * 4 < D)
+    *reinterpret_cast<float4 *>(&s_o[warp][lane * 4]) = make_float4(o[0], o[1], o[2], o[3]);
+  if (lane == 0) s_red[1][warp] = l;
+  __syncthreads();
+  float L = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) L += s_red[1][w];
+  if (threadIdx.x < D) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) v += s_o[w][threadIdx.x];
+    store_out(out + threadIdx.x, L > 0.f || L != L ? v / L : 0.f);
+  }
+  if (threadIdx.x == 0) store_lse(p, seq, kvh, r, M, L);
+}
+
+// ---------------------------------------------------------------- the weights
+
+__device__ __forceinline__ void store_weight(const Cache8AttendArgs &a, size_t head, int j,
+                                             const SeqInfo &q, float sum) {
+  // the new tokens' own rows start at zero
+  if (a.w_in && j < q.len - q.n) sum = fmaf(a.decay, a.w_in[head * a.cap + j], sum);
+  a.w_out[head * a.cap + j] = sum;
+}
+
+// From the logits the attention kernel kept.  One thread per key.
+__global__ void __launch_bounds__(kThreads) weights_kept_kernel(const AttendArgs p) {
+  __shared__ float s_z[kMaxXRows];
+  const Cache8AttendArgs &a = p.a;
+  const size_t head = blockIdx.y;
+  const int seq = static_cast<int>(head) / a.n_kv_heads;
+  const SeqInfo q = seq_info(a, seq);
+  const int j = blockIdx.x * kThreads + threadIdx.x;
+  if (q.tiles == 0 || static_cast<int>(blockIdx.x) * kThreads >= q.len) return;
+  const int rows = a.group * q.n;
+  if (threadIdx.x < rows) s_z[threadIdx.x] = p.lse2[head * a.group * a.T + threadIdx.x];
+  __syncthreads();
+  if (j >= q.len) return;
+  const float *x = p.x + (head * p.x_len + j) * p.x_cols;
+  float sum = 0.f;
+  for (int r = 0; r < rows; ++r)
+    if (s_z[r] != -INFINITY) sum += ex2(x[r] - s_z[r]);
+  store_weight(a, head, j, q, sum);
+}
+
+// From the keys again, for more query rows than logits are kept of.  A CTA
+// holds 128 keys' fragments and walks the query rows 32 at a time.
+template <int D>
+__global__ void __launch_bounds__(kThreads) weights_mma_kernel(const AttendArgs p) {
+  constexpr int KS = D / 16, NT = 4;
+  __shared__ uint2 s_q[NT * KS * 32];
+  __shared__ float s_rs[NT * 8], s_z[NT * 8];
+  const Cache8AttendArgs &a = p.a;
+  const size_t head = blockIdx.y;
+  const int seq = static_cast<int>(head) / a.n_kv_heads;
+  const int kvh = static_cast<int>(head) - seq * a.n_kv_heads;
+  const SeqInfo q = seq_info(a, seq);
+  if (q.tiles == 0 || static_cast<int>(blockIdx.x) * kTile >= q.len) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const int j0 = blockIdx.x * kTile + warp * kKeys;
+  const int rows = a.group * q.n;
+  const int seen0 = q.len - q.n + 1;
+  uint32_t ka[KS][4];
+  float ks = 0.f;
+  if (j0 < q.len) {
+    ks = __ldg(a.k_scale + head * (a.cap / a.block) + j0 / a.block);
+#pragma unroll
+    for (int h = 0; h < D / 64; ++h) {
+      // rows past the end are not read
+      const uint8_t *r0 = a.k8 + (head * a.cap + min(j0 + g, q.len - 1)) * D + (c + 4 * h) * 16;
+      const uint8_t *r1 = a.k8 + (head * a.cap + min(j0 + g + 8, q.len - 1)) * D + (c + 4 * h) * 16;
+      const uint4 x = __ldg(reinterpret_cast<const uint4 *>(r0));
+      const uint4 y = __ldg(reinterpret_cast<const uint4 *>(r1));
+      const uint32_t wx[4] = {x.x, x.y, x.z, x.w}, wy[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        ka[h * 4 + w][0] = e4m3x2_to_f16x2(wx[w]);
+        ka[h * 4 + w][1] = e4m3x2_to_f16x2(wy[w]);
+        ka[h * 4 + w][2] = e4m3x2_to_f16x2(wx[w] >> 16);
+        ka[h * 4 + w][3] = e4m3x2_to_f16x2(wy[w] >> 16);
+      }
+    }
+  }
+  float sum0 = 0.f, sum1 = 0.f;
+  for (int rb = 0; rb < rows; rb += NT * 8) {
+    // the last token of these rows sees fewer keys than this tile's first: none does
+    const int t_last = min(rb + NT * 8, rows) - 1;
+    if (static_cast<int>(blockIdx.x) * kTile >= seen0 + t_last / a.group) continue;
+    __syncthreads();
+    if (warp < NT) {
+      uint2 f[KS];
+      const float s = load_q_frags<D>(p, seq, kvh, rb + warp * 8 + g, rows, f);
+#pragma unroll
+      for (int k = 0; k < KS; ++k) s_q[(warp * KS + k) * 32 + lane] = f[k];
+      if (c == 0) {
+        const int r = rb + warp * 8 + g;
+        s_rs[warp * 8 + g] = s;
+        const float z = r < rows ? p.lse2[head * a.group * a.T + r] : INFINITY;
+        s_z[warp * 8 + g] = z == -INFINITY ? INFINITY : z;  // rows that see nothing add nothing
+      }
+    }
+    __syncthreads();
+    if (j0 >= q.len) continue;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        const uint2 b = s_q[(nt * KS + k) * 32 + lane];
+        mma16816(x, ka[k][0], ka[k][1], ka[k][2], ka[k][3], b.x, b.y);
+      }
+      const int r = nt * 8 + 2 * c;
+      const int v0 = seen0 + (rb + r) / a.group, v1 = seen0 + (rb + r + 1) / a.group;
+      const float f0 = ks * s_rs[r], f1 = ks * s_rs[r + 1], z0 = s_z[r], z1 = s_z[r + 1];
+      if (j0 + g < v0) sum0 += ex2(x[0] * f0 - z0);
+      if (j0 + g < v1) sum0 += ex2(x[1] * f1 - z1);
+      if (j0 + g + 8 < v0) sum1 += ex2(x[2] * f0 - z0);
+      if (j0 + g + 8 < v1) sum1 += ex2(x[3] * f1 - z1);
+    }
+  }
+  sum0 += __shfl_xor_sync(0xffffffffu, sum0, 1);
+  sum0 += __shfl_xor_sync(0xffffffffu, sum0, 2);
+  sum1 += __shfl_xor_sync(0xffffffffu, sum1, 1);
+  sum1 += __shfl_xor_sync(0xffffffffu, sum1, 2);
+  if (c == 0) {
+    if (j0 + g < q.len) store_weight(a, head, j0 + g, q, sum0);
+    if (j0 + g + 8 < q.len) store_weight(a, head, j0 + g + 8, q, sum1);
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) weights_simt_kernel(const AttendArgs p) {
+  __shared__ __align__(16) float s_q[kSimtRows * kMaxD];
+  const Cache8AttendArgs &a = p.a;
+  const int D = a.head_dim;
+  const size_t head = blockIdx.y;
+  const int seq = static_cast<int>(head) / a.n_kv_heads;
+  const int kvh = static_cast<int>(head) - seq * a.n_kv_heads;
+  const SeqInfo q = seq_info(a, seq);
+  if (q.tiles == 0 || static_cast<int>(blockIdx.x) * kTile >= q.len) return;
+  const int j = blockIdx.x * kTile + (threadIdx.x >> 1);
+  const int jr = min(j, q.len - 1);
+  const int rows = a.group * q.n;
+  const float f = __ldg(a.k_scale + head * (a.cap / a.block) + jr / a.block) * a.scale * kLog2e;
+  float sum = 0.f;
+  for (int rb = 0; rb < rows; rb += kSimtRows) {
+    __syncthreads();
+    for (int e = threadIdx.x; e < kSimtRows * D; e += kThreads) {
+      const int r = rb + e / D;
+      s_q[e] = r < rows ? load_q(static_cast<const T *>(a.q) + q_row(a, seq, kvh, r) * D + e % D) : 0.f;
+    }
+    __syncthreads();
+    float x[kSimtRows];
+    simt_logits(a.k8 + (head * a.cap + jr) * D, D, threadIdx.x & 1, s_q, x);
+#pragma unroll
+    for (int r = 0; r < kSimtRows; ++r) {
+      if (rb + r >= rows || j >= q.len - q.n + 1 + (rb + r) / a.group) continue;
+      const float z = p.lse2[head * a.group * a.T + rb + r];
+      if (z != -INFINITY) sum += exp2f(x[r] * f - z);
+    }
+  }
+  if (j < q.len && (threadIdx.x & 1) == 0) store_weight(a, head, j, q, sum);
+}
+
+// ------------------------------------------------------------------ launching
+
+template <int D, int NT>
+bool run_mma(const AttendArgs &p, cudaStream_t s) {
+  static int done[64];
+  using Cfg = MmaCfg<D, NT>;
+  static_assert(Cfg::kSmem <= 227 * 1024, "shared memory");
+  if (!ensure_smem_limit(attend_mma_kernel<D, NT>, Cfg::kSmem, done)) return false;
+  attend_mma_kernel<D, NT><<<p.ctas, kThreads, Cfg::kSmem, s>>>(p);
+  return cudaGetLastError() == cudaSuccess;
+}
+
+template <int kRows, typename T>
+bool run_finish(const AttendArgs &p, cudaStream_t s) {
+  const unsigned grid = static_cast<unsigned>(p.a.n_seqs) * p.a.n_kv_heads * p.row_blocks * kRows;
+  attend_finish_kernel<kRows, T><<<grid, kThreads, 0, s>>>(p);
+  return cudaGetLastError() == cudaSuccess;
+}
+
+bool use_mma(int dtype, int head_dim) {
+  return dtype == BKV_BF16 && (head_dim == 64 || head_dim == 128);
+}
+
+}  // namespace
+
+Cache8AttendPlan plan_cache8_attend(int n_seqs, int n_q_heads, int n_kv_heads, int head_dim,
+                                    int dtype, long long max_len, int T, bool weights) {
+  Cache8AttendPlan p{};
+  const long long rows = static_cast<long long>(n_q_heads / n_kv_heads) * T;
+  const bool mma = use_mma(dtype, head_dim);
+  p.nt = !mma || rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+  p.row_blocks = static_cast<int>((rows + 8 * p.nt - 1) / (8 * p.nt));
+  const long long tiles = (max_len + kTile - 1) / kTile * n_seqs * n_kv_heads * p.row_blocks;
+  const int resident = mma ? kSms * (p.nt == 1 ? 2 : 1) : kSms * 2;
+  p.ctas = static_cast<int>(std::min<long long>(tiles, resident));
+  p.x_cols = weights && rows <= kMaxXRows ? static_cast<int>((rows + 1) / 2 * 2) : 0;
+  const size_t part = static_cast<size_t>(p.ctas) * 2 * 8 * p.nt * (2 + head_dim) * 4;
+  const size_t lse = static_cast<size_t>(n_seqs) * n_q_heads * T * 4;
+  const size_t x = static_cast<size_t>(n_seqs) * n_kv_heads * align_up(max_len, kKeys) * p.x_cols * 4;
+  p.part_off = 0;
+  p.lse_off = align_up(part, kAlign);
+  p.x_off = p.lse_off + align_up(lse, kAlign);
+  p.bytes = p.x_off + align_up(x, kAlign);
+  return p;
+}
+
+bkv_status launch_cache8_attend(const Cache8AttendArgs &a, const Cache8AttendPlan &plan, int dtype,
+                                void *ws, cudaStream_t stream) {
+  if (injected_launch_failure()) return BKV_ERR_CUDA;
+  AttendArgs p;
+  p.a = a;
+  p.row_blocks = plan.row_blocks;
+  p.ctas = plan.ctas;
+  p.x_cols = plan.x_cols;
+  p.x_len = static_cast<long long>(align_up(a.max_len, kKeys));
+  uint8_t *w = static_cast<uint8_t *>(ws);
+  p.part = reinterpret_cast<float *>(w + plan.part_off);
+  p.lse2 = reinterpret_cast<float *>(w + plan.lse_off);
+  p.x = reinterpret_cast<float *>(w + plan.x_off);
+  const bool mma = use_mma(dtype, a.head_dim);
+  bool ok;
+  if (mma) {
+    const bool wide = a.head_dim == 128;
+    if (plan.nt == 1)
+      ok = (wide ? run_mma<128, 1>(p, stream) : run_mma<64, 1>(p, stream)) &&
+           run_finish<8, __nv_bfloat16>(p, stream);
+    else if (plan.nt == 2)
+      ok = (wide ? run_mma<128, 2>(p, stream) : run_mma<64, 2>(p, stream)) &&
+           run_finish<16, __nv_bfloat16>(p, stream);
+    else
+      ok = (wide ? run_mma<128, 4>(p, stream) : run_mma<64, 4>(p, stream)) &&
+           run_finish<32, __nv_bfloat16>(p, stream);
+  } else if (dtype == BKV_BF16) {
+    attend_simt_kernel<__nv_bfloat16><<<p.ctas, kThreads, 0, stream>>>(p);
+    ok = cudaGetLastError() == cudaSuccess && run_finish<kSimtRows, __nv_bfloat16>(p, stream);
+  } else {
+    attend_simt_kernel<float><<<p.ctas, kThreads, 0, stream>>>(p);
+    ok = cudaGetLastError() == cudaSuccess && run_finish<kSimtRows, float>(p, stream);
+  }
+  if (!ok) return BKV_ERR_CUDA;
+  if (a.w_out) {
+    const unsigned heads = static_cast<unsigned>(a.n_seqs) * a.n_kv_heads;
+    const unsigned tiles = static_cast<unsigned>((a.max_len + kTile - 1) / kTile);
+    if (plan.x_cols > 0)
+      weights_kept_kernel<<<dim3((a.max_len + kThreads - 1) / kThreads, heads), kThreads, 0, stream>>>(p);
+    else if (mma && a.head_dim == 128)
+      weights_mma_kernel<128><<<dim3(tiles, heads), kThreads, 0, stream>>>(p);
+    else if (mma)
+      weights_mma_kernel<64><<<dim3(tiles, heads), kThreads, 0, stream>>>(p);
+    else if (dtype == BKV_BF16)
+      weights_simt_kernel<__nv_bfloat16><<<dim3(tiles, heads), kThreads, 0, stream>>>(p);
+    else
+      weights_simt_kernel<float><<<dim3(tiles, heads), kThreads, 0, stream>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return BKV_ERR_CUDA;
+  }
+  return BKV_OK;
+}
+
+}  // namespace bkv
