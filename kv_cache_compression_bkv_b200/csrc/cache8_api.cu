@@ -75,11 +75,14 @@ bkv_status check_cache(const bkv_cache8_desc *d, const void *k8, const void *v8,
   return st;
 }
 
-// Rows of queries per KV head, and rows the call writes, within 32 bits.
-bool rows_fit(const bkv_cache8_desc *d, int32_t T) {
+// Rows of queries per KV head, rows the call writes, and its key tiles (of 128
+// keys and 8 rows at the least), within 32 bits.
+bool rows_fit(const bkv_cache8_desc *d, int32_t T, int64_t max_len) {
   if (T < 1) return false;
   const long long rows = static_cast<long long>(d->n_q_heads / d->n_kv_heads) * T;
-  return rows <= (1 << 24) && (rows + 32) <= kMaxRows / static_cast<long long>(heads_of(d));
+  const long long heads = static_cast<long long>(heads_of(d));
+  return rows <= (1 << 24) && (rows + 32) <= kMaxRows / heads &&
+         (rows + 7) / 8 * heads <= (kMaxRows >> 1) / ((max_len + 127) / 128 + 2);
 }
 
 size_t evict_workspace(const bkv_cache8_desc *d, long long K) {
@@ -97,7 +100,7 @@ extern "C" {
 size_t bkv_cache8_workspace_size(const bkv_cache8_desc *desc, int64_t max_len, int32_t T, int64_t K,
                                  int32_t weights) {
   if (check_desc8(desc) != BKV_OK || max_len < 1 || max_len > desc->capacity || T < 0 || K < 0 ||
-      K > kMaxRows || (T > 0 && !rows_fit(desc, T)))
+      K > kMaxRows || (T > 0 && !rows_fit(desc, T, max_len)))
     return 0;
   size_t n = 0;
   if (T > 0)
@@ -148,7 +151,7 @@ bkv_status bkv_cache8_attend(const bkv_cache8_desc *desc, const void *k8, const 
                              size_t workspace_bytes, void *stream) {
   const bkv_status st = check_cache(desc, k8, v8, k_scale, v_scale, lens);
   if (st == BKV_ERR_INVALID_ARG) return st;
-  if (!q || !out || max_len < 1 || max_len > desc->capacity || !rows_fit(desc, T))
+  if (!q || !out || max_len < 1 || max_len > desc->capacity || !rows_fit(desc, T, max_len))
     return BKV_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(n_new, 4) || !aligned(lse, 4) ||
       !aligned(weights_in, 4) || !aligned(weights_out, 4))

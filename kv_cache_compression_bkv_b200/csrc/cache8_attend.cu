@@ -47,18 +47,22 @@ namespace {
 
 using namespace cache8;
 
-constexpr int kWarps = 8;
+constexpr int kTile = 128;               // keys per tile
+constexpr int kWarps = 4;                // the tensor-core kernel's
 constexpr int kThreads = kWarps * 32;
-constexpr int kKeys = 16;                // keys per warp and tile
-constexpr int kTile = kWarps * kKeys;    // keys per tile
+constexpr int kKeys = 32;                // keys per warp and tile
+constexpr int kSimtWarps = 8;            // the other kernels'
+constexpr int kSimtThreads = kSimtWarps * 32;
+constexpr int kSimtKeys = 16;
 constexpr int kSms = 148;
+constexpr int kPad = 2;                  // what a segment costs beside its tiles, in tiles
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kMaxXRows = 32;  // query rows per KV head whose logits are kept for the weights
 
 struct AttendArgs {
   Cache8AttendArgs a;
-  int row_blocks, ctas, x_cols;
+  int row_blocks, ctas, x_cols, log2_block, join_rows;
   long long x_len;   // keys per (sequence, KV head) in x
   float *part;       // [ctas][2][rows][2 + head_dim]: max, sum, output
   float *lse2;       // [n_seqs][n_kv_heads][group * T], log2 units
@@ -70,6 +74,13 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+
+// Programmatic dependent launch: the next kernel of the stream may start, and
+// the wait, in that kernel, for everything before it.
+__device__ __forceinline__ void pdl_launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // ------------------------------------------------------------ the work split
 
@@ -88,48 +99,61 @@ __device__ __forceinline__ SeqInfo seq_info(const Cache8AttendArgs &a, int s) {
   return q;
 }
 
-// Called by whole warps.  Tiles before sequence `seq` (seq = n_seqs: all).
-__device__ __forceinline__ long long tiles_before(const Cache8AttendArgs &a, int units, int seq) {
-  const int lane = threadIdx.x & 31;
-  long long sum = 0;
-  for (int s = lane; s < seq; s += 32) sum += seq_info(a, s).tiles;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  return sum * units;
-}
+// The whole call's list of tiles and its cut into runs.  A segment counts as
+// `pad` tiles more than it has, put before its first: what a CTA spends on
+// beginning and ending one (queries, the merge of its warps), so that runs
+// over many short sequences take no longer than the others.
+struct Split {
+  int total, run, pad;  // counted tiles, counted tiles per run
+};
 
-// CTAs with a run: none of theirs is empty.
-__device__ __forceinline__ int busy_ctas(long long total, int ctas) {
-  return static_cast<int>(min(total, static_cast<long long>(ctas)));
+// Called by whole warps.
+__device__ __forceinline__ int warp_sum(int x) {
+  return static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(x)));
 }
-
-__device__ __forceinline__ long long run_start(long long total, int ctas, int cta) {
-  return total * cta / ctas;
+__device__ __forceinline__ Split split_of(const Cache8AttendArgs &a, int units, int ctas) {
+  int tiles = 0, segments = 0;
+  for (int s = threadIdx.x & 31; s < a.n_seqs; s += 32) {
+    const int t = seq_info(a, s).tiles;
+    tiles += t;
+    segments += t > 0 ? 1 : 0;
+  }
+  tiles = warp_sum(tiles) * units;
+  segments = warp_sum(segments) * units;
+  Split w;
+  w.pad = tiles >= 16 * ctas ? kPad : 0;
+  w.total = tiles + w.pad * segments;
+  w.run = max((w.total + ctas - 1) / ctas, 1);
+  return w;
 }
-
-// The CTA whose run holds tile x.
-__device__ __forceinline__ int cta_of(long long total, int ctas, long long x) {
-  int c = static_cast<int>(x * ctas / total);
-  while (c + 1 < ctas && run_start(total, ctas, c + 1) <= x) ++c;
-  return c;
+// Counted tiles before sequence `seq`.
+__device__ __forceinline__ int counted_before(const Cache8AttendArgs &a, const Split &w, int units,
+                                              int seq) {
+  int sum = 0;
+  for (int s = threadIdx.x & 31; s < seq; s += 32) {
+    const int t = seq_info(a, s).tiles;
+    sum += t > 0 ? t + w.pad : 0;
+  }
+  return warp_sum(sum) * units;
 }
 
 // A position in the call's list of tiles.
 struct Cursor {
   int seq, unit, tile;  // unit = KV head * row_blocks + row block
+  int at;               // counted tiles from the run's start to this tile
   SeqInfo q;
 
-  // Called by whole warps: the position of tile x (x < total).
-  __device__ __forceinline__ void seek(const Cache8AttendArgs &a, int units, long long x) {
+  // Called by whole warps: the first tile at counted tile x (x < total) or after it.
+  __device__ __forceinline__ void seek(const Cache8AttendArgs &a, const Split &w, int units, int x) {
     const int lane = threadIdx.x & 31;
-    long long before = 0;
+    int before = 0;
     for (int s0 = 0;; s0 += 32) {
-      const long long t =
-          s0 + lane < a.n_seqs ? static_cast<long long>(seq_info(a, s0 + lane).tiles) * units : 0;
-      long long sum = t;
+      int t = s0 + lane < a.n_seqs ? seq_info(a, s0 + lane).tiles : 0;
+      t = t > 0 ? (t + w.pad) * units : 0;
+      int sum = t;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, sum, o);
+        const int y = __shfl_up_sync(0xffffffffu, sum, o);
         if (lane >= o) sum += y;
       }
       const unsigned hit = __ballot_sync(0xffffffffu, before + sum > x);
@@ -142,17 +166,23 @@ struct Cursor {
       before += __shfl_sync(0xffffffffu, sum, 31);
     }
     q = seq_info(a, seq);
-    unit = static_cast<int>(x / max(q.tiles, 1));
-    tile = static_cast<int>(x - static_cast<long long>(unit) * q.tiles);
+    unit = x / (q.tiles + w.pad);
+    const int pos = x - unit * (q.tiles + w.pad) - w.pad;
+    tile = max(pos, 0);
+    at = max(-pos, 0);
   }
-  // The next tile; `more`: there is one.
-  __device__ __forceinline__ void next(const Cache8AttendArgs &a, int units) {
+  __device__ __forceinline__ void next(const Cache8AttendArgs &a, const Split &w, int units) {
+    ++at;
     if (++tile < q.tiles) return;
+    at += w.pad;
     tile = 0;
     if (++unit < units) return;
     unit = 0;
     do {
-      if (++seq >= a.n_seqs) return;
+      if (++seq >= a.n_seqs) {
+        at = INT32_MAX;  // past the end
+        return;
+      }
       q = seq_info(a, seq);
     } while (q.tiles == 0);
   }
@@ -166,6 +196,14 @@ __device__ __forceinline__ size_t q_row(const Cache8AttendArgs &a, int seq, int 
 
 __device__ __forceinline__ void store_out(__nv_bfloat16 *p, float v) { *p = __float2bfloat16(v); }
 __device__ __forceinline__ void store_out(float *p, float v) { *p = v; }
+__device__ __forceinline__ void store_out4(__nv_bfloat16 *p, float a, float b, float c, float d) {
+  __nv_bfloat162 x = __floats2bfloat162_rn(a, b), y = __floats2bfloat162_rn(c, d);
+  *reinterpret_cast<uint2 *>(p) =
+      make_uint2(*reinterpret_cast<uint32_t *>(&x), *reinterpret_cast<uint32_t *>(&y));
+}
+__device__ __forceinline__ void store_out4(float *p, float a, float b, float c, float d) {
+  *reinterpret_cast<float4 *>(p) = make_float4(a, b, c, d);
+}
 
 // lse of a row from its max and sum (log2 units): log2 units for the weights
 // pass, natural for the caller.
@@ -180,7 +218,7 @@ __device__ __forceinline__ void store_lse(const AttendArgs &p, int seq, int kvh,
 // The end of a CTA's part of a segment: kBufs buffers of unnormalised outputs
 // (summed here; element (r, d) of a buffer at off(r, d)) and the row statistics
 // m, l.  A whole segment goes out, a part to the CTA's slot.
-template <int kRows, int kBufs, typename T, typename Off>
+template <int kRows, int kBufs, int kCta, typename T, typename Off>
 __device__ __forceinline__ void write_segment(const AttendArgs &p, const float *buf, int buf_stride,
                                               const float *m, const float *l, int seq, int unit,
                                               int n, bool whole, int slot, Off &&off) {
@@ -189,7 +227,7 @@ __device__ __forceinline__ void write_segment(const AttendArgs &p, const float *
   const int kvh = unit / p.row_blocks, r0 = (unit - kvh * p.row_blocks) * kRows;
   const int rows = a.group * n;
   float *part = p.part + (static_cast<size_t>(blockIdx.x) * 2 + slot) * (kRows * (2 + D));
-  for (int e = threadIdx.x; e < kRows * D; e += kThreads) {
+  for (int e = threadIdx.x; e < kRows * D; e += kCta) {
     const int r = e / D, d = e - r * D;
     const int o = off(r, d);
     float v = 0.f;
@@ -297,99 +335,106 @@ __device__ __forceinline__ float load_q_frags(const AttendArgs &p, int seq, int 
 template <int D, int NT>
 struct MmaCfg {
   static constexpr int kRows = 8 * NT;
-  static constexpr int kCtasPerSm = NT == 1 ? 2 : 1;
-  static constexpr int kStages = NT == 1 ? 3 : 4;
-  static constexpr int kStageBytes = 2 * kKeys * D + 16;  // K, V and the two scales
+  static constexpr int kStages = NT == 1 ? 3 : 2;
+  static constexpr int kStageBytes = 2 * kKeys * D + 16;  // K, V and two scales each
   static constexpr int kRing = kWarps * kStages * kStageBytes;
   static constexpr int kBuf = kRows * D;                  // floats per merge buffer
   static constexpr int kQ = NT == 1 ? 0 : NT * (D / 16) * 32 * 8;
-  static constexpr int kStat = (2 * kWarps * kRows + kWarps + 3 * kRows) * 4;
-  static constexpr int kSmem = kRing + 4 * kBuf * 4 + kQ + kStat;
+  static constexpr int kStat = (2 * kWarps * kRows + 3 * kRows) * 4;
+  static constexpr int kSmem = kRing + 2 * kBuf * 4 + kQ + kStat;
 };
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, (MmaCfg<D, NT>::kCtasPerSm))
-    attend_mma_kernel(const AttendArgs p) {
+__global__ void __launch_bounds__(kThreads, 2) attend_mma_kernel(const AttendArgs p) {
   using Cfg = MmaCfg<D, NT>;
-  constexpr int KS = D / 16;  // k-steps of the first product, m-tiles of the second
+  constexpr int KS = D / 16;  // k-steps of the first product
+  constexpr int MT = D / 16;  // m-tiles of the second
+  constexpr int CH = D / 16;  // 16-byte chunks per row
   extern __shared__ __align__(128) uint8_t smem[];
   float *s_buf = reinterpret_cast<float *>(smem + Cfg::kRing);
-  uint2 *s_q = reinterpret_cast<uint2 *>(s_buf + 4 * Cfg::kBuf);
+  uint2 *s_q = reinterpret_cast<uint2 *>(s_buf + 2 * Cfg::kBuf);
   float *s_m = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(s_q) + Cfg::kQ);
   float *s_l = s_m + kWarps * Cfg::kRows;
-  float *s_vref = s_l + kWarps * Cfg::kRows;
-  float *s_M = s_vref + kWarps, *s_L = s_M + Cfg::kRows, *s_rs = s_L + Cfg::kRows;
+  float *s_M = s_l + kWarps * Cfg::kRows, *s_L = s_M + Cfg::kRows, *s_rs = s_L + Cfg::kRows;
 
   const Cache8AttendArgs &a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
   const int units = a.n_kv_heads * p.row_blocks;
-  const long long total = tiles_before(a, units, a.n_seqs);
-  const int ctas = busy_ctas(total, p.ctas);
-  if (static_cast<int>(blockIdx.x) >= ctas) return;
-  const long long t0 = run_start(total, ctas, blockIdx.x);
-  const long long t1 = run_start(total, ctas, blockIdx.x + 1);
+  pdl_launch_dependents();
+  const Split w = split_of(a, units, p.ctas);
+  const int t0 = blockIdx.x * w.run;
+  if (t0 >= w.total) return;
+  const int run = min(w.run, w.total - t0);
 
   const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) +
                         warp * Cfg::kStages * Cfg::kStageBytes;
-  const int sub = warp * kKeys;  // this warp's keys within a tile
+  const uint8_t *ring_ptr = smem + warp * Cfg::kStages * Cfg::kStageBytes;
 
-  // one tile of this warp into a stage of its ring
-  auto issue = [&](const Cursor &k, int stage) {
-    const int j0 = k.tile * kTile + sub;
-    if (j0 < k.q.len) {
-      const uint32_t dst = ring + stage * Cfg::kStageBytes;
-      const int kvh = k.unit / p.row_blocks;
-      const size_t head = static_cast<size_t>(k.seq) * a.n_kv_heads + kvh;
-      const size_t off = (head * a.cap + j0) * D;
-      constexpr int CH = D / 16;  // 16-byte chunks per row
-#pragma unroll
-      for (int i = 0; i < kKeys * CH / 32; ++i) {
-        const int q = i * 32 + lane;
-        const int key = q / CH, ch = q % CH;
-        const bool there = j0 + key < k.q.len;
-        // swizzles: both reads below are then free of bank conflicts
-        const int kc = D == 128 ? ch ^ ((key & 1) << 2) : ch;
-        const int vc = D == 128 ? ch ^ (key & 7) : ch ^ ((key >> 1) & 3);
-        cp_async16(dst + key * D + kc * 16, a.k8 + off + q * 16, there);
-        cp_async16(dst + kKeys * D + key * D + vc * 16, a.v8 + off + q * 16, there);
-      }
-      if (lane < 2) {
-        const size_t b = head * (a.cap / a.block) + j0 / a.block;
-        cp_async4(dst + 2 * kKeys * D + lane * 4, (lane ? a.v_scale : a.k_scale) + b);
-      }
-    }
-    cp_async_commit();
-  };
-
+  // ---- loads: this lane's 16-byte pieces of a tile, with the swizzles that
+  // make both reads below free of bank conflicts
+  constexpr int PIECES = kKeys * CH / 32;
+  const int lrow = lane / CH, lch = lane % CH;  // piece i: row lrow + i * (32 / CH)
+  const uint32_t k_dst = lrow * D + (D == 128 ? lch ^ ((lrow & 1) << 2) : lch) * 16;
+  const uint32_t v_dst0 = kKeys * D + lrow * D + (D == 128 ? lch ^ lrow : lch ^ ((lrow >> 1) & 3)) * 16;
   Cursor load, cur;
-  cur.seek(a, units, t0);
+  cur.seek(a, w, units, t0);
   load = cur;
-  long long issued = t0;
+  int load_unit = -1, load_seq = -1;
+  const uint8_t *k_src = nullptr, *v_src = nullptr;
+  const float *sc_src = nullptr;
+  auto issue = [&](int stage) {
+    if (load.unit != load_unit || load.seq != load_seq) {  // another segment
+      load_unit = load.unit;
+      load_seq = load.seq;
+      const size_t head = static_cast<size_t>(load.seq) * a.n_kv_heads + load.unit / p.row_blocks;
+      const size_t off = (head * a.cap + warp * kKeys) * D + lane * 16;
+      k_src = a.k8 + off;
+      v_src = a.v8 + off;
+      // lanes 0..3: the K and V scales of the tile's first and second 16 keys
+      sc_src = (lane & 1 ? a.v_scale : a.k_scale) + head * (a.cap >> p.log2_block);
+    }
+    const int j0 = load.tile * kTile + warp * kKeys;
+    const int there = load.q.len - j0;  // rows of this warp's keys that exist
+    if (there > 0) {
+      const uint32_t dst = ring + stage * Cfg::kStageBytes;
+      const size_t off = static_cast<size_t>(load.tile) * (kTile * D);
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i) {
+        const bool ok = lrow + i * (32 / CH) < there;
+        const uint32_t vd = D == 128 ? v_dst0 ^ ((i & 1) << 6) : v_dst0;
+        cp_async16(dst + k_dst + i * 512, k_src + off + i * 512, ok);
+        cp_async16(dst + vd + i * 512, v_src + off + i * 512, ok);
+      }
+      if (lane < 4 && (lane >> 1) * 16 < there)
+        cp_async4(dst + 2 * kKeys * D + lane * 4, sc_src + ((j0 + (lane >> 1) * 16) >> p.log2_block));
+    }
+    load.next(a, w, units);
+  };
 #pragma unroll
   for (int s = 0; s < Cfg::kStages - 1; ++s) {
-    if (issued < t1) {
-      issue(load, s);
-      load.next(a, units);
-    } else {
-      cp_async_commit();
-    }
-    ++issued;
+    if (load.at < run) issue(s);
+    cp_async_commit();
   }
 
+  // ---- what a lane reads
+  const int key0 = ((g >> 1) << 2) | (g & 1);  // and key0 + 2: rows g and g + 8 of an m-tile
   uint2 qf[NT == 1 ? KS : 1];
   float rs[NT][2];
-  float o[KS][NT][4];
+  float o[MT][NT][4];
   float m[NT][2], l[NT][2];
-  float vref = 0.f;
+  float vref = 0.f, ivref = 0.f;
+  int kvh = 0, r0 = 0, seen0 = 0;
   bool fresh = true;
-  int stage = 0;
+  int stage = 0, seg_tiles = 0;
 
-  for (long long it = t0; it < t1; ++it) {
-    const int kvh = cur.unit / p.row_blocks;
-    const int r0 = (cur.unit - kvh * p.row_blocks) * Cfg::kRows;
+  while (cur.at < run) {
     if (fresh) {  // a new segment: its queries, empty statistics
       fresh = false;
+      seg_tiles = 0;
+      kvh = cur.unit / p.row_blocks;
+      r0 = (cur.unit - kvh * p.row_blocks) * Cfg::kRows;
+      seen0 = cur.q.len - cur.q.n + 1;  // keys that token 0 sees
       const int rows = a.group * cur.q.n;
       if constexpr (NT == 1) {
         const float f = load_q_frags<D>(p, cur.seq, kvh, r0 + g, rows, qf);
@@ -415,149 +460,161 @@ __global__ void __launch_bounds__(kThreads, (MmaCfg<D, NT>::kCtasPerSm))
         m[nt][0] = m[nt][1] = -INFINITY;
         l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
-        for (int mt = 0; mt < KS; ++mt)
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int i = 0; i < 4; ++i) o[mt][nt][i] = 0.f;
       }
-      vref = 0.f;
+      vref = ivref = 0.f;
     }
-    cp_async_wait<Cfg::kStages - 2>();
+    // the stage read in the last round is free
+    if (load.at < run) issue(stage == 0 ? Cfg::kStages - 1 : stage - 1);
+    cp_async_commit();
+    cp_async_wait<Cfg::kStages - 1>();
     __syncwarp();
-    const int j0 = cur.tile * kTile + sub;
-    const int seen0 = cur.q.len - cur.q.n + 1;  // keys that token 0 sees
-    if (j0 < cur.q.len) {
-      const uint8_t *st = smem + (warp * Cfg::kStages + stage) * Cfg::kStageBytes;
-      const float ks = *reinterpret_cast<const float *>(st + 2 * kKeys * D);
-      const float vs = *reinterpret_cast<const float *>(st + 2 * kKeys * D + 4);
-      // ---- logits: rows of the tile (A) in the order that leaves lane c the
-      // probabilities of keys 4c .. 4c+3 after the transposition below
-      const int key0 = ((g >> 1) << 2) | (g & 1);  // and key0 + 2
-      float x[NT][4];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.f;
-#pragma unroll
-      for (int h = 0; h < D / 64; ++h) {
-        const int ch = D == 128 ? (c + 4 * h) ^ ((key0 & 1) << 2) : c;
-        const uint4 ka = *reinterpret_cast<const uint4 *>(st + key0 * D + ch * 16);
-        const uint4 kb = *reinterpret_cast<const uint4 *>(st + (key0 + 2) * D + ch * 16);
-        const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const uint32_t a0 = e4m3x2_to_f16x2(wa[w]), a2 = e4m3x2_to_f16x2(wa[w] >> 16);
-          const uint32_t a1 = e4m3x2_to_f16x2(wb[w]), a3 = e4m3x2_to_f16x2(wb[w] >> 16);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const uint2 b = NT == 1 ? qf[NT == 1 ? h * 4 + w : 0]
-                                    : s_q[(nt * KS + h * 4 + w) * 32 + lane];
-            mma16816(x[nt], a0, a1, a2, a3, b.x, b.y);
-          }
-        }
-      }
+    const int j0 = cur.tile * kTile + warp * kKeys;
+    const int there = cur.q.len - j0;
+    if (there > 0) {
+      const uint8_t *st = ring_ptr + stage * Cfg::kStageBytes;
+      const float4 sc = *reinterpret_cast<const float4 *>(st + 2 * kKeys * D);
+      const float ks[2] = {sc.x, sc.z};
+      const float vs[2] = {sc.y, there > 16 ? sc.w : 0.f};
+      // ---- logits, 16 keys (an m-tile) at a time; the rows are in the order
+      // that leaves lane c the probabilities of keys 4c .. 4c+3 when transposed
       const bool masked = j0 + kKeys > seen0 + r0 / a.group;
+      float x[2][NT][4];
       bool grow = false;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const float f0 = ks * rs[nt][0], f1 = ks * rs[nt][1];
-        x[nt][0] *= f0, x[nt][2] *= f0;
-        x[nt][1] *= f1, x[nt][3] *= f1;
-        if (masked) {
-          const int r = r0 + nt * 8 + 2 * c;
-          const int v0 = seen0 + r / a.group, v1 = seen0 + (r + 1) / a.group;
-          if (j0 + key0 >= v0) x[nt][0] = -INFINITY;
-          if (j0 + key0 >= v1) x[nt][1] = -INFINITY;
-          if (j0 + key0 + 2 >= v0) x[nt][2] = -INFINITY;
-          if (j0 + key0 + 2 >= v1) x[nt][3] = -INFINITY;
+      for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[t][nt][i] = 0.f;
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h) {
+          const int ch = D == 128 ? (c + 4 * h) ^ ((key0 & 1) << 2) : c;
+          const uint8_t *row = st + (t * 16 + key0) * D + ch * 16;
+          const uint4 ka = *reinterpret_cast<const uint4 *>(row);
+          const uint4 kb = *reinterpret_cast<const uint4 *>(row + 2 * D);
+          const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const uint32_t a0 = e4m3x2_to_f16x2(wa[w]), a2 = e4m3x2_to_f16x2(wa[w] >> 16);
+            const uint32_t a1 = e4m3x2_to_f16x2(wb[w]), a3 = e4m3x2_to_f16x2(wb[w] >> 16);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const uint2 b = NT == 1 ? qf[NT == 1 ? h * 4 + w : 0]
+                                      : s_q[(nt * KS + h * 4 + w) * 32 + lane];
+              mma16816(x[t][nt], a0, a1, a2, a3, b.x, b.y);
+            }
+          }
         }
-        grow |= fmaxf(x[nt][0], x[nt][2]) > m[nt][0] + 8.f;
-        grow |= fmaxf(x[nt][1], x[nt][3]) > m[nt][1] + 8.f;
-        if (p.x_cols > 0) {
-          const int col = r0 + nt * 8 + 2 * c;
-          if (col < p.x_cols) {
-            float *xs = p.x + ((static_cast<size_t>(cur.seq) * a.n_kv_heads + kvh) * p.x_len + j0 +
-                               key0) * p.x_cols + col;
-            *reinterpret_cast<float2 *>(xs) = make_float2(x[nt][0], x[nt][1]);
-            *reinterpret_cast<float2 *>(xs + 2 * p.x_cols) = make_float2(x[nt][2], x[nt][3]);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const float f0 = ks[t] * rs[nt][0], f1 = ks[t] * rs[nt][1];
+          float(&y)[4] = x[t][nt];
+          y[0] *= f0;
+          y[1] *= f1;
+          y[2] *= f0;
+          y[3] *= f1;
+          if (masked) {
+            const int r = r0 + nt * 8 + 2 * c, j = j0 + t * 16 + key0;
+            const int v0 = seen0 + r / a.group, v1 = seen0 + (r + 1) / a.group;
+            if (j >= v0) y[0] = -INFINITY;
+            if (j >= v1) y[1] = -INFINITY;
+            if (j + 2 >= v0) y[2] = -INFINITY;
+            if (j + 2 >= v1) y[3] = -INFINITY;
+          }
+          grow |= fmaxf(y[0], y[2]) > m[nt][0] + 15.f;
+          grow |= fmaxf(y[1], y[3]) > m[nt][1] + 15.f;
+          if (p.x_cols > 0) {
+            const int col = r0 + nt * 8 + 2 * c;
+            if (col < p.x_cols && t * 16 < there) {
+              float *xs = p.x + ((static_cast<size_t>(cur.seq) * a.n_kv_heads + kvh) * p.x_len + j0 +
+                                 t * 16 + key0) * p.x_cols + col;
+              *reinterpret_cast<float2 *>(xs) = make_float2(y[0], y[1]);
+              *reinterpret_cast<float2 *>(xs + 2 * p.x_cols) = make_float2(y[2], y[3]);
+            }
           }
         }
       }
+      // ---- a row's reference: 7 (in log2) under the largest logit when it was
+      // set, so that the probabilities are at most 2^15
       if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            float t = fmaxf(x[nt][i], x[nt][i + 2]);
+            float t = fmaxf(fmaxf(x[0][nt][i], x[0][nt][i + 2]), fmaxf(x[1][nt][i], x[1][nt][i + 2]));
             t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
             t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
-            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16)) - 7.f;
             if (t > m[nt][i]) {
               const float f = ex2(m[nt][i] - t);
               m[nt][i] = t;
               l[nt][i] *= f;
 #pragma unroll
-              for (int mt = 0; mt < KS; ++mt) {
+              for (int mt = 0; mt < MT; ++mt) {
                 o[mt][nt][i] *= f;
                 o[mt][nt][i + 2] *= f;
               }
             }
           }
       }
-      if (vs > vref) {  // the outputs are held in units of the largest V scale
-        const float f = vref / vs;
-        vref = vs;
+      const float vmax = fmaxf(vs[0], vs[1]);
+      if (vmax > vref) {  // the outputs are held in units of the largest V scale
+        const float f = vref / vmax;
+        vref = vmax;
+        ivref = 1.f / vmax;
 #pragma unroll
-        for (int mt = 0; mt < KS; ++mt)
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[mt][nt][i] *= f;
       }
-      const float vr = vs / vref;
-      uint32_t b[NT][2];
+      uint32_t b[NT][2][2];  // B fragments of the two k-steps: keys 4c .. 4c+3 of each m-tile
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
         const float m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
-        const float p0 = ex2(x[nt][0] - m0), p1 = ex2(x[nt][1] - m1);
-        const float p2 = ex2(x[nt][2] - m0), p3 = ex2(x[nt][3] - m1);
-        l[nt][0] += p0 + p2;
-        l[nt][1] += p1 + p3;
-        b[nt][0] = transpose8x8(as_u32(__floats2half2_rn(p0 * vr, p1 * vr)));
-        b[nt][1] = transpose8x8(as_u32(__floats2half2_rn(p2 * vr, p3 * vr)));
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const float vr = vs[t] * ivref;
+          const float p0 = ex2(x[t][nt][0] - m0), p1 = ex2(x[t][nt][1] - m1);
+          const float p2 = ex2(x[t][nt][2] - m0), p3 = ex2(x[t][nt][3] - m1);
+          l[nt][0] += p0 + p2;
+          l[nt][1] += p1 + p3;
+          b[nt][t][0] = transpose8x8(as_u32(__floats2half2_rn(p0 * vr, p1 * vr)));
+          b[nt][t][1] = transpose8x8(as_u32(__floats2half2_rn(p2 * vr, p3 * vr)));
+        }
       }
-      // ---- outputs: V^T (A) by ldmatrix, 16 keys x 16 elements a matrix
-      const uint32_t vbase = ring + stage * Cfg::kStageBytes + kKeys * D;
-      const int vkey = lane & 15;
+      // ---- outputs: V^T (A) by ldmatrix, 16 elements x 32 keys an m-tile
+      const uint32_t vbase = ring + stage * Cfg::kStageBytes + kKeys * D + lane * D;
+      const uint32_t vsw = D == 128 ? (lane & 7) << 4 : ((lane >> 1) & 3) << 4;
 #pragma unroll
-      for (int mt = 0; mt < KS; mt += 2) {
-        const int ch = mt + (lane >> 4);
-        const int vc = D == 128 ? ch ^ (vkey & 7) : ch ^ ((vkey >> 1) & 3);
-        uint32_t w0, w1, w2, w3;
+      for (int mt = 0; mt < MT; ++mt) {
+        uint32_t w[4];
         asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(w0), "=r"(w1), "=r"(w2), "=r"(w3)
-                     : "r"(vbase + vkey * D + vc * 16)
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(vbase + ((mt << 4) ^ vsw))
                      : "memory");
-        const uint32_t a0 = e4m3x2_to_f16x2(w0), a2 = e4m3x2_to_f16x2(w0 >> 16);
-        const uint32_t a1 = e4m3x2_to_f16x2(w1), a3 = e4m3x2_to_f16x2(w1 >> 16);
-        const uint32_t c0 = e4m3x2_to_f16x2(w2), c2 = e4m3x2_to_f16x2(w2 >> 16);
-        const uint32_t c1 = e4m3x2_to_f16x2(w3), c3 = e4m3x2_to_f16x2(w3 >> 16);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma16816(o[mt][nt], a0, a1, a2, a3, b[nt][0], b[nt][1]);
-          mma16816(o[mt + 1][nt], c0, c1, c2, c3, b[nt][0], b[nt][1]);
+        for (int t = 0; t < 2; ++t) {
+          const uint32_t a0 = e4m3x2_to_f16x2(w[2 * t]), a2 = e4m3x2_to_f16x2(w[2 * t] >> 16);
+          const uint32_t a1 = e4m3x2_to_f16x2(w[2 * t + 1]), a3 = e4m3x2_to_f16x2(w[2 * t + 1] >> 16);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma16816(o[mt][nt], a0, a1, a2, a3, b[nt][t][0], b[nt][t][1]);
         }
       }
     }
     __syncwarp();  // every lane has read its stage
-    if (issued < t1) {
-      issue(load, (stage + Cfg::kStages - 1) % Cfg::kStages);
-      load.next(a, units);
-    } else {
-      cp_async_commit();
-    }
-    ++issued;
     stage = stage + 1 == Cfg::kStages ? 0 : stage + 1;
+    ++seg_tiles;
 
-    if (cur.tile + 1 == cur.q.tiles || it + 1 == t1) {  // the segment ends here
+    if (cur.tile + 1 == cur.q.tiles || cur.at + 1 == run) {  // the segment ends here
+      const bool to_end = cur.tile + 1 == cur.q.tiles;
+      const bool from_start = seg_tiles == cur.tile + 1;
+      float lsum[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -566,6 +623,7 @@ __global__ void __launch_bounds__(kThreads, (MmaCfg<D, NT>::kCtasPerSm))
           t += __shfl_xor_sync(0xffffffffu, t, 4);
           t += __shfl_xor_sync(0xffffffffu, t, 8);
           t += __shfl_xor_sync(0xffffffffu, t, 16);
+          lsum[nt][i] = t;
           if (g == 0) {
             s_m[warp * Cfg::kRows + nt * 8 + 2 * c + i] = m[nt][i];
             s_l[warp * Cfg::kRows + nt * 8 + 2 * c + i] = t;
@@ -582,9 +640,11 @@ __global__ void __launch_bounds__(kThreads, (MmaCfg<D, NT>::kCtasPerSm))
           float M = -INFINITY;
 #pragma unroll
           for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w * Cfg::kRows + r]);
-          f[nt][i] = (m[nt][i] == -INFINITY ? (l[nt][i] != l[nt][i] ? 1.f : 0.f) : ex2(m[nt][i] - M)) * vref;
+          f[nt][i] = (m[nt][i] != -INFINITY ? ex2(m[nt][i] - M)
+                                            : lsum[nt][i] != lsum[nt][i] ? 1.f : 0.f) * vref;
           if (warp == 0 && g == 0) {
             float L = 0.f;
+#pragma unroll
             for (int w = 0; w < kWarps; ++w) {
               const float mw = s_m[w * Cfg::kRows + r], lw = s_l[w * Cfg::kRows + r];
               L += mw == -INFINITY ? lw : ex2(mw - M) * lw;
@@ -594,31 +654,26 @@ __global__ void __launch_bounds__(kThreads, (MmaCfg<D, NT>::kCtasPerSm))
           }
         }
       auto at = [&](int mt, int nt, int i) { return ((mt * NT + nt) * 4 + i) * 32 + lane; };
-      if (warp >= kWarps / 2) {
-        float *bf = s_buf + (warp - kWarps / 2) * Cfg::kBuf;
+      float *bf = s_buf + (warp & 1) * Cfg::kBuf;
+      if (warp >= 2) {
 #pragma unroll
-        for (int mt = 0; mt < KS; ++mt)
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 4; ++i) bf[at(mt, nt, i)] = o[mt][nt][i] * f[nt][i & 1];
       }
       __syncthreads();
-      if (warp < kWarps / 2) {
-        float *bf = s_buf + warp * Cfg::kBuf;
+      if (warp < 2) {
 #pragma unroll
-        for (int mt = 0; mt < KS; ++mt)
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 4; ++i) bf[at(mt, nt, i)] += o[mt][nt][i] * f[nt][i & 1];
       }
       __syncthreads();
-      // tiles of the segment before this one in the CTA's run
-      const bool from_start = it - cur.tile >= t0;
-      const bool to_end = cur.tile + 1 == cur.q.tiles;
-      using T = __nv_bfloat16;
-      write_segment<Cfg::kRows, 4, T>(
+      write_segment<Cfg::kRows, 2, kThreads, __nv_bfloat16>(
           p, s_buf, Cfg::kBuf, s_M, s_L, cur.seq, cur.unit, cur.q.n, from_start && to_end,
           from_start ? 1 : 0, [](int r, int d) {
             return (((d >> 4) * NT + (r >> 3)) * 4 + ((d >> 3) & 1) * 2 + (r & 1)) * 32 +
@@ -627,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, (MmaCfg<D, NT>::kCtasPerSm))
       __syncthreads();
       fresh = true;
     }
-    cur.next(a, units);
+    cur.next(a, w, units);
   }
 }
 
@@ -668,32 +723,33 @@ __device__ __forceinline__ void simt_logits(const uint8_t *key_row, int D, int h
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) attend_simt_kernel(const AttendArgs p) {
+__global__ void __launch_bounds__(kSimtThreads) attend_simt_kernel(const AttendArgs p) {
   __shared__ __align__(16) float s_q[kSimtRows * kMaxD];
-  __shared__ __align__(16) float s_buf[kWarps * kSimtRows * kMaxD];
-  __shared__ float s_p[kWarps][kKeys][kSimtRows];
-  __shared__ float s_m[kWarps][kSimtRows], s_l[kWarps][kSimtRows];
+  __shared__ __align__(16) float s_buf[kSimtWarps * kSimtRows * kMaxD];
+  __shared__ float s_p[kSimtWarps][kSimtKeys][kSimtRows];
+  __shared__ float s_m[kSimtWarps][kSimtRows], s_l[kSimtWarps][kSimtRows];
   __shared__ float s_M[kSimtRows], s_L[kSimtRows];
   const Cache8AttendArgs &a = p.a;
   const int D = a.head_dim;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int units = a.n_kv_heads * p.row_blocks;
-  const long long total = tiles_before(a, units, a.n_seqs);
-  const int ctas = busy_ctas(total, p.ctas);
-  if (static_cast<int>(blockIdx.x) >= ctas) return;
-  const long long t0 = run_start(total, ctas, blockIdx.x);
-  const long long t1 = run_start(total, ctas, blockIdx.x + 1);
+  pdl_launch_dependents();
+  const Split w = split_of(a, units, p.ctas);
+  const int t0 = blockIdx.x * w.run;
+  if (t0 >= w.total) return;
+  const int run = min(w.run, w.total - t0);
   Cursor cur;
-  cur.seek(a, units, t0);
+  cur.seek(a, w, units, t0);
+  int seg_tiles = 0;
   float o[kSimtRows][4], m[kSimtRows], l[kSimtRows];
   bool fresh = true;
-  for (long long it = t0; it < t1; ++it) {
+  while (cur.at < run) {
     const int kvh = cur.unit / p.row_blocks;
     const int r0 = (cur.unit - kvh * p.row_blocks) * kSimtRows;
     const size_t head = static_cast<size_t>(cur.seq) * a.n_kv_heads + kvh;
     if (fresh) {
       fresh = false;
-      for (int e = threadIdx.x; e < kSimtRows * D; e += kThreads) {
+      for (int e = threadIdx.x; e < kSimtRows * D; e += kSimtThreads) {
         const int r = r0 + e / D;
         s_q[e] = r < a.group * cur.q.n
                      ? load_q(static_cast<const T *>(a.q) + q_row(a, cur.seq, kvh, r) * D + e % D)
@@ -707,7 +763,7 @@ __global__ void __launch_bounds__(kThreads) attend_simt_kernel(const AttendArgs 
         o[r][0] = o[r][1] = o[r][2] = o[r][3] = 0.f;
       }
     }
-    const int j0 = cur.tile * kTile + warp * kKeys;
+    const int j0 = cur.tile * kTile + warp * kSimtKeys;
     const int seen0 = cur.q.len - cur.q.n + 1;
     if (j0 < cur.q.len) {
       const int j = min(j0 + (lane >> 1), cur.q.len - 1);  // rows past the end are not read
@@ -739,7 +795,7 @@ __global__ void __launch_bounds__(kThreads) attend_simt_kernel(const AttendArgs 
       }
       __syncwarp();
       if (lane * 4 < D) {
-        const int keys = min(kKeys, cur.q.len - j0);
+        const int keys = min(kSimtKeys, cur.q.len - j0);
         for (int k = 0; k < keys; ++k) {
           float v[4];
           values4(__ldg(reinterpret_cast<const uint32_t *>(a.v8 + (head * a.cap + j0 + k) * D) + lane), v);
@@ -753,7 +809,8 @@ __global__ void __launch_bounds__(kThreads) attend_simt_kernel(const AttendArgs 
       }
       __syncwarp();
     }
-    if (cur.tile + 1 == cur.q.tiles || it + 1 == t1) {
+    ++seg_tiles;
+    if (cur.tile + 1 == cur.q.tiles || cur.at + 1 == run) {
 #pragma unroll
       for (int r = 0; r < kSimtRows; ++r) {
         float t = l[r];
@@ -769,115 +826,33 @@ __global__ void __launch_bounds__(kThreads) attend_simt_kernel(const AttendArgs 
 #pragma unroll
       for (int r = 0; r < kSimtRows; ++r) {
         float M = -INFINITY, L = 0.f;
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][r]);
+        for (int w = 0; w < kSimtWarps; ++w) M = fmaxf(M, s_m[w][r]);
         const float f = m[r] == -INFINITY ? (l[r] != l[r] ? 1.f : 0.f) : exp2f(m[r] - M);
         if (lane * 4 < D)
           *reinterpret_cast<float4 *>(s_buf + (warp * kSimtRows + r) * D + lane * 4) =
               make_float4(o[r][0] * f, o[r][1] * f, o[r][2] * f, o[r][3] * f);
         if (threadIdx.x == 0) {
-          for (int w = 0; w < kWarps; ++w)
+          for (int w = 0; w < kSimtWarps; ++w)
             L += s_m[w][r] == -INFINITY ? s_l[w][r] : exp2f(s_m[w][r] - M) * s_l[w][r];
           s_M[r] = M;
           s_L[r] = L;
         }
       }
       __syncthreads();
-      const bool from_start = it - cur.tile >= t0;
+      const bool from_start = seg_tiles == cur.tile + 1;
       const bool to_end = cur.tile + 1 == cur.q.tiles;
-      write_segment<kSimtRows, kWarps, T>(p, s_buf, kSimtRows * D, s_M, s_L, cur.seq, cur.unit,
+      seg_tiles = 0;
+      write_segment<kSimtRows, kSimtWarps, kSimtThreads, T>(p, s_buf, kSimtRows * D, s_M, s_L, cur.seq, cur.unit,
                                           cur.q.n, from_start && to_end, from_start ? 1 : 0,
                                           [D](int r, int d) { return r * D + d; });
       __syncthreads();
       fresh = true;
     }
-    cur.next(a, units);
+    cur.next(a, w, units);
   }
 }
 
-// ------------------------------------------------------------------- the join
-
-// One CTA per (sequence, KV head, row block) row: joins the parts of a segment
-// that several CTAs computed, and writes the empty rows of sequences without
-// cached keys.  Each warp takes every eighth part, in order; the warps' sums
-// are added in order, so results do not depend on timing.
-template <int kRows, typename T>
-__global__ void __launch_bounds__(kThreads) attend_finish_kernel(const AttendArgs p) {
-  __shared__ float s_o[kWarps][kMaxD];
-  __shared__ float s_red[2][kWarps];
-  const Cache8AttendArgs &a = p.a;
-  const int D = a.head_dim;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int units = a.n_kv_heads * p.row_blocks;
-  const int row = blockIdx.x % kRows;
-  const int u = blockIdx.x / kRows;
-  const int seq = u / units, unit = u - seq * units;
-  const int kvh = unit / p.row_blocks;
-  const int r = (unit - kvh * p.row_blocks) * kRows + row;
-  const SeqInfo q = seq_info(a, seq);
-  if (q.bad) {
-    if (threadIdx.x == 0) record_device_status(BKV_DEV_ASSERT, 611);
-    return;
-  }
-  if (r >= a.group * q.n) return;
-  T *out = static_cast<T *>(a.out) + q_row(a, seq, kvh, r) * D;
-  if (q.tiles == 0) {
-    if (threadIdx.x < D) store_out(out + threadIdx.x, 0.f);
-    if (threadIdx.x == 0) store_lse(p, seq, kvh, r, -INFINITY, 0.f);
-    return;
-  }
-  const long long total = tiles_before(a, units, a.n_seqs);
-  const long long b = tiles_before(a, units, seq) + static_cast<long long>(unit) * q.tiles;
-  const int ctas = busy_ctas(total, p.ctas);
-  const int c0 = cta_of(total, ctas, b), c1 = cta_of(total, ctas, b + q.tiles - 1);
-  if (c0 == c1) return;  // written by its CTA
-  const int parts = c1 - c0 + 1;
-  const int stride = kRows * (2 + D);
-  // part i: CTA c0 + i; slot 1 of the CTA the segment starts in, slot 0 after it
-  auto part = [&](int i) {
-    return p.part + (static_cast<size_t>(c0 + i) * 2 + (i == 0 ? 1 : 0)) * stride;
-  };
-  float M = -INFINITY;
-  for (int i = threadIdx.x; i < parts; i += kThreads) M = fmaxf(M, part(i)[row]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  if (lane == 0) s_red[0][warp] = M;
-  __syncthreads();
-  M = s_red[0][0];
-#pragma unroll
-  for (int w = 1; w < kWarps; ++w) M = fmaxf(M, s_red[0][w]);
-  float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int i = warp; i < parts; i += kWarps) {
-    const float *s = part(i);
-    const float mi = s[row], li = s[kRows + row];
-    const float f = mi == -INFINITY ? 0.f : exp2f(mi - M);
-    l += mi == -INFINITY ? li : f * li;
-    if (lane * 4 < D) {
-      const float4 v = *reinterpret_cast<const float4 *>(s + 2 * kRows + row * D + lane * 4);
-      if (f > 0.f || mi != mi) {
-        o[0] = fmaf(f, v.x, o[0]), o[1] = fmaf(f, v.y, o[1]);
-        o[2] = fmaf(f, v.z, o[2]), o[3] = fmaf(f, v.w, o[3]);
-      } else if (li != li) {
-        o[0] = o[1] = o[2] = o[3] = li;  // NaN logits
-      }
-    }
-  }
-  if (lane * 4 < D)
-    *reinterpret_cast<float4 *>(&s_o[warp][lane * 4]) = make_float4(o[0], o[1], o[2], o[3]);
-  if (lane == 0) s_red[1][warp] = l;
-  __syncthreads();
-  float L = 0.f;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) L += s_red[1][w];
-  if (threadIdx.x < D) {
-    float v = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) v += s_o[w][threadIdx.x];
-    store_out(out + threadIdx.x, L > 0.f || L != L ? v / L : 0.f);
-  }
-  if (threadIdx.x == 0) store_lse(p, seq, kvh, r, M, L);
-}
-
-// ---------------------------------------------------------------- the weights
+// ------------------------------------------- the join of parts, and the weights
 
 __device__ __forceinline__ void store_weight(const Cache8AttendArgs &a, size_t head, int j,
                                              const SeqInfo &q, float sum) {
@@ -886,30 +861,157 @@ __device__ __forceinline__ void store_weight(const Cache8AttendArgs &a, size_t h
   a.w_out[head * a.cap + j] = sum;
 }
 
-// From the logits the attention kernel kept.  One thread per key.
-__global__ void __launch_bounds__(kThreads) weights_kept_kernel(const AttendArgs p) {
+// The parts of a segment: the CTAs c0 .. c0 + n - 1 (n = 1: whole).
+struct Parts {
+  int c0, n;
+};
+__device__ __forceinline__ Parts parts_of(const Split &w, int first, int tiles) {
+  Parts x;
+  x.c0 = first / w.run;
+  x.n = (first + tiles - 1) / w.run - x.c0 + 1;
+  return x;
+}
+
+// First the CTAs that join: p.join_rows rows of a (sequence, KV head, row
+// block) each, one row at a time with every warp (few segments in many parts)
+// or a row per warp (many segments in few).  They write the rows of segments
+// that several CTAs computed, and the empty rows of sequences without cached
+// keys.  A row's parts are dealt to its warps in turn and the warps' sums added
+// in order, so results do not depend on timing.
+// Then, where the attention kernel kept its logits, the CTAs of the weights:
+// one per 256 keys of a (sequence, KV head), which need the rows' lse and so
+// join the parts' statistics for themselves.
+// Launched while the attention kernel runs: everything before the wait reads
+// only the lengths, and every CTA waits, so that this kernel never ends first.
+template <int kRows, typename T>
+__global__ void __launch_bounds__(kSimtThreads) attend_finish_kernel(const AttendArgs p) {
+  __shared__ float s_o[kSimtWarps][kMaxD];
+  __shared__ float s_l[kSimtWarps];
   __shared__ float s_z[kMaxXRows];
   const Cache8AttendArgs &a = p.a;
-  const size_t head = blockIdx.y;
-  const int seq = static_cast<int>(head) / a.n_kv_heads;
+  const int D = a.head_dim;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int units = a.n_kv_heads * p.row_blocks;
+  const int per_unit = kRows / p.join_rows;
+  const int joins = a.n_seqs * units * per_unit;
+  const int stride = kRows * (2 + D);
+  // a part's statistics and output: slot 1 of the CTA the segment starts in,
+  // slot 0 after it
+  auto part = [&](const Parts &x, int i) {
+    return p.part + (static_cast<size_t>(x.c0 + i) * 2 + (i == 0 ? 1 : 0)) * stride;
+  };
+  if (static_cast<int>(blockIdx.x) >= joins) {
+    const int b = blockIdx.x - joins;
+    const int chunks = static_cast<int>((a.max_len + kSimtThreads - 1) / kSimtThreads);
+    const int head = b / chunks, j0 = (b - head * chunks) * kSimtThreads;
+    const int seq = head / a.n_kv_heads;
+    const SeqInfo q = seq_info(a, seq);
+    const bool none = q.tiles == 0 || j0 >= q.len;
+    const Split w = split_of(a, units, p.ctas);
+    const int before = counted_before(a, w, units, seq);
+    pdl_wait();
+    if (none) return;
+    const int rows = a.group * q.n;
+    for (int r = warp; r < rows; r += kSimtWarps) {
+      const int unit = (head - seq * a.n_kv_heads) * p.row_blocks + r / kRows, row = r % kRows;
+      const Parts x = parts_of(w, before + unit * (q.tiles + w.pad) + w.pad, q.tiles);
+      float z;
+      if (x.n == 1) {
+        z = p.lse2[static_cast<size_t>(head) * a.group * a.T + r];
+      } else {
+        float M = -INFINITY, L = 0.f;
+        for (int i = lane; i < x.n; i += 32) M = fmaxf(M, part(x, i)[row]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        for (int i = lane; i < x.n; i += 32) {
+          const float mi = part(x, i)[row], li = part(x, i)[kRows + row];
+          L += mi == -INFINITY ? li : exp2f(mi - M) * li;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+        z = L > 0.f || L != L ? M + log2f(L) : -INFINITY;
+      }
+      if (lane == 0) s_z[r] = z == -INFINITY ? INFINITY : z;  // rows that see nothing add nothing
+    }
+    __syncthreads();
+    const int j = j0 + threadIdx.x;
+    if (j >= q.len) return;
+    const float2 *x =
+        reinterpret_cast<const float2 *>(p.x + (static_cast<size_t>(head) * p.x_len + j) * p.x_cols);
+    float sum = 0.f;
+    int r = 0;
+    for (; r + 1 < rows; r += 2) {
+      const float2 v = x[r >> 1];
+      sum += ex2(v.x - s_z[r]);
+      sum += ex2(v.y - s_z[r + 1]);
+    }
+    if (r < rows) sum += ex2(x[r >> 1].x - s_z[r]);
+    store_weight(a, head, j, q, sum);
+    return;
+  }
+  const int u = blockIdx.x / per_unit;
+  const int seq = u / units, unit = u - seq * units;
+  const int kvh = unit / p.row_blocks;
+  const int deal = kSimtWarps / p.join_rows;  // warps per row
+  const int row = (blockIdx.x - u * per_unit) * p.join_rows + warp / deal;
+  const int r = (unit - kvh * p.row_blocks) * kRows + row;
   const SeqInfo q = seq_info(a, seq);
-  const int j = blockIdx.x * kThreads + threadIdx.x;
-  if (q.tiles == 0 || static_cast<int>(blockIdx.x) * kThreads >= q.len) return;
-  const int rows = a.group * q.n;
-  if (threadIdx.x < rows) s_z[threadIdx.x] = p.lse2[head * a.group * a.T + threadIdx.x];
-  __syncthreads();
-  if (j >= q.len) return;
-  const float *x = p.x + (head * p.x_len + j) * p.x_cols;
-  float sum = 0.f;
-  for (int r = 0; r < rows; ++r)
-    if (s_z[r] != -INFINITY) sum += ex2(x[r] - s_z[r]);
-  store_weight(a, head, j, q, sum);
+  const Split w = split_of(a, units, p.ctas);
+  Parts x = {0, 0};
+  if (q.tiles > 0)
+    x = parts_of(w, counted_before(a, w, units, seq) + unit * (q.tiles + w.pad) + w.pad, q.tiles);
+  pdl_wait();
+  if (q.bad) {
+    if (threadIdx.x == 0) record_device_status(BKV_DEV_ASSERT, 611);
+    return;
+  }
+  if (x.n == 1) return;  // written by its CTA
+  const bool live = r < a.group * q.n;
+  float M = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+  if (live && x.n > 0) {
+    for (int i = lane; i < x.n; i += 32) M = fmaxf(M, part(x, i)[row]);
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
+#pragma unroll 4
+    for (int i = warp % deal; i < x.n; i += deal) {
+      const float *s = part(x, i);
+      const float mi = s[row], li = s[kRows + row];
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (lane * 4 < D) v = *reinterpret_cast<const float4 *>(s + 2 * kRows + row * D + lane * 4);
+      // a part without keys for this row is zeros; NaN logits leave it without a
+      // reference and with NaN sums, which have to stay
+      const float f = mi == -INFINITY ? 1.f : exp2f(mi - M);
+      l = fmaf(f, li, l);
+      o[0] = fmaf(f, v.x, o[0]), o[1] = fmaf(f, v.y, o[1]);
+      o[2] = fmaf(f, v.z, o[2]), o[3] = fmaf(f, v.w, o[3]);
+    }
+  }
+  if (deal > 1) {
+    if (lane * 4 < D)
+      *reinterpret_cast<float4 *>(&s_o[warp][lane * 4]) = make_float4(o[0], o[1], o[2], o[3]);
+    if (lane == 0) s_l[warp] = l;
+    __syncthreads();
+    if (warp % deal != 0) return;
+    for (int i = 1; i < deal; ++i) {
+      l += s_l[warp + i];
+      if (lane * 4 < D) {
+        const float4 v = *reinterpret_cast<const float4 *>(&s_o[warp + i][lane * 4]);
+        o[0] += v.x, o[1] += v.y, o[2] += v.z, o[3] += v.w;
+      }
+    }
+  }
+  if (!live) return;
+  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+  if (lane * 4 < D)
+    store_out4(static_cast<T *>(a.out) + q_row(a, seq, kvh, r) * D + lane * 4, o[0] * inv, o[1] * inv,
+               o[2] * inv, o[3] * inv);
+  if (lane == 0) store_lse(p, seq, kvh, r, M, l);
 }
 
 // From the keys again, for more query rows than logits are kept of.  A CTA
 // holds 128 keys' fragments and walks the query rows 32 at a time.
 template <int D>
-__global__ void __launch_bounds__(kThreads) weights_mma_kernel(const AttendArgs p) {
+__global__ void __launch_bounds__(kSimtThreads) weights_mma_kernel(const AttendArgs p) {
   constexpr int KS = D / 16, NT = 4;
   __shared__ uint2 s_q[NT * KS * 32];
   __shared__ float s_rs[NT * 8], s_z[NT * 8];
@@ -920,7 +1022,7 @@ __global__ void __launch_bounds__(kThreads) weights_mma_kernel(const AttendArgs 
   const SeqInfo q = seq_info(a, seq);
   if (q.tiles == 0 || static_cast<int>(blockIdx.x) * kTile >= q.len) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  const int j0 = blockIdx.x * kTile + warp * kKeys;
+  const int j0 = blockIdx.x * kTile + warp * kSimtKeys;
   const int rows = a.group * q.n;
   const int seen0 = q.len - q.n + 1;
   uint32_t ka[KS][4];
@@ -992,7 +1094,7 @@ __global__ void __launch_bounds__(kThreads) weights_mma_kernel(const AttendArgs 
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) weights_simt_kernel(const AttendArgs p) {
+__global__ void __launch_bounds__(kSimtThreads) weights_simt_kernel(const AttendArgs p) {
   __shared__ __align__(16) float s_q[kSimtRows * kMaxD];
   const Cache8AttendArgs &a = p.a;
   const int D = a.head_dim;
@@ -1008,7 +1110,7 @@ __global__ void __launch_bounds__(kThreads) weights_simt_kernel(const AttendArgs
   float sum = 0.f;
   for (int rb = 0; rb < rows; rb += kSimtRows) {
     __syncthreads();
-    for (int e = threadIdx.x; e < kSimtRows * D; e += kThreads) {
+    for (int e = threadIdx.x; e < kSimtRows * D; e += kSimtThreads) {
       const int r = rb + e / D;
       s_q[e] = r < rows ? load_q(static_cast<const T *>(a.q) + q_row(a, seq, kvh, r) * D + e % D) : 0.f;
     }
@@ -1031,17 +1133,32 @@ template <int D, int NT>
 bool run_mma(const AttendArgs &p, cudaStream_t s) {
   static int done[64];
   using Cfg = MmaCfg<D, NT>;
-  static_assert(Cfg::kSmem <= 227 * 1024, "shared memory");
+  static_assert(Cfg::kSmem <= 113 * 1024, "shared memory");
   if (!ensure_smem_limit(attend_mma_kernel<D, NT>, Cfg::kSmem, done)) return false;
   attend_mma_kernel<D, NT><<<p.ctas, kThreads, Cfg::kSmem, s>>>(p);
   return cudaGetLastError() == cudaSuccess;
 }
 
 template <int kRows, typename T>
-bool run_finish(const AttendArgs &p, cudaStream_t s) {
-  const unsigned grid = static_cast<unsigned>(p.a.n_seqs) * p.a.n_kv_heads * p.row_blocks * kRows;
-  attend_finish_kernel<kRows, T><<<grid, kThreads, 0, s>>>(p);
-  return cudaGetLastError() == cudaSuccess;
+bool run_finish(AttendArgs p, cudaStream_t s) {
+  const long long segments = static_cast<long long>(p.a.n_seqs) * p.a.n_kv_heads * p.row_blocks;
+  p.join_rows = segments >= kSms ? 8 : 1;
+  long long grid = segments * (kRows / p.join_rows);
+  if (p.x_cols > 0)
+    grid += static_cast<long long>(p.a.n_seqs) * p.a.n_kv_heads *
+            ((p.a.max_len + kSimtThreads - 1) / kSimtThreads);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kSimtThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, attend_finish_kernel<kRows, T>, p) == cudaSuccess) return true;
+  cudaGetLastError();
+  return false;
 }
 
 bool use_mma(int dtype, int head_dim) {
@@ -1055,10 +1172,10 @@ Cache8AttendPlan plan_cache8_attend(int n_seqs, int n_q_heads, int n_kv_heads, i
   Cache8AttendPlan p{};
   const long long rows = static_cast<long long>(n_q_heads / n_kv_heads) * T;
   const bool mma = use_mma(dtype, head_dim);
-  p.nt = !mma || rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+  p.nt = !mma || rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 24 ? 3 : 4;
   p.row_blocks = static_cast<int>((rows + 8 * p.nt - 1) / (8 * p.nt));
   const long long tiles = (max_len + kTile - 1) / kTile * n_seqs * n_kv_heads * p.row_blocks;
-  const int resident = mma ? kSms * (p.nt == 1 ? 2 : 1) : kSms * 2;
+  const int resident = 2 * kSms;
   p.ctas = static_cast<int>(std::min<long long>(tiles, resident));
   p.x_cols = weights && rows <= kMaxXRows ? static_cast<int>((rows + 1) / 2 * 2) : 0;
   const size_t part = static_cast<size_t>(p.ctas) * 2 * 8 * p.nt * (2 + head_dim) * 4;
@@ -1078,6 +1195,7 @@ bkv_status launch_cache8_attend(const Cache8AttendArgs &a, const Cache8AttendPla
   p.a = a;
   p.row_blocks = plan.row_blocks;
   p.ctas = plan.ctas;
+  p.log2_block = a.block == 16 ? 4 : a.block == 32 ? 5 : a.block == 64 ? 6 : 7;
   p.x_cols = plan.x_cols;
   p.x_len = static_cast<long long>(align_up(a.max_len, kKeys));
   uint8_t *w = static_cast<uint8_t *>(ws);
@@ -1094,30 +1212,31 @@ bkv_status launch_cache8_attend(const Cache8AttendArgs &a, const Cache8AttendPla
     else if (plan.nt == 2)
       ok = (wide ? run_mma<128, 2>(p, stream) : run_mma<64, 2>(p, stream)) &&
            run_finish<16, __nv_bfloat16>(p, stream);
+    else if (plan.nt == 3)
+      ok = (wide ? run_mma<128, 3>(p, stream) : run_mma<64, 3>(p, stream)) &&
+           run_finish<24, __nv_bfloat16>(p, stream);
     else
       ok = (wide ? run_mma<128, 4>(p, stream) : run_mma<64, 4>(p, stream)) &&
            run_finish<32, __nv_bfloat16>(p, stream);
   } else if (dtype == BKV_BF16) {
-    attend_simt_kernel<__nv_bfloat16><<<p.ctas, kThreads, 0, stream>>>(p);
+    attend_simt_kernel<__nv_bfloat16><<<p.ctas, kSimtThreads, 0, stream>>>(p);
     ok = cudaGetLastError() == cudaSuccess && run_finish<kSimtRows, __nv_bfloat16>(p, stream);
   } else {
-    attend_simt_kernel<float><<<p.ctas, kThreads, 0, stream>>>(p);
+    attend_simt_kernel<float><<<p.ctas, kSimtThreads, 0, stream>>>(p);
     ok = cudaGetLastError() == cudaSuccess && run_finish<kSimtRows, float>(p, stream);
   }
   if (!ok) return BKV_ERR_CUDA;
-  if (a.w_out) {
+  if (a.w_out && plan.x_cols == 0) {
     const unsigned heads = static_cast<unsigned>(a.n_seqs) * a.n_kv_heads;
     const unsigned tiles = static_cast<unsigned>((a.max_len + kTile - 1) / kTile);
-    if (plan.x_cols > 0)
-      weights_kept_kernel<<<dim3((a.max_len + kThreads - 1) / kThreads, heads), kThreads, 0, stream>>>(p);
-    else if (mma && a.head_dim == 128)
-      weights_mma_kernel<128><<<dim3(tiles, heads), kThreads, 0, stream>>>(p);
+    if (mma && a.head_dim == 128)
+      weights_mma_kernel<128><<<dim3(tiles, heads), kSimtThreads, 0, stream>>>(p);
     else if (mma)
-      weights_mma_kernel<64><<<dim3(tiles, heads), kThreads, 0, stream>>>(p);
+      weights_mma_kernel<64><<<dim3(tiles, heads), kSimtThreads, 0, stream>>>(p);
     else if (dtype == BKV_BF16)
-      weights_simt_kernel<__nv_bfloat16><<<dim3(tiles, heads), kThreads, 0, stream>>>(p);
+      weights_simt_kernel<__nv_bfloat16><<<dim3(tiles, heads), kSimtThreads, 0, stream>>>(p);
     else
-      weights_simt_kernel<float><<<dim3(tiles, heads), kThreads, 0, stream>>>(p);
+      weights_simt_kernel<float><<<dim3(tiles, heads), kSimtThreads, 0, stream>>>(p);
     if (cudaGetLastError() != cudaSuccess) return BKV_ERR_CUDA;
   }
   return BKV_OK;
