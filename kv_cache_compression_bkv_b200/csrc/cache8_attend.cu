@@ -63,6 +63,7 @@ constexpr int kMaxXRows = 32;  // query rows per KV head whose logits are kept f
 struct AttendArgs {
   Cache8AttendArgs a;
   int row_blocks, ctas, x_cols, log2_block, join_rows;
+  int w_keys, w_chunks;  // keys per weights CTA, and its CTAs per (sequence, KV head)
   long long x_len;   // keys per (sequence, KV head) in x
   float *part;       // [ctas][2][rows][2 + head_dim]: max, sum, output
   float *lse2;       // [n_seqs][n_kv_heads][group * T], log2 units
@@ -107,13 +108,15 @@ struct Split {
   int total, run, pad;  // counted tiles, counted tiles per run
 };
 
-// Called by whole warps.
 __device__ __forceinline__ int warp_sum(int x) {
   return static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(x)));
 }
-__device__ __forceinline__ Split split_of(const Cache8AttendArgs &a, int units, int ctas) {
-  int tiles = 0, segments = 0;
-  for (int s = threadIdx.x & 31; s < a.n_seqs; s += 32) {
+// Called by whole warps.  mine: the tiles of sequence `lane`, for the calls below.
+__device__ __forceinline__ Split split_of(const Cache8AttendArgs &a, int units, int ctas, int *mine) {
+  const int lane = threadIdx.x & 31;
+  *mine = lane < a.n_seqs ? seq_info(a, lane).tiles : 0;
+  int tiles = *mine, segments = *mine > 0 ? 1 : 0;
+  for (int s = lane + 32; s < a.n_seqs; s += 32) {
     const int t = seq_info(a, s).tiles;
     tiles += t;
     segments += t > 0 ? 1 : 0;
@@ -128,9 +131,10 @@ __device__ __forceinline__ Split split_of(const Cache8AttendArgs &a, int units, 
 }
 // Counted tiles before sequence `seq`.
 __device__ __forceinline__ int counted_before(const Cache8AttendArgs &a, const Split &w, int units,
-                                              int seq) {
-  int sum = 0;
-  for (int s = threadIdx.x & 31; s < seq; s += 32) {
+                                              int mine, int seq) {
+  const int lane = threadIdx.x & 31;
+  int sum = lane < seq && mine > 0 ? mine + w.pad : 0;
+  for (int s = lane + 32; s < seq; s += 32) {
     const int t = seq_info(a, s).tiles;
     sum += t > 0 ? t + w.pad : 0;
   }
@@ -144,11 +148,12 @@ struct Cursor {
   SeqInfo q;
 
   // Called by whole warps: the first tile at counted tile x (x < total) or after it.
-  __device__ __forceinline__ void seek(const Cache8AttendArgs &a, const Split &w, int units, int x) {
+  __device__ __forceinline__ void seek(const Cache8AttendArgs &a, const Split &w, int units,
+                                       int mine, int x) {
     const int lane = threadIdx.x & 31;
     int before = 0;
     for (int s0 = 0;; s0 += 32) {
-      int t = s0 + lane < a.n_seqs ? seq_info(a, s0 + lane).tiles : 0;
+      int t = s0 == 0 ? mine : s0 + lane < a.n_seqs ? seq_info(a, s0 + lane).tiles : 0;
       t = t > 0 ? (t + w.pad) * units : 0;
       int sum = t;
 #pragma unroll
@@ -284,26 +289,39 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
 }
 
-// The f16 B fragments of one query row n = lane / 4 for every k-step: lane
-// c = lane % 4 holds the elements of 16-byte code chunks c and c + 4, the four
-// of word w in k-step w (chunk c) or 4 + w (chunk c + 4).  Returns the row's
-// factor: f16 value * factor = q * scale * log2(e).
+// A lane's part of query row r (n = lane / 4 of an n-tile): the elements of the
+// 16-byte code chunks c and c + 4 (c = lane % 4).
 template <int D>
-__device__ __forceinline__ float load_q_frags(const AttendArgs &p, int seq, int kvh, int r, int rows,
-                                              uint2 (&f)[D / 16]) {
+struct RawQ {
+  uint4 v[D / 64][2];
+};
+template <int D>
+__device__ __forceinline__ void load_q_raw(const AttendArgs &p, int seq, int kvh, int r, int rows,
+                                           RawQ<D> &q) {
   const int c = threadIdx.x & 3;
-  uint4 raw[D / 64][2];
+#pragma unroll
+  for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      q.v[h][i] = make_uint4(0, 0, 0, 0);
+      if (r < rows)
+        q.v[h][i] = __ldg(reinterpret_cast<const uint4 *>(
+                              static_cast<const __nv_bfloat16 *>(p.a.q) +
+                              q_row(p.a, seq, kvh, r) * D + (c + 4 * h) * 16) + i);
+    }
+}
+
+// The f16 B fragments of the rows for every k-step: word w of chunk c goes to
+// k-step w, of chunk c + 4 to k-step 4 + w.  Returns the row's factor:
+// f16 value * factor = q * scale * log2(e).
+template <int D>
+__device__ __forceinline__ float q_frags(const AttendArgs &p, const RawQ<D> &q, uint2 (&f)[D / 16]) {
   uint32_t amax = 0;
 #pragma unroll
   for (int h = 0; h < D / 64; ++h)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      raw[h][i] = make_uint4(0, 0, 0, 0);
-      if (r < rows)
-        raw[h][i] = __ldg(reinterpret_cast<const uint4 *>(
-                              static_cast<const __nv_bfloat16 *>(p.a.q) +
-                              q_row(p.a, seq, kvh, r) * D + (c + 4 * h) * 16) + i);
-      const uint32_t w[4] = {raw[h][i].x, raw[h][i].y, raw[h][i].z, raw[h][i].w};
+      const uint32_t w[4] = {q.v[h][i].x, q.v[h][i].y, q.v[h][i].z, q.v[h][i].w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const uint32_t lo = (w[k] & 0x7fffu) << 16, hi = w[k] & 0x7fff0000u;
@@ -320,7 +338,7 @@ __device__ __forceinline__ float load_q_frags(const AttendArgs &p, int seq, int 
   for (int h = 0; h < D / 64; ++h)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const uint32_t w[4] = {raw[h][i].x, raw[h][i].y, raw[h][i].z, raw[h][i].w};
+      const uint32_t w[4] = {q.v[h][i].x, q.v[h][i].y, q.v[h][i].z, q.v[h][i].w};
       uint32_t y[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k)
@@ -362,7 +380,8 @@ __global__ void __launch_bounds__(kThreads, 2) attend_mma_kernel(const AttendArg
   const int g = lane >> 2, c = lane & 3;
   const int units = a.n_kv_heads * p.row_blocks;
   pdl_launch_dependents();
-  const Split w = split_of(a, units, p.ctas);
+  int mine;
+  const Split w = split_of(a, units, p.ctas, &mine);
   const int t0 = blockIdx.x * w.run;
   if (t0 >= w.total) return;
   const int run = min(w.run, w.total - t0);
@@ -378,8 +397,16 @@ __global__ void __launch_bounds__(kThreads, 2) attend_mma_kernel(const AttendArg
   const uint32_t k_dst = lrow * D + (D == 128 ? lch ^ ((lrow & 1) << 2) : lch) * 16;
   const uint32_t v_dst0 = kKeys * D + lrow * D + (D == 128 ? lch ^ lrow : lch ^ ((lrow >> 1) & 3)) * 16;
   Cursor load, cur;
-  cur.seek(a, w, units, t0);
+  cur.seek(a, w, units, mine, t0);
   load = cur;
+  // the first segment's queries, ahead of the stream of codes
+  RawQ<D> first_q;
+  const int first_at = cur.at;
+  if constexpr (NT == 1) {
+    const int kvh = cur.unit / p.row_blocks;
+    load_q_raw<D>(p, cur.seq, kvh, (cur.unit - kvh * p.row_blocks) * Cfg::kRows + g,
+                  a.group * cur.q.n, first_q);
+  }
   int load_unit = -1, load_seq = -1;
   const uint8_t *k_src = nullptr, *v_src = nullptr;
   const float *sc_src = nullptr;
@@ -437,13 +464,16 @@ __global__ void __launch_bounds__(kThreads, 2) attend_mma_kernel(const AttendArg
       seen0 = cur.q.len - cur.q.n + 1;  // keys that token 0 sees
       const int rows = a.group * cur.q.n;
       if constexpr (NT == 1) {
-        const float f = load_q_frags<D>(p, cur.seq, kvh, r0 + g, rows, qf);
+        if (cur.at != first_at) load_q_raw<D>(p, cur.seq, kvh, r0 + g, rows, first_q);
+        const float f = q_frags<D>(p, first_q, qf);
         rs[0][0] = __shfl_sync(0xffffffffu, f, (2 * c) * 4);
         rs[0][1] = __shfl_sync(0xffffffffu, f, (2 * c + 1) * 4);
       } else {
         if (warp < NT) {
           uint2 f[KS];
-          const float r = load_q_frags<D>(p, cur.seq, kvh, r0 + warp * 8 + g, rows, f);
+          RawQ<D> raw;
+          load_q_raw<D>(p, cur.seq, kvh, r0 + warp * 8 + g, rows, raw);
+          const float r = q_frags<D>(p, raw, f);
 #pragma unroll
           for (int s = 0; s < KS; ++s) s_q[(warp * KS + s) * 32 + lane] = f[s];
           if (c == 0) s_rs[warp * 8 + g] = r;
@@ -734,12 +764,13 @@ __global__ void __launch_bounds__(kSimtThreads) attend_simt_kernel(const AttendA
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int units = a.n_kv_heads * p.row_blocks;
   pdl_launch_dependents();
-  const Split w = split_of(a, units, p.ctas);
+  int mine;
+  const Split w = split_of(a, units, p.ctas, &mine);
   const int t0 = blockIdx.x * w.run;
   if (t0 >= w.total) return;
   const int run = min(w.run, w.total - t0);
   Cursor cur;
-  cur.seek(a, w, units, t0);
+  cur.seek(a, w, units, mine, t0);
   int seg_tiles = 0;
   float o[kSimtRows][4], m[kSimtRows], l[kSimtRows];
   bool fresh = true;
@@ -879,7 +910,7 @@ __device__ __forceinline__ Parts parts_of(const Split &w, int first, int tiles) 
 // keys.  A row's parts are dealt to its warps in turn and the warps' sums added
 // in order, so results do not depend on timing.
 // Then, where the attention kernel kept its logits, the CTAs of the weights:
-// one per 256 keys of a (sequence, KV head), which need the rows' lse and so
+// one per p.w_keys keys of a (sequence, KV head), which need the rows' lse and so
 // join the parts' statistics for themselves.
 // Launched while the attention kernel runs: everything before the wait reads
 // only the lengths, and every CTA waits, so that this kernel never ends first.
@@ -902,13 +933,13 @@ __global__ void __launch_bounds__(kSimtThreads) attend_finish_kernel(const Atten
   };
   if (static_cast<int>(blockIdx.x) >= joins) {
     const int b = blockIdx.x - joins;
-    const int chunks = static_cast<int>((a.max_len + kSimtThreads - 1) / kSimtThreads);
-    const int head = b / chunks, j0 = (b - head * chunks) * kSimtThreads;
+    const int head = b / p.w_chunks, j0 = (b - head * p.w_chunks) * p.w_keys;
     const int seq = head / a.n_kv_heads;
     const SeqInfo q = seq_info(a, seq);
     const bool none = q.tiles == 0 || j0 >= q.len;
-    const Split w = split_of(a, units, p.ctas);
-    const int before = counted_before(a, w, units, seq);
+    int mine;
+    const Split w = split_of(a, units, p.ctas, &mine);
+    const int before = counted_before(a, w, units, mine, seq);
     pdl_wait();
     if (none) return;
     const int rows = a.group * q.n;
@@ -934,19 +965,20 @@ __global__ void __launch_bounds__(kSimtThreads) attend_finish_kernel(const Atten
       if (lane == 0) s_z[r] = z == -INFINITY ? INFINITY : z;  // rows that see nothing add nothing
     }
     __syncthreads();
-    const int j = j0 + threadIdx.x;
-    if (j >= q.len) return;
-    const float2 *x =
-        reinterpret_cast<const float2 *>(p.x + (static_cast<size_t>(head) * p.x_len + j) * p.x_cols);
-    float sum = 0.f;
-    int r = 0;
-    for (; r + 1 < rows; r += 2) {
-      const float2 v = x[r >> 1];
-      sum += ex2(v.x - s_z[r]);
-      sum += ex2(v.y - s_z[r + 1]);
+    const int j1 = min(j0 + p.w_keys, q.len);
+    for (int j = j0 + threadIdx.x; j < j1; j += kSimtThreads) {
+      const float2 *x = reinterpret_cast<const float2 *>(
+          p.x + (static_cast<size_t>(head) * p.x_len + j) * p.x_cols);
+      float sum = 0.f;
+      int r = 0;
+      for (; r + 1 < rows; r += 2) {
+        const float2 v = x[r >> 1];
+        sum += ex2(v.x - s_z[r]);
+        sum += ex2(v.y - s_z[r + 1]);
+      }
+      if (r < rows) sum += ex2(x[r >> 1].x - s_z[r]);
+      store_weight(a, head, j, q, sum);
     }
-    if (r < rows) sum += ex2(x[r >> 1].x - s_z[r]);
-    store_weight(a, head, j, q, sum);
     return;
   }
   const int u = blockIdx.x / per_unit;
@@ -956,10 +988,11 @@ __global__ void __launch_bounds__(kSimtThreads) attend_finish_kernel(const Atten
   const int row = (blockIdx.x - u * per_unit) * p.join_rows + warp / deal;
   const int r = (unit - kvh * p.row_blocks) * kRows + row;
   const SeqInfo q = seq_info(a, seq);
-  const Split w = split_of(a, units, p.ctas);
+  int mine;
+  const Split w = split_of(a, units, p.ctas, &mine);
   Parts x = {0, 0};
   if (q.tiles > 0)
-    x = parts_of(w, counted_before(a, w, units, seq) + unit * (q.tiles + w.pad) + w.pad, q.tiles);
+    x = parts_of(w, counted_before(a, w, units, mine, seq) + unit * (q.tiles + w.pad) + w.pad, q.tiles);
   pdl_wait();
   if (q.bad) {
     if (threadIdx.x == 0) record_device_status(BKV_DEV_ASSERT, 611);
@@ -1054,7 +1087,9 @@ __global__ void __launch_bounds__(kSimtThreads) weights_mma_kernel(const AttendA
     __syncthreads();
     if (warp < NT) {
       uint2 f[KS];
-      const float s = load_q_frags<D>(p, seq, kvh, rb + warp * 8 + g, rows, f);
+      RawQ<D> raw;
+      load_q_raw<D>(p, seq, kvh, rb + warp * 8 + g, rows, raw);
+      const float s = q_frags<D>(p, raw, f);
 #pragma unroll
       for (int k = 0; k < KS; ++k) s_q[(warp * KS + k) * 32 + lane] = f[k];
       if (c == 0) {
@@ -1144,9 +1179,15 @@ bool run_finish(AttendArgs p, cudaStream_t s) {
   const long long segments = static_cast<long long>(p.a.n_seqs) * p.a.n_kv_heads * p.row_blocks;
   p.join_rows = segments >= kSms ? 8 : 1;
   long long grid = segments * (kRows / p.join_rows);
-  if (p.x_cols > 0)
-    grid += static_cast<long long>(p.a.n_seqs) * p.a.n_kv_heads *
-            ((p.a.max_len + kSimtThreads - 1) / kSimtThreads);
+  if (p.x_cols > 0) {
+    // about four CTAs an SM: the lse of a CTA's rows cost it as much as some
+    // hundreds of keys
+    const long long heads = static_cast<long long>(p.a.n_seqs) * p.a.n_kv_heads;
+    const long long keys = (heads * p.a.max_len / (4 * kSms) + kSimtThreads) / kSimtThreads;
+    p.w_keys = kSimtThreads * static_cast<int>(std::min<long long>(keys, 64));
+    p.w_chunks = static_cast<int>((p.a.max_len + p.w_keys - 1) / p.w_keys);
+    grid += heads * p.w_chunks;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(kSimtThreads);
