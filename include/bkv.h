@@ -315,8 +315,8 @@ bkv_status bkv_score_noalloc(const bkv_cache_desc *desc, const void *k,
  *
  * Supported: dtype (of new rows, queries and outputs) bf16 or f32, head_dim a
  * multiple of 16 up to 128, block 16, 32, 64 or 128, capacity a multiple of
- * block, n_seqs * n_kv_heads at most 65535.  Codes, new rows, queries and
- * outputs are 16-byte aligned, the rest 4-byte.  Attention uses the tensor
+ * block, n_seqs * n_kv_heads at most 65535.  Codes, new rows, queries,
+ * outputs and weights are 16-byte aligned, the rest 4-byte.  Attention uses the tensor
  * cores for bf16 with head_dim 64 or 128 and the CUDA cores otherwise. */
 typedef struct {
   int32_t n_seqs;

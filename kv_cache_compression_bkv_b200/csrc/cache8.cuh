@@ -61,26 +61,24 @@ __device__ __forceinline__ __half2 as_half2(uint32_t x) {
 }
 __device__ __forceinline__ uint32_t as_u32(__half2 x) { return *reinterpret_cast<uint32_t *>(&x); }
 
-// Four codes moved from one block's scale to another's, multiplied by 2^k
-// (k = old exponent - new exponent).  In f16 the product is exact down to
-// 2^-21, far below the 2^-10 under which e4m3 rounds to zero; k > 15 takes a
-// second factor (a small old code under a far smaller new scale).
-__device__ __forceinline__ uint32_t rescale4(uint32_t codes, __half2 f1, __half2 f2) {
-  const uint32_t lo = as_u32(__hmul2(__hmul2(as_half2(e4m3x2_to_f16x2(codes)), f1), f2));
-  const uint32_t hi = as_u32(__hmul2(__hmul2(as_half2(e4m3x2_to_f16x2(codes >> 16)), f1), f2));
+// Codes moved from one block's scale to another's, multiplied by 2^k (k = old
+// exponent - new exponent).  In f16 the product is exact down to 2^-21, far
+// below the 2^-10 under which e4m3 rounds to zero.  2^15 is f16's largest power:
+// k > 15 (a small old code under a far smaller new scale) takes a second factor.
+__device__ __forceinline__ uint32_t rescale4(uint32_t codes, __half2 f) {
+  const uint32_t lo = as_u32(__hmul2(as_half2(e4m3x2_to_f16x2(codes)), f));
+  const uint32_t hi = as_u32(__hmul2(as_half2(e4m3x2_to_f16x2(codes >> 16)), f));
   return f16x2_to_e4m3x2(lo) | (f16x2_to_e4m3x2(hi) << 16);
 }
-__device__ __forceinline__ void rescale_factors(int k, __half2 *f1, __half2 *f2) {
-  k = max(-24, min(k, 24));  // below 2^-24 every code becomes zero
-  const int a = max(-12, min(k, 12));
-  *f1 = __float2half2_rn(pow2f(a));
-  *f2 = __float2half2_rn(pow2f(k - a));
-}
 __device__ __forceinline__ uint4 rescale16(uint4 c, int k) {
-  __half2 f1, f2;
-  rescale_factors(k, &f1, &f2);
-  return make_uint4(rescale4(c.x, f1, f2), rescale4(c.y, f1, f2), rescale4(c.z, f1, f2),
-                    rescale4(c.w, f1, f2));
+  if (k > 15) {  // at most 17: from 2^-9 to 2^8
+    const __half2 f = __float2half2_rn(pow2f(min(k, 24) - 9));
+    c = make_uint4(rescale4(c.x, f), rescale4(c.y, f), rescale4(c.z, f), rescale4(c.w, f));
+    k = 9;
+  }
+  // below 2^-24 every code becomes zero
+  const __half2 f = __float2half2_rn(pow2f(max(k, -24)));
+  return make_uint4(rescale4(c.x, f), rescale4(c.y, f), rescale4(c.z, f), rescale4(c.w, f));
 }
 
 __device__ __forceinline__ __half2 absmax4(uint32_t codes, __half2 m) {

@@ -154,7 +154,7 @@ bkv_status bkv_cache8_attend(const bkv_cache8_desc *desc, const void *k8, const 
   if (!q || !out || max_len < 1 || max_len > desc->capacity || !rows_fit(desc, T, max_len))
     return BKV_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(n_new, 4) || !aligned(lse, 4) ||
-      !aligned(weights_in, 4) || !aligned(weights_out, 4))
+      !aligned(weights_in, 16) || !aligned(weights_out, 16))
     return BKV_ERR_INVALID_ARG;
   if (!std::isfinite(scale) || scale < 0.f || !std::isfinite(decay) ||
       (weights_in && !weights_out))
@@ -213,7 +213,7 @@ bkv_status bkv_cache8_evict(const bkv_cache8_desc *desc, const void *k8, const v
   if (dst->n_seqs != desc->n_seqs || dst->n_kv_heads != desc->n_kv_heads ||
       dst->head_dim != desc->head_dim || dst->block != desc->block)
     return BKV_ERR_INVALID_ARG;
-  if (!weights || !aligned(weights, 4) || !aligned(weights_dst, 4) || !aligned(idx, 4) ||
+  if (!weights || !aligned(weights, 16) || !aligned(weights_dst, 16) || !aligned(idx, 4) ||
       !aligned(new_lens, 4))
     return BKV_ERR_INVALID_ARG;
   if (max_len < 1 || max_len > desc->capacity || K < 1 || K > kMaxRows || sink < 0 || recent < 0 ||

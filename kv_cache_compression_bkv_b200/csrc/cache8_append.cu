@@ -24,42 +24,75 @@ namespace {
 using namespace cache8;
 
 constexpr int kMaxThreads = 256;
-constexpr int kPieces = 4;  // 16-element pieces per thread: 128 rows x 128 / 16 / 256
 
-// 16 elements as floats
-__device__ __forceinline__ void load16(const float *p, float (&v)[16]) {
+// 16 elements as they are stored, and as floats
+template <typename T>
+struct Piece;
+template <>
+struct Piece<float> {
+  float4 v[4];
+  __device__ __forceinline__ void load(const float *p) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 x = __ldcs(reinterpret_cast<const float4 *>(p) + i);
-    v[4 * i] = x.x, v[4 * i + 1] = x.y, v[4 * i + 2] = x.z, v[4 * i + 3] = x.w;
+    for (int i = 0; i < 4; ++i) v[i] = __ldcs(reinterpret_cast<const float4 *>(p) + i);
   }
-}
-__device__ __forceinline__ void load16(const __nv_bfloat16 *p, float (&v)[16]) {
+  __device__ __forceinline__ float at(int i) const {
+    const float4 x = v[i >> 2];
+    return (i & 3) == 0 ? x.x : (i & 3) == 1 ? x.y : (i & 3) == 2 ? x.z : x.w;
+  }
+  // the bits of the largest |x| among the finite elements; *odd: some are not finite
+  __device__ __forceinline__ uint32_t amax(bool *odd) const {
+    uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint4 x = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t b = __float_as_uint(at(i)) & 0x7fffffffu;
+      if (b < 0x7f800000u) m = max(m, b); else *odd = true;
+    }
+    return m;
+  }
+};
+template <>
+struct Piece<__nv_bfloat16> {
+  uint32_t v[8];
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      v[8 * i + 2 * k] = __uint_as_float(w[k] << 16);
-      v[8 * i + 2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+    for (int i = 0; i < 2; ++i) {
+      const uint4 x = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
+      v[4 * i] = x.x, v[4 * i + 1] = x.y, v[4 * i + 2] = x.z, v[4 * i + 3] = x.w;
     }
   }
-}
-
-// the bits of |x|, 0 for infinities and NaN (which do not set the scale)
-__device__ __forceinline__ uint32_t finite_abs_bits(float x) {
-  const uint32_t b = __float_as_uint(x) & 0x7fffffffu;
-  return b < 0x7f800000u ? b : 0u;
-}
+  __device__ __forceinline__ float at(int i) const {
+    return __uint_as_float(i & 1 ? v[i >> 1] & 0xffff0000u : v[i >> 1] << 16);
+  }
+  __device__ __forceinline__ uint32_t amax(bool *odd) const {
+    // two elements at a time; infinities and NaN are the largest, so only
+    // where one turns up are the elements looked at one by one
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = __vmaxu2(m, v[i] & 0x7fff7fffu);
+    m = max(m & 0xffffu, m >> 16);
+    if (m >= 0x7f80u) {
+      *odd = true;
+      m = 0;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t b = (i & 1 ? v[i >> 1] >> 16 : v[i >> 1]) & 0x7fffu;
+        if (b < 0x7f80u) m = max(m, b);
+      }
+    }
+    return m << 16;
+  }
+};
 
 // A value that is not finite becomes a NaN code.
-__device__ __forceinline__ float storable(float x, float inv) {
-  const bool finite = (__float_as_uint(x) & 0x7fffffffu) < 0x7f800000u;
-  return finite ? x * inv : __uint_as_float(0x7fc00000u);
+__device__ __forceinline__ float storable(float x, float inv, bool odd) {
+  const float y = x * inv;
+  if (odd && (__float_as_uint(x) & 0x7fffffffu) >= 0x7f800000u) return __uint_as_float(0x7fc00000u);
+  return y;
 }
 
-template <typename T>
+// kPieces: 16-element pieces per thread, as few as the sizes allow, so that
+// more CTAs are resident and more loads in flight.
+template <typename T, int kPieces>
 __global__ void __launch_bounds__(kMaxThreads) append_kernel(const Cache8AppendArgs a) {
   __shared__ uint32_t s_max[kMaxThreads / 32];
   unsigned u = blockIdx.x;
@@ -88,17 +121,17 @@ __global__ void __launch_bounds__(kMaxThreads) append_kernel(const Cache8AppendA
                  (head * a.T + (r0 - first)) * static_cast<size_t>(a.head_dim);
   const float was = r0 > base ? *scale : 0.f;
   const int pieces = (r1 - r0) * pr;
-  float v[kPieces][16];
+  Piece<T> v[kPieces];
   uint32_t amax = 0;
+  bool odd = false;
 #pragma unroll
   for (int i = 0; i < kPieces; ++i) {
     const int p = threadIdx.x + i * blockDim.x;
-    if (p < pieces) {
-      load16(src + static_cast<size_t>(p) * 16, v[i]);
-#pragma unroll
-      for (int k = 0; k < 16; ++k) amax = max(amax, finite_abs_bits(v[i][k]));
-    }
+    if (p < pieces) v[i].load(src + static_cast<size_t>(p) * 16);
   }
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i)
+    if (static_cast<int>(threadIdx.x + i * blockDim.x) < pieces) amax = max(amax, v[i].amax(&odd));
   amax = __reduce_max_sync(0xffffffffu, amax);
   if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = amax;
   __syncthreads();
@@ -116,8 +149,9 @@ __global__ void __launch_bounds__(kMaxThreads) append_kernel(const Cache8AppendA
       uint32_t w[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        w[k] = to_e4m3x2(storable(v[i][4 * k], inv), storable(v[i][4 * k + 1], inv)) |
-               (to_e4m3x2(storable(v[i][4 * k + 2], inv), storable(v[i][4 * k + 3], inv)) << 16);
+        w[k] = to_e4m3x2(storable(v[i].at(4 * k), inv, odd), storable(v[i].at(4 * k + 1), inv, odd)) |
+               (to_e4m3x2(storable(v[i].at(4 * k + 2), inv, odd),
+                          storable(v[i].at(4 * k + 3), inv, odd)) << 16);
       reinterpret_cast<uint4 *>(codes)[static_cast<size_t>(r0 - base) * pr + p] =
           make_uint4(w[0], w[1], w[2], w[3]);
     }
@@ -138,14 +172,22 @@ bkv_status launch_cache8_append(const Cache8AppendArgs &a, int dtype, cudaStream
   if (injected_launch_failure()) return BKV_ERR_CUDA;
   const long long ctas = 2LL * a.n_seqs * a.n_kv_heads * a.blocks_per_seq;
   if (ctas > INT32_MAX) return BKV_ERR_INVALID_ARG;
-  // a thread holds at most kPieces pieces; 128 threads at least, so that older
-  // rows that have to move to a larger scale move quickly
+  // 128 threads at least, so that older rows that have to move to a larger
+  // scale move quickly; up to 128 rows x 128 / 16 = 1024 pieces
   const int pieces = std::min(a.T, a.block) * a.head_dim / 16;
   const int threads = std::min(kMaxThreads, std::max(128, (pieces + 31) / 32 * 32));
+  const int per = (pieces + threads - 1) / threads;
+  auto launch = [&](auto kernel) {
+    kernel<<<static_cast<unsigned>(ctas), threads, 0, stream>>>(a);
+  };
   if (dtype == BKV_BF16)
-    append_kernel<__nv_bfloat16><<<static_cast<unsigned>(ctas), threads, 0, stream>>>(a);
+    per == 1   ? launch(append_kernel<__nv_bfloat16, 1>)
+    : per == 2 ? launch(append_kernel<__nv_bfloat16, 2>)
+               : launch(append_kernel<__nv_bfloat16, 4>);
   else
-    append_kernel<float><<<static_cast<unsigned>(ctas), threads, 0, stream>>>(a);
+    per == 1   ? launch(append_kernel<float, 1>)
+    : per == 2 ? launch(append_kernel<float, 2>)
+               : launch(append_kernel<float, 4>);
   return cudaGetLastError() == cudaSuccess ? BKV_OK : BKV_ERR_CUDA;
 }
 

@@ -13,7 +13,7 @@
 // mask words, and the kept positions are written in ascending order at the
 // words' prefix offsets.
 //
-// Compaction: a CTA takes 128 new rows of one (sequence, head, K or V), which
+// Compaction: a CTA takes 128 new rows of one (sequence, head), K and V, which
 // are whole blocks of the new cache.  It gathers the rows' codes and old
 // scales, reduces each new block's largest magnitude (exact: a code times a
 // power of two), takes the scale that the append would take, moves the codes
@@ -42,7 +42,7 @@ constexpr int kSelThreads = 1024;
 constexpr int kBins = 2048;
 constexpr int kStageMax = 45056;  // positions whose weights fit in shared memory
 // mask words per thread: positions up to kSelThreads * 32 * kWordsMax
-constexpr int kMaskWords(long long L) { return static_cast<int>((L + 31) / 32); }
+constexpr int kMaskWords(long long L) { return static_cast<int>((L + 127) / 128 * 4); }
 
 // NaN ranks below every number
 __device__ __forceinline__ uint32_t rank_key(float w) { return w != w ? 0u : order_key(w); }
@@ -113,17 +113,35 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Cache8E
       const int bits = pass == 2 ? 10 : 11;
       for (int b = tid; b < kBins; b += kSelThreads) s_hist[b] = 0;
       __syncthreads();
-      if (pass == 0 && kStaged) {
-        for (int j = tid; j < L; j += kSelThreads) {
-          const uint32_t k = rank_key(__ldg(w + j));
-          s_key[j] = k;
-          if (j >= lo && j < hi) atomicAdd(&s_hist[k >> 21], 1u);
+      // four positions a thread and step, kBatch steps' loads in flight; a row
+      // is 16-byte aligned and allocated to a multiple of 16 positions
+      constexpr int kBatch = 4;
+      const int quads = (L + 3) >> 2;
+      for (int q0 = tid; q0 < quads; q0 += kBatch * kSelThreads) {
+        uint4 k[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          const int q = q0 + u * kSelThreads;
+          if (q >= quads) continue;
+          if (kStaged && pass > 0) {
+            k[u] = reinterpret_cast<const uint4 *>(s_key)[q];
+          } else {
+            const float4 f = __ldg(reinterpret_cast<const float4 *>(w) + q);
+            k[u] = make_uint4(rank_key(f.x), rank_key(f.y), rank_key(f.z), rank_key(f.w));
+            if (kStaged) reinterpret_cast<uint4 *>(s_key)[q] = k[u];
+          }
         }
-      } else {
-        for (int j = lo + tid; j < hi; j += kSelThreads) {
-          const uint32_t k = key_at(j);
-          if (pass == 0 || (k >> (shift + bits)) == prefix)
-            atomicAdd(&s_hist[(k >> shift) & ((1u << bits) - 1)], 1u);
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          const int q = q0 + u * kSelThreads;
+          if (q >= quads) continue;
+          const uint32_t v[4] = {k[u].x, k[u].y, k[u].z, k[u].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int j = 4 * q + i;
+            if (j >= lo && j < hi && (pass == 0 || (v[i] >> (shift + bits)) == prefix))
+              atomicAdd(&s_hist[(v[i] >> shift) & ((1u << bits) - 1)], 1u);
+          }
         }
       }
       __syncthreads();
@@ -193,28 +211,28 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Cache8E
 
 constexpr int kRows = 128;     // new rows per CTA and round
 constexpr int kThreads = 256;
-constexpr int kPieces = 4;     // 16-byte pieces per thread: 128 rows x 8 / 256
+constexpr int kPieces = 4;     // 16-byte pieces of K, and of V, per thread: 128 rows x 8 / 256
 
-template <bool kInPlace>
+// kPr: 16-byte pieces per row when it is a power of two (8, 4), 0: any number.
+template <bool kInPlace, int kPr>
 __global__ void __launch_bounds__(kThreads) evict_compact_kernel(const Cache8EvictArgs a) {
   __shared__ int32_t s_idx[kRows];
-  __shared__ int s_exp[kRows];           // the rows' old scale exponents
-  __shared__ uint32_t s_max[kRows / 16]; // per new block: bits of the largest magnitude
+  __shared__ int s_exp[2][kRows];           // the rows' old scale exponents (K, V)
+  __shared__ uint32_t s_max[2][kRows / 16]; // per new block: bits of the largest magnitude
   const int tid = threadIdx.x;
-  unsigned u = blockIdx.x;
-  const int part = u % a.ctas_per_head;  // in place: the rank in the cluster
-  u /= a.ctas_per_head;
-  const int kv = u & 1;
-  const int head = u >> 1, seq = head / a.n_kv_heads;
+  const int head = blockIdx.x / a.ctas_per_head;
+  const int part = blockIdx.x - head * a.ctas_per_head;  // in place: the rank in the cluster
+  const int seq = head / a.n_kv_heads;
   const int n = a.kept[seq];
-  if (kv == 0 && part == 0 && tid == 0 && head % a.n_kv_heads == 0 && n >= 0 && a.new_lens)
+  if (part == 0 && tid == 0 && head - seq * a.n_kv_heads == 0 && n >= 0 && a.new_lens)
     a.new_lens[seq] = n;
-  const int pr = a.head_dim >> 4;
-  const int block = a.block;
-  const uint8_t *src = (kv ? a.v8 : a.k8) + static_cast<size_t>(head) * a.cap * a.head_dim;
-  const float *src_scale = (kv ? a.v_scale : a.k_scale) + static_cast<size_t>(head) * (a.cap / block);
-  uint8_t *dst = (kv ? a.v8_dst : a.k8_dst) + static_cast<size_t>(head) * a.dst_cap * a.head_dim;
-  float *dst_scale = (kv ? a.v_scale_dst : a.k_scale_dst) + static_cast<size_t>(head) * (a.dst_cap / block);
+  const int pr = kPr ? kPr : a.head_dim >> 4;
+  const int lb = a.log2_block;
+  const size_t D = a.head_dim;
+  const size_t src0 = static_cast<size_t>(head) * a.cap * D;
+  const size_t dst0 = static_cast<size_t>(head) * a.dst_cap * D;
+  const size_t ssc0 = static_cast<size_t>(head) * (a.cap >> lb);
+  const size_t dsc0 = static_cast<size_t>(head) * (a.dst_cap >> lb);
   const float *w_src = a.weights + static_cast<size_t>(head) * a.cap;
   float *w_dst = a.weights_dst ? a.weights_dst + static_cast<size_t>(head) * a.dst_cap : nullptr;
   const int32_t *idx = a.idx + static_cast<size_t>(head) * a.K;
@@ -226,34 +244,49 @@ __global__ void __launch_bounds__(kThreads) evict_compact_kernel(const Cache8Evi
     const int base = i0 + part * kRows;
     const int rows = max(0, min(kRows, n - base));
     if (!kInPlace && rows == 0) return;
+    // threads 0..127: the rows' positions and K scales, the others the V scales
+    const int lr = tid & (kRows - 1);
     float wv = 0.f;
-    if (tid < rows) {
-      const int j = idx[base + tid];
-      s_idx[tid] = j;
-      s_exp[tid] = exp_of(kInPlace ? __ldcg(src_scale + j / block) : __ldg(src_scale + j / block));
-      if (kv == 0 && w_dst) wv = kInPlace ? __ldcg(w_src + j) : __ldg(w_src + j);
+    if (lr < rows) {
+      const int j = idx[base + lr];
+      const float *sc = (tid < kRows ? a.k_scale : a.v_scale) + ssc0 + (j >> lb);
+      s_exp[tid >= kRows][lr] = exp_of(kInPlace ? __ldcg(sc) : __ldg(sc));
+      if (tid < kRows) {
+        s_idx[lr] = j;
+        if (w_dst) wv = kInPlace ? __ldcg(w_src + j) : __ldg(w_src + j);
+      }
     }
-    if (tid >= kThreads - kRows / 16) s_max[tid - (kThreads - kRows / 16)] = 0;
+    if (tid < 2 * (kRows / 16)) s_max[tid / (kRows / 16)][tid % (kRows / 16)] = 0;
     __syncthreads();
-    uint4 c[kPieces];
+    uint4 c[2][kPieces];
     const int pieces = rows * pr;
+    auto row_of = [&](int p) { return kPr == 8 ? p >> 3 : kPr == 4 ? p >> 2 : p / pr; };
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
       const int p = tid + i * kThreads;
       if (p < pieces) {
-        const int r = p / pr;
-        const uint4 *q = reinterpret_cast<const uint4 *>(
-            src + static_cast<size_t>(s_idx[r]) * a.head_dim) + (p - r * pr);
-        c[i] = kInPlace ? __ldcg(q) : __ldcs(q);
+        const int r = row_of(p);
+        const size_t off = src0 + static_cast<size_t>(s_idx[r]) * D + (p - r * pr) * 16;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const uint4 *q = reinterpret_cast<const uint4 *>((kv ? a.v8 : a.k8) + off);
+          c[kv][i] = kInPlace ? __ldcg(q) : __ldcs(q);
+        }
       }
     }
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
       const int p = tid + i * kThreads;
-      if (p < pieces) {
-        const int r = p / pr;
-        const float m = absmax16(c[i]) * pow2f(s_exp[r]);
-        atomicMax(&s_max[r / block], __float_as_uint(m));
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        uint32_t m = 0;
+        if (p < pieces) m = __float_as_uint(absmax16(c[kv][i]) * pow2f(s_exp[kv][row_of(p)]));
+        if (kPr != 0) {  // a warp's rows (4 or 8, aligned) lie in one block
+          m = __reduce_max_sync(0xffffffffu, m);
+          if ((tid & 31) == 0 && p < pieces) atomicMax(&s_max[kv][row_of(p) >> lb], m);
+        } else if (p < pieces) {
+          atomicMax(&s_max[kv][row_of(p) >> lb], m);
+        }
       }
     }
     // every read of this round has returned in every CTA before any write
@@ -262,20 +295,32 @@ __global__ void __launch_bounds__(kThreads) evict_compact_kernel(const Cache8Evi
     for (int i = 0; i < kPieces; ++i) {
       const int p = tid + i * kThreads;
       if (p < pieces) {
-        const int r = p / pr;
-        const int k = s_exp[r] - scale_exp(__uint_as_float(s_max[r / block]));
-        if (k != 0) c[i] = rescale16(c[i], k);
-        uint4 *q = reinterpret_cast<uint4 *>(dst + static_cast<size_t>(base) * a.head_dim) + p;
-        if (kInPlace) __stcg(q, c[i]); else __stcs(q, c[i]);
+        const int r = row_of(p);
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const int k = s_exp[kv][r] - scale_exp(__uint_as_float(s_max[kv][r >> lb]));
+          if (k != 0) c[kv][i] = rescale16(c[kv][i], k);
+          uint4 *q = reinterpret_cast<uint4 *>((kv ? a.v8_dst : a.k8_dst) + dst0 +
+                                               static_cast<size_t>(base) * D) + p;
+          if (kInPlace) __stcg(q, c[kv][i]); else __stcs(q, c[kv][i]);
+        }
       }
     }
-    if (tid < rows) {
-      if (tid % block == 0)
-        dst_scale[(base + tid) / block] = pow2f(scale_exp(__uint_as_float(s_max[tid / block])));
-      if (kv == 0 && w_dst) w_dst[base + tid] = wv;
+    if (lr < rows) {
+      if ((lr & (a.block - 1)) == 0)
+        (tid < kRows ? a.k_scale_dst : a.v_scale_dst)[dsc0 + ((base + lr) >> lb)] =
+            pow2f(scale_exp(__uint_as_float(s_max[tid >= kRows][lr >> lb])));
+      if (tid < kRows && w_dst) w_dst[base + lr] = wv;
     }
     if (kInPlace) __syncthreads();  // s_idx, s_exp and s_max are free again
   }
+}
+
+template <bool kInPlace>
+auto compact_kernel_for(int head_dim) {
+  return head_dim == 128  ? evict_compact_kernel<kInPlace, 8>
+         : head_dim == 64 ? evict_compact_kernel<kInPlace, 4>
+                          : evict_compact_kernel<kInPlace, 0>;
 }
 
 }  // namespace
@@ -284,9 +329,10 @@ bkv_status launch_cache8_evict(Cache8EvictArgs a, bool in_place, cudaStream_t st
   if (injected_launch_failure()) return BKV_ERR_CUDA;
   static int done_staged[64], done_plain[64];
   a.mask_words = kMaskWords(a.max_len);
+  a.log2_block = a.block == 16 ? 4 : a.block == 32 ? 5 : a.block == 64 ? 6 : 7;
   const bool staged = a.max_len <= kStageMax;
   const int mask_bytes = 2 * 4 * a.mask_words;
-  const int smem = mask_bytes + (staged ? 4 * static_cast<int>(a.max_len) : 0);
+  const int smem = mask_bytes + (staged ? 4 * static_cast<int>((a.max_len + 3) / 4 * 4) : 0);
   const unsigned heads = static_cast<unsigned>(a.n_seqs) * a.n_kv_heads;
   if (staged) {
     if (!ensure_smem_limit(evict_select_kernel<true>, 200 << 10, done_staged)) return BKV_ERR_CUDA;
@@ -302,7 +348,7 @@ bkv_status launch_cache8_evict(Cache8EvictArgs a, bool in_place, cudaStream_t st
     per = per >= 8 ? 8 : per >= 4 ? 4 : per >= 2 ? 2 : 1;  // the cluster's CTAs
     a.ctas_per_head = static_cast<int>(per);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(2 * heads * per));
+    cfg.gridDim = dim3(static_cast<unsigned>(heads * per));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
@@ -311,14 +357,15 @@ bkv_status launch_cache8_evict(Cache8EvictArgs a, bool in_place, cudaStream_t st
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, evict_compact_kernel<true>, a) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, compact_kernel_for<true>(a.head_dim), a) != cudaSuccess) {
       cudaGetLastError();
       return BKV_ERR_CUDA;
     }
     return BKV_OK;
   }
   a.ctas_per_head = static_cast<int>(per);
-  evict_compact_kernel<false><<<static_cast<unsigned>(2 * heads * per), kThreads, 0, stream>>>(a);
+  auto kernel = compact_kernel_for<false>(a.head_dim);
+  kernel<<<static_cast<unsigned>(heads * per), kThreads, 0, stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? BKV_OK : BKV_ERR_CUDA;
 }
 

@@ -84,9 +84,9 @@ def test_append_refuses(bad):
     dict(T=0), dict(T=1 << 23), dict(max_len=0), dict(max_len=1025), dict(scale=-1.0),
     dict(scale=float("nan")), dict(scale=float("inf")), dict(decay=float("nan")),
     dict(decay=float("inf")), dict(win=WIN, wout=0), dict(q=Q + 8), dict(out=OUT + 2),
-    dict(lse=LSE + 2), dict(win=WIN + 2), dict(wout=WOUT + 1), dict(nn=NN + 2),
+    dict(lse=LSE + 2), dict(win=WIN + 4), dict(wout=WOUT + 8), dict(nn=NN + 2),
     dict(out=Q), dict(out=K8), dict(out=V8 + 64), dict(lse=OUT), dict(wout=KS), dict(wout=K8),
-    dict(win=WIN, wout=WIN + 4), dict(ws=OUT), dict(ws=K8), dict(wout=Q), dict(lse=LENS),
+    dict(win=WIN, wout=WIN + 16), dict(ws=OUT), dict(ws=K8), dict(wout=Q), dict(lse=LENS),
 ])
 def test_attend_refuses(bad):
     assert attend(desc(), **bad) == INVALID
@@ -106,13 +106,13 @@ def test_attend_workspace():
     dict(K=-1), dict(K=1 << 31), dict(sink=-1), dict(recent=-1), dict(sink=200, recent=57),
     dict(dst=desc(cap=192)), dict(dst=desc(S=1, cap=256)), dict(dst=desc(Hq=4, Hkv=1, cap=256)),
     dict(dst=desc(d=64, cap=256)), dict(dst=desc(cap=256, block=32)), dict(dst=desc(cap=250)),
-    dict(k8=K8 + 8), dict(kd=KD + 4), dict(w=WIN + 2), dict(wd=WD + 1), dict(idx=IDX + 2),
+    dict(k8=K8 + 8), dict(kd=KD + 4), dict(w=WIN + 4), dict(wd=WD + 8), dict(idx=IDX + 2),
     dict(nl=NL + 1), dict(kd=K8), dict(kd=K8, vd=V8), dict(vd=KD), dict(wd=WIN), dict(idx=WIN),
     dict(nl=IDX), dict(ws=KD), dict(ksd=KS), dict(idx=LENS),
     # in place with one of the five elsewhere, or another capacity
     dict(kd=K8, vd=V8, ksd=KS, vsd=VSD, dst=desc()),
     dict(kd=K8, vd=V8, ksd=KS, vsd=VS, dst=desc(cap=512)),
-    dict(kd=K8, vd=V8, ksd=KS, vsd=VS, dst=desc(), wd=WIN + 4),
+    dict(kd=K8, vd=V8, ksd=KS, vsd=VS, dst=desc(), wd=WIN + 16),
 ])
 def test_evict_refuses(bad):
     assert evict(desc(), **bad) == INVALID
