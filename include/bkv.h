@@ -383,7 +383,7 @@ bkv_status bkv_cache8_attend(const bkv_cache8_desc *desc, const void *k8,
 /* Eviction by accumulated attention weight.  Every (sequence, KV head) of
  * length L = lens[s] > K keeps its first `sink` rows, its last `recent` rows
  * and, of the rest, the K - sink - recent with the largest weights (ties: the
- * lower position; a NaN weight ranks last); one of L <= K keeps every row.
+ * lower position; a NaN weight ranks as -infinity); one of L <= K keeps every row.
  * The kept rows move, in ascending order, to rows 0 .. min(K, L) - 1 of the
  * destination, with their weights, and every block of the destination takes
  * the scale of its rows (values are as before but for codes that leave
@@ -399,8 +399,7 @@ bkv_status bkv_cache8_attend(const bkv_cache8_desc *desc, const void *k8,
  *   idx          device out, optional int32 [n_seqs][n_kv_heads][K]: the kept
  *                positions, the first min(K, L) of each row
  *   new_lens     device out, optional int32 [n_seqs]: min(K, L); may be lens
- * Requires 1 <= K, sink + recent <= K, 1 <= max_len <= capacity; max_len
- * up to 786432 (BKV_ERR_UNSUPPORTED past that). */
+ * Requires 1 <= K, sink + recent <= K, 1 <= max_len <= capacity. */
 bkv_status bkv_cache8_evict(const bkv_cache8_desc *desc, const void *k8,
                             const void *v8, const float *k_scale,
                             const float *v_scale, const float *weights,

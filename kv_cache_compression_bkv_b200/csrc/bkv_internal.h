@@ -186,9 +186,8 @@ struct Cache8EvictArgs {
   int32_t *new_lens;           // [n_seqs] or NULL; may be lens
   int n_seqs, n_kv_heads, head_dim, block, sink, recent;
   long long cap, dst_cap, max_len, K;
-  int mask_words, ctas_per_head, log2_block;  // filled by the launcher
+  int ctas_per_head, log2_block;  // filled by the launcher
 };
-constexpr long long kCache8EvictMaxLen = 786432;  // two position bitmasks in shared memory
 bkv_status launch_cache8_evict(Cache8EvictArgs a, bool in_place, cudaStream_t stream);
 
 // Fault injection for the host-side error paths: when the environment

@@ -220,7 +220,6 @@ bkv_status bkv_cache8_evict(const bkv_cache8_desc *desc, const void *k8, const v
       static_cast<long long>(sink) + recent > K || dst->capacity < std::min<int64_t>(K, max_len))
     return BKV_ERR_INVALID_ARG;
   if (st != BKV_OK) return st;
-  if (max_len > kCache8EvictMaxLen) return BKV_ERR_UNSUPPORTED;
   const bool in_place = k8_dst == k8 && v8_dst == v8 && k_scale_dst == k_scale &&
                         v_scale_dst == v_scale && dst->capacity == desc->capacity;
   const size_t cb = code_bytes(desc), sb = scale_bytes(desc), wb = weight_bytes(desc);

@@ -4,14 +4,18 @@
 //
 // Select: one CTA per (sequence, KV head).  A row of L > K positions keeps the
 // first `sink`, the last `recent` and, of the rest, the K - sink - recent with
-// the largest weights, ties to the lower position.  The weights are ranked as
-// order-preserving 32-bit keys (order_key.cuh); three radix passes of 11, 11
-// and 10 bits over a shared-memory histogram give the threshold key and how
-// many of its ties stay.  The keys are staged in shared memory when the row
-// fits, so HBM sees the row once.  Then every position becomes one bit of a
-// mask (a ballot per 32 positions), ties are dropped by a prefix sum over the
-// mask words, and the kept positions are written in ascending order at the
-// words' prefix offsets.
+// the largest weights, ties to the lower position.  The row is read three
+// times, from HBM once and then from L2, so that it takes no shared memory and
+// several CTAs share an SM: a histogram of the weights' top 11 bits gives the
+// bin of the threshold; the order-preserving keys (order_key.cuh) of that bin,
+// a few percent, are listed in shared memory and two more radix steps over the
+// list give the threshold and how many of its ties stay; last, each warp turns
+// 1024 positions into 32 mask words by ballots, drops surplus ties by a prefix
+// sum, and writes the kept positions in ascending order, a coalesced store per
+// word.  Bound by instruction issue (a row is 4 bytes a position), so the inner
+// loops take the weights as they are: bins by raw bits, put in order when they
+// are summed, comparisons as floats, and no range checks but in the chunks
+// where the candidates begin and end.
 //
 // Compaction: a CTA takes 128 new rows of one (sequence, head), K and V, which
 // are whole blocks of the new cache.  It gathers the rows' codes and old
@@ -38,14 +42,16 @@ namespace {
 using namespace cache8;
 namespace cg = cooperative_groups;
 
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 512;
+constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kStageMax = 45056;  // positions whose weights fit in shared memory
-// mask words per thread: positions up to kSelThreads * 32 * kWordsMax
-constexpr int kMaskWords(long long L) { return static_cast<int>((L + 127) / 128 * 4); }
+constexpr int kListMax = 8192;  // keys of the threshold's bin that are listed
 
-// NaN ranks below every number
-__device__ __forceinline__ uint32_t rank_key(float w) { return w != w ? 0u : order_key(w); }
+// A weight as it is ranked: NaN as -infinity, -0 as +0.
+__device__ __forceinline__ float ranked(float w) { return fmaxf(w + 0.f, -INFINITY); }
+// Bins of raw bits, and the order of their values: negative floats (bins 1024
+// and up) fall as their bits rise.
+__device__ __forceinline__ uint32_t bin_of(float v) { return __float_as_uint(v) >> 21; }
 
 // Exclusive prefix sum over the CTA of one value per thread; `total` for all.
 __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *s_warp, uint32_t *total) {
@@ -59,30 +65,87 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *s_warp, uin
   __syncthreads();  // s_warp is free again
   if (lane == 31) s_warp[warp] = x;
   __syncthreads();
-  if (warp == 0) {
-    uint32_t t = s_warp[lane];
+  uint32_t t = lane < kSelWarps ? s_warp[lane] : 0u;  // every warp sums for itself
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, t, o);
-      if (lane >= o) t += y;
-    }
-    s_warp[lane] = t;
+  for (int o = 1; o < kSelWarps; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, t, o);
+    if (lane >= o) t += y;
   }
-  __syncthreads();
-  *total = s_warp[31];
-  return x - v + (warp ? s_warp[warp - 1] : 0u);
+  *total = __shfl_sync(0xffffffffu, t, kSelWarps - 1);
+  const uint32_t before = __shfl_sync(0xffffffffu, t, max(warp - 1, 0));
+  return x - v + (warp ? before : 0u);
 }
 
-template <bool kStaged>
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Cache8EvictArgs a) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ uint32_t s_hist[kBins];
-  __shared__ uint32_t s_warp[32];
-  __shared__ uint32_t s_bin, s_above;
-  uint32_t *s_mask = reinterpret_cast<uint32_t *>(smem);              // above the threshold, or protected
-  uint32_t *s_tie = s_mask + a.mask_words;                            // equal to it
-  uint32_t *s_key = s_tie + a.mask_words;
-  const int tid = threadIdx.x, lane = tid & 31;
+// The bin of the histogram that holds the need-th largest value; need becomes
+// its rank within the bin.  kRaw: bins of raw bits, else of keys.  Leaves the
+// histogram zeroed.
+template <bool kRaw>
+__device__ __forceinline__ uint32_t find_bin(uint32_t *s_hist, uint32_t *s_warp, uint32_t *s_bin,
+                                             uint32_t *need) {
+  // suffix counts: four bins a thread, the largest values first
+  const int top = kBins - 4 - 4 * static_cast<int>(threadIdx.x);  // the four: top + 3 .. top
+  const bool neg = kRaw && top < 1024;
+  const int b = !kRaw ? top : neg ? 2044 - top : top - 1024;      // where they are
+  const uint4 c = *reinterpret_cast<const uint4 *>(s_hist + b);
+  *reinterpret_cast<uint4 *>(s_hist + b) = make_uint4(0, 0, 0, 0);
+  uint32_t total;
+  uint32_t above = block_scan(c.x + c.y + c.z + c.w, s_warp, &total);
+  const uint32_t n[4] = {neg ? c.x : c.w, neg ? c.y : c.z, neg ? c.z : c.y, neg ? c.w : c.x};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (above < *need && *need <= above + n[i]) {
+      s_bin[0] = static_cast<uint32_t>(neg ? b + i : b + 3 - i);
+      s_bin[1] = above;
+    }
+    above += n[i];
+  }
+  __syncthreads();
+  *need -= s_bin[1];
+  return s_bin[0];
+}
+
+// Calls f(v, candidate) for the ranked weight of every position, by whole
+// warps; four positions a lane and step, kBatch steps' loads in flight.
+template <typename F>
+__device__ __forceinline__ void for_weights(const float *w, int L, int lo, int hi, F &&f) {
+  constexpr int kBatch = 4;
+  const unsigned quads = (static_cast<unsigned>(L) + 3) >> 2;  // a row is allocated to whole quads
+  const unsigned first = threadIdx.x & ~31u, lane = threadIdx.x & 31u;
+  const unsigned l = static_cast<unsigned>(lo), h = static_cast<unsigned>(hi);
+  for (unsigned q0 = first; q0 < quads; q0 += kBatch * kSelThreads) {
+    float4 v[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const unsigned q = q0 + u * kSelThreads + lane;
+      if (q < quads) v[u] = __ldg(reinterpret_cast<const float4 *>(w) + q);
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const unsigned j0 = 4 * (q0 + u * kSelThreads);  // this warp's 128 positions
+      if (j0 >= h || j0 + 128 <= l) continue;
+      if (j0 >= l && j0 + 128 <= h) {
+        f(ranked(v[u].x), true);
+        f(ranked(v[u].y), true);
+        f(ranked(v[u].z), true);
+        f(ranked(v[u].w), true);
+      } else {
+        const unsigned j = j0 + 4 * lane;
+        f(ranked(v[u].x), j >= l && j < h);
+        f(ranked(v[u].y), j + 1 >= l && j + 1 < h);
+        f(ranked(v[u].z), j + 2 >= l && j + 2 < h);
+        f(ranked(v[u].w), j + 3 >= l && j + 3 < h);
+      }
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kSelThreads, 3) evict_select_kernel(const Cache8EvictArgs a) {
+  __shared__ __align__(16) uint32_t s_hist[kBins];
+  __shared__ uint32_t s_list[kListMax];
+  __shared__ uint32_t s_warp[kSelWarps];
+  __shared__ uint32_t s_bin[2], s_count;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int head = blockIdx.x, seq = head / a.n_kv_heads;
   const int L = a.lens[seq];
   if (L < 0 || L > a.max_len) {
@@ -102,109 +165,94 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Cache8E
   const float *w = a.weights + static_cast<size_t>(head) * a.cap;
   const int lo = a.sink, hi = L - a.recent;  // candidates: [lo, hi)
   uint32_t need = static_cast<uint32_t>(K - a.sink - a.recent);
-  auto key_at = [&](int j) { return kStaged ? s_key[j] : rank_key(__ldg(w + j)); };
-
-  uint32_t thr = 0, ties = 0;  // keep keys > thr, and the first `ties` equal to it
+  float thr = INFINITY;  // keep weights > thr, and the first `ties` equal to it
+  uint32_t ties = 0;
   if (need > 0) {
-    uint32_t prefix = 0;
-#pragma unroll
-    for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-      const int bits = pass == 2 ? 10 : 11;
-      for (int b = tid; b < kBins; b += kSelThreads) s_hist[b] = 0;
-      __syncthreads();
-      // four positions a thread and step, kBatch steps' loads in flight; a row
-      // is 16-byte aligned and allocated to a multiple of 16 positions
-      constexpr int kBatch = 4;
-      const int quads = (L + 3) >> 2;
-      for (int q0 = tid; q0 < quads; q0 += kBatch * kSelThreads) {
-        uint4 k[kBatch];
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-          const int q = q0 + u * kSelThreads;
-          if (q >= quads) continue;
-          if (kStaged && pass > 0) {
-            k[u] = reinterpret_cast<const uint4 *>(s_key)[q];
-          } else {
-            const float4 f = __ldg(reinterpret_cast<const float4 *>(w) + q);
-            k[u] = make_uint4(rank_key(f.x), rank_key(f.y), rank_key(f.z), rank_key(f.w));
-            if (kStaged) reinterpret_cast<uint4 *>(s_key)[q] = k[u];
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-          const int q = q0 + u * kSelThreads;
-          if (q >= quads) continue;
-          const uint32_t v[4] = {k[u].x, k[u].y, k[u].z, k[u].w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int j = 4 * q + i;
-            if (j >= lo && j < hi && (pass == 0 || (v[i] >> (shift + bits)) == prefix))
-              atomicAdd(&s_hist[(v[i] >> shift) & ((1u << bits) - 1)], 1u);
-          }
-        }
+    for (int b = tid; b < kBins; b += kSelThreads) s_hist[b] = 0;
+    if (tid == 0) s_count = 0;
+    __syncthreads();
+    for_weights(w, L, lo, hi, [&](float v, bool cand) {
+      if (cand) atomicAdd(&s_hist[bin_of(v)], 1u);
+    });
+    __syncthreads();
+    const uint32_t raw = find_bin<true>(s_hist, s_warp, s_bin, &need);
+    // the bin's keys, listed, and their next 11 bits counted
+    for_weights(w, L, lo, hi, [&](float v, bool cand) {
+      const bool in = cand && bin_of(v) == raw;
+      const unsigned m = __ballot_sync(0xffffffffu, in);
+      if (m == 0) return;
+      uint32_t at = 0;
+      if (lane == 0) at = atomicAdd(&s_count, static_cast<uint32_t>(__popc(m)));
+      at = __shfl_sync(0xffffffffu, at, 0) + __popc(m & ((1u << lane) - 1));
+      if (in) {
+        const uint32_t k = order_key(v);
+        atomicAdd(&s_hist[(k >> 10) & 2047u], 1u);
+        if (at < kListMax) s_list[at] = k;
       }
-      __syncthreads();
-      // the bin that holds the need-th largest key: suffix counts, two bins a
-      // thread, the largest bins first
-      const int b1 = kBins - 1 - 2 * tid, b0 = b1 - 1;
-      const uint32_t c1 = s_hist[b1], c0 = s_hist[b0];
-      uint32_t total;
-      const uint32_t above = block_scan(c0 + c1, s_warp, &total);
-      if (above < need && need <= above + c1) {
-        s_bin = static_cast<uint32_t>(b1);
-        s_above = above;
-      } else if (above + c1 < need && need <= above + c1 + c0) {
-        s_bin = static_cast<uint32_t>(b0);
-        s_above = above + c1;
-      }
-      __syncthreads();
-      prefix = (prefix << bits) | s_bin;
-      need -= s_above;
+    });
+    __syncthreads();
+    const uint32_t top = raw < 1024 ? 1024 + raw : 2047 - raw;  // the bin's keys' top bits
+    const uint32_t mid = (top << 11) | find_bin<false>(s_hist, s_warp, s_bin, &need);
+    const uint32_t n = s_count;
+    if (n <= kListMax) {
+      for (uint32_t i = tid; i < n; i += kSelThreads)
+        if ((s_list[i] >> 10) == mid) atomicAdd(&s_hist[s_list[i] & 1023u], 1u);
+    } else {  // a crowded bin: the row again
+      for_weights(w, L, lo, hi, [&](float v, bool cand) {
+        const uint32_t k = order_key(v);
+        if (cand && (k >> 10) == mid) atomicAdd(&s_hist[k & 1023u], 1u);
+      });
     }
-    thr = prefix;
+    __syncthreads();
+    thr = key_value((mid << 10) | find_bin<false>(s_hist, s_warp, s_bin, &need));
     ties = need;
   }
-  // masks: a bit per position
-  const int words = (L + 31) >> 5;
-  for (int q = tid >> 5; q < words; q += kSelThreads / 32) {
-    const int j = q * 32 + lane;
-    const bool cand = j >= lo && j < hi;
-    const uint32_t k = cand && ties > 0 ? key_at(j) : 0u;
-    const uint32_t m = __ballot_sync(0xffffffffu,
-                                     j < L && (!cand || (ties > 0 && k > thr)));
-    const uint32_t t = __ballot_sync(0xffffffffu, cand && ties > 0 && k == thr);
-    if (lane == 0) {
-      s_mask[q] = m;
-      s_tie[q] = t;
+  // kept positions, 32 words of 32 positions a warp at a time
+  uint32_t ties_before = 0, at0 = 0;
+  for (unsigned base = 0; base < static_cast<unsigned>(L); base += 1024u * kSelWarps) {
+    const unsigned jw = base + 1024u * warp, j0 = jw + lane;  // this warp's positions
+    const unsigned l = static_cast<unsigned>(lo), h = static_cast<unsigned>(hi);
+    uint32_t keep = 0, tie = 0;  // of word `lane` of this warp's 32
+    if (ties > 0 && jw >= l && jw + 1024 <= h) {
+#pragma unroll 8
+      for (int q = 0; q < 32; ++q) {
+        const float v = fmaxf(__ldg(w + j0 + 32u * q), -INFINITY);
+        const uint32_t m = __ballot_sync(0xffffffffu, v > thr);
+        const uint32_t t = __ballot_sync(0xffffffffu, v == thr);
+        if (lane == q) {
+          keep = m;
+          tie = t;
+        }
+      }
+    } else {
+      for (int q = 0; q < 32; ++q) {
+        const unsigned j = j0 + 32u * q;
+        const bool there = j < static_cast<unsigned>(L);
+        const bool cand = j >= l && j < h;
+        const float v = cand && ties > 0 ? fmaxf(__ldg(w + j), -INFINITY) : 0.f;
+        const uint32_t m = __ballot_sync(0xffffffffu, there && (!cand || (ties > 0 && v > thr)));
+        const uint32_t t = __ballot_sync(0xffffffffu, cand && ties > 0 && v == thr);
+        if (lane == q) {
+          keep = m;
+          tie = t;
+        }
+      }
     }
-  }
-  __syncthreads();
-  // each thread owns a run of words; ties kept in position order
-  const int per = (words + kSelThreads - 1) / kSelThreads;
-  const int q0 = min(tid * per, words), q1 = min(q0 + per, words);
-  uint32_t cnt = 0, total;
-  for (int q = q0; q < q1; ++q) cnt += __popc(s_tie[q]);
-  uint32_t before = block_scan(cnt, s_warp, &total);
-  cnt = 0;
-  for (int q = q0; q < q1; ++q) {
-    uint32_t t = s_tie[q];
-    const uint32_t c = __popc(t);
+    uint32_t total;
+    const uint32_t c = __popc(tie);
+    const uint32_t before = ties_before + block_scan(c, s_warp, &total);
+    ties_before += total;
     if (before + c > ties) {  // drop the highest positions
       const uint32_t stay = before < ties ? ties - before : 0u;
-      for (uint32_t d = c; d > stay; --d) t &= ~(0x80000000u >> __clz(t));
+      for (uint32_t d = c; d > stay; --d) tie &= ~(0x80000000u >> __clz(tie));
     }
-    before += c;
-    const uint32_t m = s_mask[q] | t;
-    s_mask[q] = m;
-    cnt += __popc(m);
-  }
-  uint32_t at = block_scan(cnt, s_warp, &total);
-  for (int q = q0; q < q1; ++q) {
-    uint32_t m = s_mask[q];
-    while (m) {
-      idx[at++] = q * 32 + __ffs(m) - 1;
-      m &= m - 1;
+    keep |= tie;
+    const uint32_t at = at0 + block_scan(__popc(keep), s_warp, &total);
+    at0 += total;
+#pragma unroll 4
+    for (int q = 0; q < 32; ++q) {
+      const uint32_t m = __shfl_sync(0xffffffffu, keep, q), o = __shfl_sync(0xffffffffu, at, q);
+      if ((m >> lane) & 1u) idx[o + __popc(m & ((1u << lane) - 1))] = static_cast<int32_t>(j0 + 32u * q);
     }
   }
 }
@@ -223,6 +271,8 @@ __global__ void __launch_bounds__(kThreads) evict_compact_kernel(const Cache8Evi
   const int head = blockIdx.x / a.ctas_per_head;
   const int part = blockIdx.x - head * a.ctas_per_head;  // in place: the rank in the cluster
   const int seq = head / a.n_kv_heads;
+  // launched while the select kernel ends: nothing of its is read before this
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int n = a.kept[seq];
   if (part == 0 && tid == 0 && head - seq * a.n_kv_heads == 0 && n >= 0 && a.new_lens)
     a.new_lens[seq] = n;
@@ -327,46 +377,30 @@ auto compact_kernel_for(int head_dim) {
 
 bkv_status launch_cache8_evict(Cache8EvictArgs a, bool in_place, cudaStream_t stream) {
   if (injected_launch_failure()) return BKV_ERR_CUDA;
-  static int done_staged[64], done_plain[64];
-  a.mask_words = kMaskWords(a.max_len);
   a.log2_block = a.block == 16 ? 4 : a.block == 32 ? 5 : a.block == 64 ? 6 : 7;
-  const bool staged = a.max_len <= kStageMax;
-  const int mask_bytes = 2 * 4 * a.mask_words;
-  const int smem = mask_bytes + (staged ? 4 * static_cast<int>((a.max_len + 3) / 4 * 4) : 0);
   const unsigned heads = static_cast<unsigned>(a.n_seqs) * a.n_kv_heads;
-  if (staged) {
-    if (!ensure_smem_limit(evict_select_kernel<true>, 200 << 10, done_staged)) return BKV_ERR_CUDA;
-    evict_select_kernel<true><<<heads, kSelThreads, smem, stream>>>(a);
-  } else {
-    if (!ensure_smem_limit(evict_select_kernel<false>, 200 << 10, done_plain)) return BKV_ERR_CUDA;
-    evict_select_kernel<false><<<heads, kSelThreads, smem, stream>>>(a);
-  }
+  evict_select_kernel<<<heads, kSelThreads, 0, stream>>>(a);
   if (cudaGetLastError() != cudaSuccess) return BKV_ERR_CUDA;
   const long long rows = std::min<long long>(a.K, a.max_len);
   long long per = (rows + kRows - 1) / kRows;
-  if (in_place) {
-    per = per >= 8 ? 8 : per >= 4 ? 4 : per >= 2 ? 2 : 1;  // the cluster's CTAs
-    a.ctas_per_head = static_cast<int>(per);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(heads * per));
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = static_cast<unsigned>(per);
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, compact_kernel_for<true>(a.head_dim), a) != cudaSuccess) {
-      cudaGetLastError();
-      return BKV_ERR_CUDA;
-    }
-    return BKV_OK;
-  }
+  if (in_place) per = per >= 8 ? 8 : per >= 4 ? 4 : per >= 2 ? 2 : 1;  // the cluster's CTAs
   a.ctas_per_head = static_cast<int>(per);
-  auto kernel = compact_kernel_for<false>(a.head_dim);
-  kernel<<<static_cast<unsigned>(heads * per), kThreads, 0, stream>>>(a);
-  return cudaGetLastError() == cudaSuccess ? BKV_OK : BKV_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(heads * per));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = static_cast<unsigned>(per);
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = in_place ? 2 : 1;
+  auto kernel = in_place ? compact_kernel_for<true>(a.head_dim) : compact_kernel_for<false>(a.head_dim);
+  if (cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess) return BKV_OK;
+  cudaGetLastError();
+  return BKV_ERR_CUDA;
 }
 
 }  // namespace bkv

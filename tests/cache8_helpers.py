@@ -104,7 +104,7 @@ def kept_positions(w, L, K, sink, recent):
 
     def key(j):
         x = float(w[j])
-        return (-x, j) if x == x else (math.inf, j)        # NaN last
+        return (-x if x == x else math.inf, j)             # NaN as -infinity
 
-    order = sorted(mid, key=lambda j: (1, j) if float(w[j]) != float(w[j]) else (0,) + key(j))
+    order = sorted(mid, key=key)
     return sorted(list(range(sink)) + list(range(L - recent, L)) + order[:K - sink - recent])

@@ -344,7 +344,8 @@ EVICTS = [
     (2, 1, 64, 16, [64, 64], 100, 5, 5),               # budgets above the lengths
     (1, 2, 128, 16, [3000], 1, 0, 1),
     (1, 2, 128, 16, [3000], 1, 0, 0),
-    (1, 1, 16, 16, [46000], 9001, 7, 1000),            # too long to stage
+    (1, 1, 16, 16, [46000], 9001, 7, 1000),            # a crowded threshold bin (ties)
+    (1, 1, 16, 16, [40000], 39000, 0, 0),
 ]
 
 
@@ -369,6 +370,7 @@ def make_evict(i, special=True):
         w[:, :, 13::101] = math.inf
         w[:, :, 17::103] = -0.0
         w[:, :, 23::107] = -1.5
+        w[:, :, 29::109] = -math.inf
     return dev, rc, w, cap
 
 
