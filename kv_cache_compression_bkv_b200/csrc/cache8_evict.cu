@@ -108,7 +108,7 @@ __device__ __forceinline__ uint32_t find_bin(uint32_t *s_hist, uint32_t *s_warp,
 // warps; four positions a lane and step, kBatch steps' loads in flight.
 template <typename F>
 __device__ __forceinline__ void for_weights(const float *w, int L, int lo, int hi, F &&f) {
-  constexpr int kBatch = 4;
+  constexpr int kBatch = 8;
   const unsigned quads = (static_cast<unsigned>(L) + 3) >> 2;  // a row is allocated to whole quads
   const unsigned first = threadIdx.x & ~31u, lane = threadIdx.x & 31u;
   const unsigned l = static_cast<unsigned>(lo), h = static_cast<unsigned>(hi);
@@ -139,7 +139,7 @@ __device__ __forceinline__ void for_weights(const float *w, int L, int lo, int h
   }
 }
 
-__global__ void __launch_bounds__(kSelThreads, 3) evict_select_kernel(const Cache8EvictArgs a) {
+__global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Cache8EvictArgs a) {
   __shared__ __align__(16) uint32_t s_hist[kBins];
   __shared__ uint32_t s_list[kListMax];
   __shared__ uint32_t s_warp[kSelWarps];
@@ -178,15 +178,10 @@ __global__ void __launch_bounds__(kSelThreads, 3) evict_select_kernel(const Cach
     const uint32_t raw = find_bin<true>(s_hist, s_warp, s_bin, &need);
     // the bin's keys, listed, and their next 11 bits counted
     for_weights(w, L, lo, hi, [&](float v, bool cand) {
-      const bool in = cand && bin_of(v) == raw;
-      const unsigned m = __ballot_sync(0xffffffffu, in);
-      if (m == 0) return;
-      uint32_t at = 0;
-      if (lane == 0) at = atomicAdd(&s_count, static_cast<uint32_t>(__popc(m)));
-      at = __shfl_sync(0xffffffffu, at, 0) + __popc(m & ((1u << lane) - 1));
-      if (in) {
+      if (cand && bin_of(v) == raw) {
         const uint32_t k = order_key(v);
         atomicAdd(&s_hist[(k >> 10) & 2047u], 1u);
+        const uint32_t at = atomicAdd(&s_count, 1u);
         if (at < kListMax) s_list[at] = k;
       }
     });
@@ -207,52 +202,89 @@ __global__ void __launch_bounds__(kSelThreads, 3) evict_select_kernel(const Cach
     thr = key_value((mid << 10) | find_bin<false>(s_hist, s_warp, s_bin, &need));
     ties = need;
   }
-  // kept positions, 32 words of 32 positions a warp at a time
+  // Kept positions, 1024 a warp at a time: in step t of 8 a lane has positions
+  // 128 t + 4 lane .. + 3, bits 4 t .. 4 t + 3 of its words.
+  const unsigned lt = (1u << lane) - 1;
   uint32_t ties_before = 0, at0 = 0;
   for (unsigned base = 0; base < static_cast<unsigned>(L); base += 1024u * kSelWarps) {
-    const unsigned jw = base + 1024u * warp, j0 = jw + lane;  // this warp's positions
+    const unsigned jw = base + 1024u * warp, j0 = jw + 4 * lane;
     const unsigned l = static_cast<unsigned>(lo), h = static_cast<unsigned>(hi);
-    uint32_t keep = 0, tie = 0;  // of word `lane` of this warp's 32
-    if (ties > 0 && jw >= l && jw + 1024 <= h) {
-#pragma unroll 8
-      for (int q = 0; q < 32; ++q) {
-        const float v = fmaxf(__ldg(w + j0 + 32u * q), -INFINITY);
-        const uint32_t m = __ballot_sync(0xffffffffu, v > thr);
-        const uint32_t t = __ballot_sync(0xffffffffu, v == thr);
-        if (lane == q) {
-          keep = m;
-          tie = t;
+    uint32_t keep = 0, tie = 0;
+    const bool inner = ties > 0 && jw >= l && jw + 1024 <= h;
+    if (inner || jw < static_cast<unsigned>(L)) {
+      float4 v[8];
+#pragma unroll
+      for (int t = 0; t < 8; ++t)  // a row is allocated to whole quads
+        if (inner || j0 + 128 * t < static_cast<unsigned>(L))
+          v[t] = __ldg(reinterpret_cast<const float4 *>(w + j0 + 128 * t));
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        const float y[4] = {v[t].x, v[t].y, v[t].z, v[t].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float x = fmaxf(y[i], -INFINITY);
+          if (x > thr) keep |= 1u << (4 * t + i);
+          if (x == thr) tie |= 1u << (4 * t + i);
         }
       }
-    } else {
-      for (int q = 0; q < 32; ++q) {
-        const unsigned j = j0 + 32u * q;
-        const bool there = j < static_cast<unsigned>(L);
-        const bool cand = j >= l && j < h;
-        const float v = cand && ties > 0 ? fmaxf(__ldg(w + j), -INFINITY) : 0.f;
-        const uint32_t m = __ballot_sync(0xffffffffu, there && (!cand || (ties > 0 && v > thr)));
-        const uint32_t t = __ballot_sync(0xffffffffu, cand && ties > 0 && v == thr);
-        if (lane == q) {
-          keep = m;
-          tie = t;
+      if (!inner) {  // the sink and the recent rows, and what lies past the end
+        uint32_t cand = 0, there = 0;
+#pragma unroll
+        for (int t = 0; t < 32; ++t) {
+          const unsigned j = j0 + 128 * (t >> 2) + (t & 3);
+          if (j < static_cast<unsigned>(L)) there |= 1u << t;
+          if (j >= l && j < h) cand |= 1u << t;
         }
+        // without a candidate to keep (ties == 0) the threshold is infinity
+        keep = (ties > 0 ? keep & cand : 0u) | (there & ~cand);
+        tie &= ties > 0 ? cand : 0u;
       }
     }
     uint32_t total;
-    const uint32_t c = __popc(tie);
-    const uint32_t before = ties_before + block_scan(c, s_warp, &total);
+    // ties, in position order; most rows have no more than they keep
+    const uint32_t mine = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(__popc(tie)));
+    uint32_t rank = ties_before + block_scan(lane == 0 ? mine : 0u, s_warp, &total);
+    rank = __shfl_sync(0xffffffffu, rank, 0);  // ties before this warp's
     ties_before += total;
-    if (before + c > ties) {  // drop the highest positions
-      const uint32_t stay = before < ties ? ties - before : 0u;
-      for (uint32_t d = c; d > stay; --d) tie &= ~(0x80000000u >> __clz(tie));
+    if (rank + mine <= ties) {
+      keep |= tie;
+    } else if (rank < ties) {
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        const uint32_t n = (tie >> (4 * t)) & 15u;
+        uint32_t before = 0, all = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const unsigned m = __ballot_sync(0xffffffffu, (n >> i) & 1u);
+          before += __popc(m & lt);
+          all += __popc(m);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if ((n >> i) & 1u) {
+            if (rank + before < ties) keep |= 1u << (4 * t + i);
+            ++before;
+          }
+        rank += all;
+      }
     }
-    keep |= tie;
-    const uint32_t at = at0 + block_scan(__popc(keep), s_warp, &total);
+    const uint32_t kept = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(__popc(keep)));
+    uint32_t at = at0 + block_scan(lane == 0 ? kept : 0u, s_warp, &total);
+    at = __shfl_sync(0xffffffffu, at, 0);
     at0 += total;
-#pragma unroll 4
-    for (int q = 0; q < 32; ++q) {
-      const uint32_t m = __shfl_sync(0xffffffffu, keep, q), o = __shfl_sync(0xffffffffu, at, q);
-      if ((m >> lane) & 1u) idx[o + __popc(m & ((1u << lane) - 1))] = static_cast<int32_t>(j0 + 32u * q);
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      const uint32_t n = (keep >> (4 * t)) & 15u;
+      uint32_t o = at;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const unsigned m = __ballot_sync(0xffffffffu, (n >> i) & 1u);
+        o += __popc(m & lt);
+        at += __popc(m);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if ((n >> i) & 1u) idx[o++] = static_cast<int32_t>(j0 + 128 * t + i);
     }
   }
 }
