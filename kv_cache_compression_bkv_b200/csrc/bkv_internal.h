@@ -165,6 +165,8 @@ struct Cache8AttendArgs {
 // host's sizes alone
 struct Cache8AttendPlan {
   int nt;            // n-tiles of 8 query rows in a row block
+  int row_tiles;     // 128-row tiles in a row block of the tcgen05 kernel (0: not used)
+  int block_rows;    // query rows in a row block
   int row_blocks;    // row blocks per (sequence, KV head)
   int ctas;          // CTAs that share the key tiles
   int x_cols;        // logits kept per key for the weights pass (0: none kept)
@@ -221,6 +223,7 @@ int take_status_fps(cudaStream_t, int *);
 int take_status_selftest(cudaStream_t, int *);
 int take_status_cache8_append(cudaStream_t, int *);
 int take_status_cache8_attend(cudaStream_t, int *);
+int take_status_cache8_attend_tc(cudaStream_t, int *);
 int take_status_cache8_evict(cudaStream_t, int *);
 
 }  // namespace bkv

@@ -38,7 +38,7 @@
 
 #include "bkv_device_status.cuh"
 #include "bkv_internal.h"
-#include "cache8.cuh"
+#include "cache8_attend.cuh"
 
 BKV_DEFINE_STATUS_ACCESSOR(take_status_cache8_attend)
 
@@ -47,178 +47,12 @@ namespace {
 
 using namespace cache8;
 
-constexpr int kTile = 128;               // keys per tile
 constexpr int kWarps = 4;                // the tensor-core kernel's
 constexpr int kThreads = kWarps * 32;
 constexpr int kKeys = 32;                // keys per warp and tile
 constexpr int kSimtWarps = 8;            // the other kernels'
 constexpr int kSimtThreads = kSimtWarps * 32;
 constexpr int kSimtKeys = 16;
-constexpr int kSms = 148;
-constexpr int kPad = 2;                  // what a segment costs beside its tiles, in tiles
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kMaxXRows = 32;  // query rows per KV head whose logits are kept for the weights
-
-struct AttendArgs {
-  Cache8AttendArgs a;
-  int row_blocks, ctas, x_cols, log2_block, join_rows;
-  int w_keys, w_chunks;  // keys per weights CTA, and its CTAs per (sequence, KV head)
-  long long x_len;   // keys per (sequence, KV head) in x
-  float *part;       // [ctas][2][rows][2 + head_dim]: max, sum, output
-  float *lse2;       // [n_seqs][n_kv_heads][group * T], log2 units
-  float *x;          // [n_seqs][n_kv_heads][x_len][x_cols], log2 units
-};
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// Programmatic dependent launch: the next kernel of the stream may start, and
-// the wait, in that kernel, for everything before it.
-__device__ __forceinline__ void pdl_launch_dependents() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
-// ------------------------------------------------------------ the work split
-
-struct SeqInfo {
-  int len, n;   // cached rows, new tokens
-  int tiles;    // key tiles per segment (0: nothing to do, or refused)
-  bool bad;
-};
-
-__device__ __forceinline__ SeqInfo seq_info(const Cache8AttendArgs &a, int s) {
-  SeqInfo q;
-  q.len = a.lens[s];
-  q.n = a.n_new ? a.n_new[s] : a.T;
-  q.bad = q.len < 0 || q.len > a.max_len || q.n < 0 || q.n > a.T;
-  q.tiles = q.bad || q.n == 0 ? 0 : (q.len + kTile - 1) / kTile;
-  return q;
-}
-
-// The whole call's list of tiles and its cut into runs.  A segment counts as
-// `pad` tiles more than it has, put before its first: what a CTA spends on
-// beginning and ending one (queries, the merge of its warps), so that runs
-// over many short sequences take no longer than the others.
-struct Split {
-  int total, run, pad;  // counted tiles, counted tiles per run
-};
-
-__device__ __forceinline__ int warp_sum(int x) {
-  return static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(x)));
-}
-// Called by whole warps.  mine: the tiles of sequence `lane`, for the calls below.
-__device__ __forceinline__ Split split_of(const Cache8AttendArgs &a, int units, int ctas, int *mine) {
-  const int lane = threadIdx.x & 31;
-  *mine = lane < a.n_seqs ? seq_info(a, lane).tiles : 0;
-  int tiles = *mine, segments = *mine > 0 ? 1 : 0;
-  for (int s = lane + 32; s < a.n_seqs; s += 32) {
-    const int t = seq_info(a, s).tiles;
-    tiles += t;
-    segments += t > 0 ? 1 : 0;
-  }
-  tiles = warp_sum(tiles) * units;
-  segments = warp_sum(segments) * units;
-  Split w;
-  w.pad = tiles >= 16 * ctas ? kPad : 0;
-  w.total = tiles + w.pad * segments;
-  w.run = max((w.total + ctas - 1) / ctas, 1);
-  return w;
-}
-// Counted tiles before sequence `seq`.
-__device__ __forceinline__ int counted_before(const Cache8AttendArgs &a, const Split &w, int units,
-                                              int mine, int seq) {
-  const int lane = threadIdx.x & 31;
-  int sum = lane < seq && mine > 0 ? mine + w.pad : 0;
-  for (int s = lane + 32; s < seq; s += 32) {
-    const int t = seq_info(a, s).tiles;
-    sum += t > 0 ? t + w.pad : 0;
-  }
-  return warp_sum(sum) * units;
-}
-
-// A position in the call's list of tiles.
-struct Cursor {
-  int seq, unit, tile;  // unit = KV head * row_blocks + row block
-  int at;               // counted tiles from the run's start to this tile
-  SeqInfo q;
-
-  // Called by whole warps: the first tile at counted tile x (x < total) or after it.
-  __device__ __forceinline__ void seek(const Cache8AttendArgs &a, const Split &w, int units,
-                                       int mine, int x) {
-    const int lane = threadIdx.x & 31;
-    int before = 0;
-    for (int s0 = 0;; s0 += 32) {
-      int t = s0 == 0 ? mine : s0 + lane < a.n_seqs ? seq_info(a, s0 + lane).tiles : 0;
-      t = t > 0 ? (t + w.pad) * units : 0;
-      int sum = t;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += y;
-      }
-      const unsigned hit = __ballot_sync(0xffffffffu, before + sum > x);
-      if (hit != 0 || s0 + 32 >= a.n_seqs) {
-        const int l = hit != 0 ? __ffs(hit) - 1 : 0;
-        seq = s0 + l;
-        x -= before + __shfl_sync(0xffffffffu, sum - t, l);
-        break;
-      }
-      before += __shfl_sync(0xffffffffu, sum, 31);
-    }
-    q = seq_info(a, seq);
-    unit = x / (q.tiles + w.pad);
-    const int pos = x - unit * (q.tiles + w.pad) - w.pad;
-    tile = max(pos, 0);
-    at = max(-pos, 0);
-  }
-  __device__ __forceinline__ void next(const Cache8AttendArgs &a, const Split &w, int units) {
-    ++at;
-    if (++tile < q.tiles) return;
-    at += w.pad;
-    tile = 0;
-    if (++unit < units) return;
-    unit = 0;
-    do {
-      if (++seq >= a.n_seqs) {
-        at = INT32_MAX;  // past the end
-        return;
-      }
-      q = seq_info(a, seq);
-    } while (q.tiles == 0);
-  }
-};
-
-// Where row r of a (sequence, KV head) lives in q and out, in rows.
-__device__ __forceinline__ size_t q_row(const Cache8AttendArgs &a, int seq, int kvh, int r) {
-  const int t = r / a.group, g = r - t * a.group;
-  return (static_cast<size_t>(seq) * a.n_q_heads + kvh * a.group + g) * a.T + t;
-}
-
-__device__ __forceinline__ void store_out(__nv_bfloat16 *p, float v) { *p = __float2bfloat16(v); }
-__device__ __forceinline__ void store_out(float *p, float v) { *p = v; }
-__device__ __forceinline__ void store_out4(__nv_bfloat16 *p, float a, float b, float c, float d) {
-  __nv_bfloat162 x = __floats2bfloat162_rn(a, b), y = __floats2bfloat162_rn(c, d);
-  *reinterpret_cast<uint2 *>(p) =
-      make_uint2(*reinterpret_cast<uint32_t *>(&x), *reinterpret_cast<uint32_t *>(&y));
-}
-__device__ __forceinline__ void store_out4(float *p, float a, float b, float c, float d) {
-  *reinterpret_cast<float4 *>(p) = make_float4(a, b, c, d);
-}
-
-// lse of a row from its max and sum (log2 units): log2 units for the weights
-// pass, natural for the caller.
-__device__ __forceinline__ void store_lse(const AttendArgs &p, int seq, int kvh, int r, float m,
-                                          float l) {
-  const Cache8AttendArgs &a = p.a;
-  const float z = l > 0.f || l != l ? m + log2f(l) : -INFINITY;
-  p.lse2[(static_cast<size_t>(seq) * a.n_kv_heads + kvh) * a.group * a.T + r] = z;
-  if (a.lse) a.lse[q_row(a, seq, kvh, r)] = z * kLn2;
-}
 
 // The end of a CTA's part of a segment: kBufs buffers of unnormalised outputs
 // (summed here; element (r, d) of a buffer at off(r, d)) and the row statistics
@@ -1214,12 +1048,14 @@ Cache8AttendPlan plan_cache8_attend(int n_seqs, int n_q_heads, int n_kv_heads, i
   const long long rows = static_cast<long long>(n_q_heads / n_kv_heads) * T;
   const bool mma = use_mma(dtype, head_dim);
   p.nt = !mma || rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 24 ? 3 : 4;
-  p.row_blocks = static_cast<int>((rows + 8 * p.nt - 1) / (8 * p.nt));
+  p.row_tiles = mma && rows > 32 ? (rows <= 128 ? 1 : 2) : 0;
+  p.block_rows = p.row_tiles ? 128 * p.row_tiles : 8 * p.nt;
+  p.row_blocks = static_cast<int>((rows + p.block_rows - 1) / p.block_rows);
   const long long tiles = (max_len + kTile - 1) / kTile * n_seqs * n_kv_heads * p.row_blocks;
-  const int resident = 2 * kSms;
+  const int resident = p.row_tiles ? kSms : 2 * kSms;
   p.ctas = static_cast<int>(std::min<long long>(tiles, resident));
   p.x_cols = weights && rows <= kMaxXRows ? static_cast<int>((rows + 1) / 2 * 2) : 0;
-  const size_t part = static_cast<size_t>(p.ctas) * 2 * 8 * p.nt * (2 + head_dim) * 4;
+  const size_t part = static_cast<size_t>(p.ctas) * 2 * p.block_rows * (2 + head_dim) * 4;
   const size_t lse = static_cast<size_t>(n_seqs) * n_q_heads * T * 4;
   const size_t x = static_cast<size_t>(n_seqs) * n_kv_heads * align_up(max_len, kKeys) * p.x_cols * 4;
   p.part_off = 0;
@@ -1247,7 +1083,11 @@ bkv_status launch_cache8_attend(const Cache8AttendArgs &a, const Cache8AttendPla
   bool ok;
   if (mma) {
     const bool wide = a.head_dim == 128;
-    if (plan.nt == 1)
+    if (plan.row_tiles)
+      ok = launch_attend_tc(p, plan.row_tiles, stream) &&
+           (plan.row_tiles == 1 ? run_finish<128, __nv_bfloat16>(p, stream)
+                                : run_finish<256, __nv_bfloat16>(p, stream));
+    else if (plan.nt == 1)
       ok = (wide ? run_mma<128, 1>(p, stream) : run_mma<64, 1>(p, stream)) &&
            run_finish<8, __nv_bfloat16>(p, stream);
     else if (plan.nt == 2)

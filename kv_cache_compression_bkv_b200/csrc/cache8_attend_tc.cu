@@ -1,0 +1,631 @@
+// cache8_attend_tc.cu -- attention over the 8-bit cache for many query rows on
+// the 5th-generation tensor cores (bf16 queries, head_dim 64 or 128).
+//
+// A CTA holds one or two tiles of 128 query rows of a (sequence, KV head) and
+// walks its run of 128-key tiles (cache8_attend.cuh).  Both products are
+// kind::f16 tcgen05.mma with f32 accumulators in TMEM:
+//   S = Q K^T   Q and K f16 in shared memory, K-major, 128-byte swizzle
+//   O += P V    P f16 in TMEM over the columns S was read from, V f16 in shared
+//               memory as it is cached (keys x elements: MN-major)
+// e4m3 codes are exact in f16, so converter warps turn each tile's codes into
+// f16 once for all the CTA's rows, multiplied by the power of two between the
+// block's scale and the tile's largest (K) or the run's largest (V): exact down
+// to 2^-24 under it.  The f8f6f4 product would take the codes as they are, but
+// then the probabilities have to be split into 8-bit parts to keep f16's 11
+// bits, which costs the softmax warps more than the conversion costs others.
+//
+// Warps: 4 per row tile do the softmax, one thread a row (TMEM lane); the
+// converters load codes into registers ahead of need, half of them K, half V;
+// one warp issues the MMAs.  With two row tiles the tensor cores work on one
+// while the other's softmax runs; with one, S is double-buffered.
+// A row's reference is set 7 (in log2) under the largest logit and moves only
+// when a 32-column sum of probabilities passes 2^15, so the common path takes
+// no maxima; moving it rescales O in TMEM, after the MMAs that are under way.
+//
+// Bound by the tensor cores and exp (a 256 x 128 tile: 2 x 2 x 512 cycles of
+// MMA, 32768 exps at 16 a cycle); one row tile with few rows by the codes'
+// bytes.
+#include <cuda_bf16.h>
+
+#include <type_traits>
+
+#include "bkv_device_status.cuh"
+#include "cache8_attend.cuh"
+#include "sm100.cuh"
+
+BKV_DEFINE_STATUS_ACCESSOR(take_status_cache8_attend_tc)
+
+namespace bkv {
+namespace {
+
+using namespace cache8;
+using namespace sm100;
+
+enum : int { kWhereConv = 631, kWhereMma = 632, kWhereSoft = 633, kWhereOut = 634, kWhereDrain = 635 };
+
+// A CTA's part of a segment.
+struct Part {
+  int seq, unit, kvh, r0;   // r0: first query row of the row block
+  int len, n, rows;         // rows: of the (sequence, KV head)
+  int tile0, live;          // first tile, tiles that a row of the block sees
+  bool from_start, to_end;
+};
+
+// Walks the parts of a CTA's run, in whole warps.
+template <int kRows>
+struct PartIter {
+  Cursor c;
+  int run;
+  __device__ __forceinline__ bool next(const AttendArgs &p, const Split &w, int units, Part *x) {
+    if (c.at >= run) return false;
+    const Cache8AttendArgs &a = p.a;
+    const int count = min(c.q.tiles - c.tile, run - c.at);
+    x->seq = c.seq;
+    x->unit = c.unit;
+    x->kvh = c.unit / p.row_blocks;
+    x->r0 = (c.unit - x->kvh * p.row_blocks) * kRows;
+    x->len = c.q.len;
+    x->n = c.q.n;
+    x->rows = a.group * c.q.n;
+    x->tile0 = c.tile;
+    x->from_start = c.tile == 0;
+    x->to_end = c.tile + count == c.q.tiles;
+    const int last = min(x->r0 + kRows, x->rows) - 1;  // below r0: a block without rows
+    const int sees = last < x->r0 ? 0 : max(c.q.len - c.q.n + 1 + last / a.group, 0);
+    x->live = max(min(count, (sees + kTile - 1) / kTile - c.tile), 0);
+    c.tile += count - 1;
+    c.at += count - 1;
+    c.next(a, w, units);
+    return true;
+  }
+};
+
+__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+      "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Instruction descriptor of kind::f16 with f16 A/B, f32 D; b_mn: B is MN-major.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn) {
+  return (1u << 4) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// Shared-memory descriptor of an MN-major f16 operand with the 128-byte swizzle:
+// rows of one K index hold 64 MN elements (128 B); 8 K indices are an atom of
+// 1024 B, atoms along K follow each other, the next 64 MN elements lie
+// `mn_stride` bytes on.
+__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t addr, uint32_t mn_stride) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(mn_stride >> 4) << 16;  // leading byte offset: along MN
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;      // stride byte offset: along K
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+
+constexpr int kHalf = 128 * 128;  // bytes of 128 rows x 64 f16
+
+template <int D, int RT>
+struct TcCfg {
+  static constexpr int kHalves = D / 64;
+  static constexpr int kTileBytes = kHalves * kHalf;   // 128 rows (or keys) in f16
+  static constexpr int kSoftWarps = 4 * RT;
+  static constexpr int kConvWarps = 11 - kSoftWarps;
+  // 12 warps, three to a scheduler, leave 168 registers a thread (13: 128)
+  static constexpr int kThreads = 12 * 32;
+  static constexpr int kSmem = (RT + 4) * kTileBytes + 1024;  // Q, two stages of K and V; alignment
+};
+
+struct TcShared {
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], drain;
+  uint32_t tmem;
+  float k_scale[4];   // of the last tiles
+  float v_scale[4];   // of the last parts
+};
+
+// 16 codes as f16, times a power of two: 32 bytes at chunk pair ch of row `row`
+// of a tile; odd halves store the second chunk first, which keeps the 8 lanes
+// of a row free of bank conflicts.
+__device__ __forceinline__ void store_f16(uint8_t *tile, int row, int ch, uint4 c, __half2 f) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+  uint32_t h[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    h[2 * i] = as_u32(__hmul2(as_half2(e4m3x2_to_f16x2(w[i])), f));
+    h[2 * i + 1] = as_u32(__hmul2(as_half2(e4m3x2_to_f16x2(w[i] >> 16)), f));
+  }
+  const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
+  uint8_t *half = tile + (ch >> 2) * kHalf;
+  const int c2 = (ch & 3) * 2, flip = (ch >> 2) & 1;
+  *reinterpret_cast<uint4 *>(half + sw128_offset(row, c2 + flip)) = flip ? hi : lo;
+  *reinterpret_cast<uint4 *>(half + sw128_offset(row, c2 + 1 - flip)) = flip ? lo : hi;
+}
+
+template <int D, int RT>
+__global__ void __launch_bounds__((TcCfg<D, RT>::kThreads), 1) attend_tc_kernel(const AttendArgs p) {
+  using Cfg = TcCfg<D, RT>;
+  constexpr int kRows = 128 * RT;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ TcShared sh;
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t *s_q = smem, *s_k = s_q + RT * Cfg::kTileBytes, *s_v = s_k + 2 * Cfg::kTileBytes;
+
+  pdl_launch_dependents();
+  const Cache8AttendArgs &a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int units = a.n_kv_heads * p.row_blocks;
+  int mine;
+  const Split w = split_of(a, units, p.ctas, &mine);
+  const int t0 = blockIdx.x * w.run;
+  if (t0 >= w.total) return;
+  PartIter<kRows> parts;
+  parts.run = min(w.run, w.total - t0);
+  parts.c.seek(a, w, units, mine, t0);
+
+  constexpr int kMmaWarp = Cfg::kSoftWarps + Cfg::kConvWarps;
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(&sh.tmem), 512);
+    tmem_relinquish();
+    if (lane == 0) {
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(smem_u32(&sh.k_full[i]), Cfg::kConvWarps);
+        mbar_init(smem_u32(&sh.v_full[i]), Cfg::kConvWarps);
+        mbar_init(smem_u32(&sh.k_empty[i]), 1);
+        mbar_init(smem_u32(&sh.v_empty[i]), 1);
+        mbar_init(smem_u32(&sh.q_full[i]), 4);
+        mbar_init(smem_u32(&sh.s_full[i]), 1);
+        mbar_init(smem_u32(&sh.p_full[i]), 4);
+        mbar_init(smem_u32(&sh.pv_done[i]), 1);
+      }
+      mbar_init(smem_u32(&sh.drain), 1);
+      fence_barrier_init();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  // columns: S (and P) of row tile or buffer i at 128 i, O of row tile i at 256 + 128 i
+  auto s_col = [&](int i) { return tmem + 128u * i; };
+  auto o_col = [&](int i) { return tmem + 256u + 128u * i; };
+
+  if (warp == kMmaWarp) {
+    // ------------------------------------------------------------- the MMAs
+    constexpr uint32_t idesc_qk = idesc_f16_f32(128, 128, false);
+    constexpr uint32_t idesc_pv = idesc_f16_f32(128, D, true);
+    const uint32_t q0 = smem_u32(s_q), k0 = smem_u32(s_k), v0 = smem_u32(s_v);
+    auto qk = [&](int x, int t, int buf) {  // S[buf] = Q_x K(t)^T
+      if (lane == 0) {
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) {
+          const uint32_t off = (s >> 2) * kHalf + (s & 3) * 32;
+          umma_f16(s_col(buf), smem_desc_k_sw128(q0 + x * Cfg::kTileBytes + off),
+                   smem_desc_k_sw128(k0 + (t & 1) * Cfg::kTileBytes + off), idesc_qk, s != 0);
+        }
+        umma_commit(smem_u32(&sh.s_full[buf]));
+      }
+    };
+    auto pv = [&](int x, int t, int buf, bool first) {  // O_x += P[buf] V(t)
+      if (lane == 0) {
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+          umma_f16_ts(o_col(x), s_col(buf) + 8u * s,
+                      smem_desc_mn_sw128(v0 + (t & 1) * Cfg::kTileBytes + s * 2048, kHalf), idesc_pv,
+                      !(first && s == 0));
+        umma_commit(smem_u32(&sh.pv_done[x]));
+      }
+    };
+    auto wait = [&](uint64_t *bar, int phase) {
+      const bool ok = mbar_wait_warp(smem_u32(bar), phase & 1, kWhereMma);
+      tc_fence_after();
+      return ok;
+    };
+    auto commit = [&](uint64_t *bar) {
+      if (lane == 0) umma_commit(smem_u32(bar));
+    };
+    Part x;
+    int t = 0, seg = 0;
+    bool ok = true;
+    while (ok && parts.next(p, w, units, &x)) {
+      if (x.live == 0) continue;
+      for (int i = 0; i < RT && ok; ++i) ok = wait(&sh.q_full[i], seg);
+      ok = ok && wait(&sh.k_full[t & 1], t >> 1);
+      if (!ok) break;
+      for (int i = 0; i < RT; ++i) qk(i, t, RT == 2 ? i : t & 1);
+      commit(&sh.k_empty[t & 1]);
+      for (int j = 0; j < x.live && ok; ++j, ++t) {
+        const bool more = j + 1 < x.live;
+        if (RT == 1 && more) {
+          if (!(ok = wait(&sh.k_full[(t + 1) & 1], (t + 1) >> 1))) break;
+          qk(0, t + 1, (t + 1) & 1);
+          commit(&sh.k_empty[(t + 1) & 1]);
+        }
+        if (!(ok = wait(&sh.v_full[t & 1], t >> 1))) break;
+        for (int i = 0; i < RT; ++i) {
+          if (!(ok = wait(&sh.p_full[i], t))) break;
+          pv(i, t, RT == 2 ? i : t & 1, j == 0);
+          if (RT == 2 && more) {
+            if (i == 0 && !(ok = wait(&sh.k_full[(t + 1) & 1], (t + 1) >> 1))) break;
+            qk(i, t + 1, i);
+          }
+        }
+        if (!ok) break;
+        commit(&sh.v_empty[t & 1]);
+        if (RT == 2 && more) commit(&sh.k_empty[(t + 1) & 1]);
+      }
+      ++seg;
+    }
+    commit(&sh.drain);
+    mbar_wait_warp(smem_u32(&sh.drain), 0, kWhereDrain);
+  } else if (warp >= Cfg::kSoftWarps) {
+    // ------------------------------------------------------- the converters
+    // K and V of a tile in turn, each by all converter warps; NB of them are
+    // held in registers ahead of need
+    constexpr int CH = D / 16;                       // 16-code chunks per key
+    constexpr int kThr = Cfg::kConvWarps * 32;
+    constexpr int NP = (128 * CH + kThr - 1) / kThr; // pieces per thread
+    constexpr int NB = RT == 2 ? 2 : 4;
+    const int tid = (warp - Cfg::kSoftWarps) * 32 + lane;
+    PartIter<kRows> load_parts = parts;
+    Part lx, x;
+    lx.live = x.live = 0;
+    int lj = -1, cj = -1;  // tiles within the parts being loaded and converted
+    bool more = true;
+    uint4 c[NB][NP];
+    int ex[NB];  // lanes 0..7: exponent of the scale of keys 16 lane .. of the tile
+    auto load = [&](int b) {
+      if ((b & 1) == 0) {
+        ++lj;
+        while (more && lj >= lx.live) {
+          more = load_parts.next(p, w, units, &lx);
+          lj = 0;
+          if (!more) lx.live = 0;
+        }
+      }
+      if (!more) return;
+      const int j0 = (lx.tile0 + lj) * kTile;
+      const size_t head = static_cast<size_t>(lx.seq) * a.n_kv_heads + lx.kvh;
+      const uint4 *src = reinterpret_cast<const uint4 *>((b & 1 ? a.v8 : a.k8) + (head * a.cap + j0) * D);
+      const int keys = lx.len - j0;
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const int q = i * kThr + tid;
+        c[b][i] = make_uint4(0, 0, 0, 0);  // keys past the end are zeros
+        if (q / CH < min(keys, kTile)) c[b][i] = __ldcs(src + q);
+      }
+      ex[b] = -127;
+      if (lane < 8 && lane * 16 < keys)
+        ex[b] = exp_of(__ldg((b & 1 ? a.v_scale : a.k_scale) + head * (a.cap >> p.log2_block) +
+                             ((j0 + lane * 16) >> p.log2_block)));
+    };
+#pragma unroll
+    for (int b = 0; b < NB; ++b) load(b);
+    int t = -1, seg = -1, ref = -127;
+    bool ok = true;
+    while (ok) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const bool is_v = (b & 1) != 0;
+        if (!is_v) {  // the next tile
+          ++cj;
+          ++t;
+          while (ok && cj >= x.live) {
+            ok = parts.next(p, w, units, &x);
+            cj = 0;
+            if (!ok || x.live == 0) continue;
+            // a new part: its largest V scale
+            const float *sc = a.v_scale + (static_cast<size_t>(x.seq) * a.n_kv_heads + x.kvh) *
+                                              (a.cap >> p.log2_block);
+            const int b1 = (min((x.tile0 + x.live) * kTile, x.len) - 1) >> p.log2_block;
+            ref = -127;
+            for (int i = ((x.tile0 * kTile) >> p.log2_block) + lane; i <= b1; i += 32)
+              ref = max(ref, exp_of(__ldg(sc + i)));
+            ref = __reduce_max_sync(0xffffffffu, ref);
+            ++seg;
+            if (tid == 0) sh.v_scale[seg & 3] = pow2f(max(ref, -126));
+          }
+          if (!ok) break;
+        }
+        const int stage = t & 1;
+        if (!(ok = mbar_wait_warp(smem_u32(is_v ? &sh.v_empty[stage] : &sh.k_empty[stage]),
+                                  ((t >> 1) & 1) ^ 1, kWhereConv)))
+          break;
+        const int top = is_v ? ref : __reduce_max_sync(0xffffffffu, ex[b]);
+        uint8_t *tile = (is_v ? s_v : s_k) + stage * Cfg::kTileBytes;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          const int q = i * kThr + tid;
+          const int row = q / CH;
+          const int k = __shfl_sync(0xffffffffu, ex[b], (row >> 4) & 7) - top;
+          if (128 * CH % kThr == 0 || q < 128 * CH)
+            store_f16(tile, row, q % CH, c[b][i], __float2half2_rn(pow2f(max(k, -24))));
+        }
+        if (!is_v && tid == 0) sh.k_scale[t & 3] = pow2f(max(top, -126));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(is_v ? &sh.v_full[stage] : &sh.k_full[stage]));
+        load(b);
+      }
+    }
+  } else {
+    // ---------------------------------------------------------- the softmax
+    const int x_tile = warp >> 2;               // row tile
+    const int trow = (warp & 3) * 32 + lane;    // row in it, TMEM lane
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    Part x;
+    int t = 0, seg = 0;
+    bool ok = true;
+    // Waits, once, until tile t - 1 of the part (its tile j - 1) is in O.  A phase
+    // must not pass unwaited, or its parity would be taken for the next one's:
+    // with two row tiles a tile's logits are made after the tile before is in
+    // O; with one this is called for every tile before its P is handed on.
+    int pv_seen = 0;  // tiles known to be in O
+    auto wait_pv = [&](int j, int t) {
+      if (j == 0 || pv_seen == t) return true;
+      pv_seen = t;
+      const bool done = mbar_wait_warp(smem_u32(&sh.pv_done[x_tile]), (t - 1) & 1, kWhereSoft);
+      tc_fence_after();
+      return done;
+    };
+    while (ok && parts.next(p, w, units, &x)) {
+      const int r = x.r0 + x_tile * 128 + trow;
+      const bool row = r < x.rows;
+      const int sees = x.len - x.n + 1 + r / a.group;  // keys this row sees
+      const bool warp_rows = x.r0 + x_tile * 128 + (warp & 3) * 32 < x.rows;
+      const bool whole = x.from_start && x.to_end;
+      float ref = -INFINITY, l = 0.f, vscale = 0.f;
+      if (x.live > 0) {
+        // queries: f16 under a power of two per 32 rows, largest in [2^14, 2^15)
+        {
+          uint4 v[D / 8];
+          uint32_t amax = 0;
+          const uint4 *src = reinterpret_cast<const uint4 *>(
+              static_cast<const __nv_bfloat16 *>(a.q) + (row ? q_row(a, x.seq, x.kvh, r) * D : 0));
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            v[i] = row ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+            const uint32_t y[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t lo = (y[k] & 0x7fffu) << 16, hi = y[k] & 0x7fff0000u;
+              if (lo < 0x7f800000u) amax = max(amax, lo);
+              if (hi < 0x7f800000u) amax = max(amax, hi);
+            }
+          }
+          amax = __reduce_max_sync(0xffffffffu, amax);
+          const int e = amax == 0 ? 0 : max(static_cast<int>(amax >> 23) - 127, -112);
+          const float up = pow2f(14 - e);
+          uint8_t *tile = s_q + x_tile * Cfg::kTileBytes;
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            const uint32_t y[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            uint32_t h[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              h[k] = as_u32(__floats2half2_rn(__uint_as_float(y[k] << 16) * up,
+                                              __uint_as_float(y[k] & 0xffff0000u) * up));
+            *reinterpret_cast<uint4 *>(tile + (i >> 3) * kHalf + sw128_offset(trow, i & 7)) =
+                make_uint4(h[0], h[1], h[2], h[3]);
+          }
+          vscale = pow2f(e - 14) * (a.scale * kLog2e);  // for now: the logits' factor
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sh.q_full[x_tile]));
+        }
+        const float q_factor = vscale;
+        for (int j = 0; j < x.live; ++j, ++t) {
+          const int buf = RT == 2 ? x_tile : t & 1;
+          if (!(ok = mbar_wait_warp(smem_u32(&sh.s_full[buf]), RT == 2 ? t & 1 : (t >> 1) & 1,
+                                    kWhereSoft)))
+            break;
+          tc_fence_after();
+          if (warp_rows) {
+            const uint32_t s_addr = s_col(buf) + lanes;
+            const float f = q_factor * sh.k_scale[t & 3];
+            const int j0 = (x.tile0 + j) * kTile;
+            const int nvis = sees - j0;
+            const bool masked = __any_sync(0xffffffffu, nvis < kTile);
+            uint32_t ph[64];
+            float sum = 0.f;
+            // probabilities under the row's reference; false: it has to move
+            auto pass = [&](auto with_mask) {
+              const float ru = ref == -INFINITY ? 0.f : ref;
+              bool fine = true;
+              sum = 0.f;
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                float v[32];
+                tmem_ld_32x32b_x32(s_addr + 32u * c, v);
+                tmem_ld_wait_regs(v);
+                float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                  float y0 = fmaf(v[i], f, -ru), y1 = fmaf(v[i + 1], f, -ru);
+                  if (decltype(with_mask)::value) {
+                    if (c * 32 + i >= nvis) y0 = -INFINITY;
+                    if (c * 32 + i + 1 >= nvis) y1 = -INFINITY;
+                  }
+                  const float e0 = ex2(y0), e1 = ex2(y1);
+                  part[(i >> 1) & 3] += e0 + e1;
+                  ph[c * 16 + (i >> 1)] = as_u32(__floats2half2_rn(e0, e1));
+                }
+                const float s = (part[0] + part[1]) + (part[2] + part[3]);
+                fine &= s <= 32768.f;
+                sum += s;
+              }
+              return fine;
+            };
+            using Yes = std::true_type;
+            using No = std::false_type;
+            bool fine = false;
+            if (j > 0) fine = masked ? pass(Yes{}) : pass(No{});
+            if (__any_sync(0xffffffffu, !fine)) {
+              float top = -INFINITY;
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                float v[32];
+                tmem_ld_32x32b_x32(s_addr + 32u * c, v);
+                tmem_ld_wait_regs(v);
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  top = fmaxf(top, c * 32 + i < nvis ? v[i] * f : -INFINITY);
+              }
+              top -= 7.f;
+              float corr = 1.f;
+              if (!fine && top > ref) {
+                corr = ref == -INFINITY ? 0.f : ex2(ref - top);
+                ref = top;
+                l *= corr;
+              }
+              __syncwarp();
+              if (j > 0) {
+                // O, once the MMAs of the tile before have added to it
+                if (!(ok = wait_pv(j, t))) break;
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                  float v[32];
+                  uint32_t u[32];
+                  tmem_ld_32x32b_x32(o_col(x_tile) + lanes + 32u * c, v);
+                  tmem_ld_wait_regs(v);
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(v[i] * corr);
+                  tmem_st_32x32b_x32(o_col(x_tile) + lanes + 32u * c, u);
+                }
+                tmem_st_wait();
+              }
+              pass(Yes{});
+            }
+            l += sum;
+            __syncwarp();  // tcgen05 loads and stores are the whole warp's
+            if (p.x_cols > 0) {
+              // the logits, for the weights: rows side by side for each key
+              float *xs = p.x + ((static_cast<size_t>(x.seq) * a.n_kv_heads + x.kvh) * p.x_len + j0) *
+                                    p.x_cols + r;
+#pragma unroll 1
+              for (int c = 0; c < 4; ++c) {
+                float v[32];
+                tmem_ld_32x32b_x32(s_addr + 32u * c, v);
+                tmem_ld_wait_regs(v);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                  const int key = c * 32 + i;
+                  if (r < p.x_cols && key < x.len - j0)
+                    xs[static_cast<size_t>(key) * p.x_cols] = key < nvis ? v[i] * f : -INFINITY;
+                }
+                __syncwarp();
+              }
+            }
+            tmem_st_32x32b_x32(s_addr, ph);
+            tmem_st_32x32b_x32(s_addr + 32u, ph + 32);
+            tmem_st_wait();
+          }
+          if (RT == 1 && !(ok = wait_pv(j, t))) break;
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sh.p_full[x_tile]));
+        }
+        if (!ok) break;
+        if (!(ok = mbar_wait_warp(smem_u32(&sh.pv_done[x_tile]), (t - 1) & 1, kWhereOut))) break;
+        tc_fence_after();
+        vscale = sh.v_scale[seg & 3];
+        ++seg;
+      }
+      if (!warp_rows) continue;
+      // ---- the part's end: a whole segment goes out, a part to its slot
+      float *part = p.part + (static_cast<size_t>(blockIdx.x) * 2 + (x.from_start ? 1 : 0)) *
+                                 (kRows * (2 + D));
+      const int pr = x_tile * 128 + trow;
+      const float mul = !whole ? vscale : l > 0.f || l != l ? vscale / l : 0.f;
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        float v[32];
+        __syncwarp();
+        if (x.live > 0) {
+          tmem_ld_32x32b_x32(o_col(x_tile) + lanes + 32u * c, v);
+          tmem_ld_wait_regs(v);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = 0.f;
+        }
+        // rows without a visible key so far hold zeros, whatever the scale
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = x.live > 0 ? v[i] * mul : 0.f;
+        if (row && whole) {
+          __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + q_row(a, x.seq, x.kvh, r) * D + 32 * c;
+#pragma unroll
+          for (int i = 0; i < 32; i += 8) {
+            uint4 y;
+            __nv_bfloat162 h;
+            h = __floats2bfloat162_rn(v[i], v[i + 1]), y.x = *reinterpret_cast<uint32_t *>(&h);
+            h = __floats2bfloat162_rn(v[i + 2], v[i + 3]), y.y = *reinterpret_cast<uint32_t *>(&h);
+            h = __floats2bfloat162_rn(v[i + 4], v[i + 5]), y.z = *reinterpret_cast<uint32_t *>(&h);
+            h = __floats2bfloat162_rn(v[i + 6], v[i + 7]), y.w = *reinterpret_cast<uint32_t *>(&h);
+            *reinterpret_cast<uint4 *>(out + i) = y;
+          }
+        } else if (row) {
+          float4 *dst = reinterpret_cast<float4 *>(part + 2 * kRows + pr * D + 32 * c);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        }
+      }
+      __syncwarp();
+      tc_fence_before();
+      if (row && whole) store_lse(p, x.seq, x.kvh, r, ref, l);
+      if (row && !whole) {
+        part[pr] = ref;
+        part[kRows + pr] = l;
+      }
+      __syncwarp();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D, int RT>
+bool run_tc(const AttendArgs &p, cudaStream_t s) {
+  static int done[64];
+  using Cfg = TcCfg<D, RT>;
+  static_assert(Cfg::kSmem + sizeof(TcShared) <= 227 * 1024, "shared memory");
+  if (!ensure_smem_limit(attend_tc_kernel<D, RT>, Cfg::kSmem, done)) return false;
+  attend_tc_kernel<D, RT><<<p.ctas, Cfg::kThreads, Cfg::kSmem, s>>>(p);
+  return cudaGetLastError() == cudaSuccess;
+}
+
+}  // namespace
+
+bool launch_attend_tc(const cache8::AttendArgs &p, int row_tiles, cudaStream_t s) {
+  if (p.a.head_dim == 128) return row_tiles == 1 ? run_tc<128, 1>(p, s) : run_tc<128, 2>(p, s);
+  return row_tiles == 1 ? run_tc<64, 1>(p, s) : run_tc<64, 2>(p, s);
+}
+
+}  // namespace bkv
