@@ -600,6 +600,7 @@ bkv_status bkv_read_device_status(void *stream, int32_t *where_out) {
   if (code == 0) code = take_status_cache8_append(s, &where);
   if (code == 0) code = take_status_cache8_attend(s, &where);
   if (code == 0) code = take_status_cache8_attend_tc(s, &where);
+  if (code == 0) code = take_status_cache8_weights_tc(s, &where);
   if (code == 0) code = take_status_cache8_evict(s, &where);
   if (code < 0) return BKV_ERR_CUDA;
   if (where_out) *where_out = code ? where : 0;

@@ -224,6 +224,7 @@ int take_status_selftest(cudaStream_t, int *);
 int take_status_cache8_append(cudaStream_t, int *);
 int take_status_cache8_attend(cudaStream_t, int *);
 int take_status_cache8_attend_tc(cudaStream_t, int *);
+int take_status_cache8_weights_tc(cudaStream_t, int *);
 int take_status_cache8_evict(cudaStream_t, int *);
 
 }  // namespace bkv

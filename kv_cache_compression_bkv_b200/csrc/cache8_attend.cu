@@ -875,93 +875,7 @@ __global__ void __launch_bounds__(kSimtThreads) attend_finish_kernel(const Atten
   if (lane == 0) store_lse(p, seq, kvh, r, M, l);
 }
 
-// From the keys again, for more query rows than logits are kept of.  A CTA
-// holds 128 keys' fragments and walks the query rows 32 at a time.
-template <int D>
-__global__ void __launch_bounds__(kSimtThreads) weights_mma_kernel(const AttendArgs p) {
-  constexpr int KS = D / 16, NT = 4;
-  __shared__ uint2 s_q[NT * KS * 32];
-  __shared__ float s_rs[NT * 8], s_z[NT * 8];
-  const Cache8AttendArgs &a = p.a;
-  const size_t head = blockIdx.y;
-  const int seq = static_cast<int>(head) / a.n_kv_heads;
-  const int kvh = static_cast<int>(head) - seq * a.n_kv_heads;
-  const SeqInfo q = seq_info(a, seq);
-  if (q.tiles == 0 || static_cast<int>(blockIdx.x) * kTile >= q.len) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  const int j0 = blockIdx.x * kTile + warp * kSimtKeys;
-  const int rows = a.group * q.n;
-  const int seen0 = q.len - q.n + 1;
-  uint32_t ka[KS][4];
-  float ks = 0.f;
-  if (j0 < q.len) {
-    ks = __ldg(a.k_scale + head * (a.cap / a.block) + j0 / a.block);
-#pragma unroll
-    for (int h = 0; h < D / 64; ++h) {
-      // rows past the end are not read
-      const uint8_t *r0 = a.k8 + (head * a.cap + min(j0 + g, q.len - 1)) * D + (c + 4 * h) * 16;
-      const uint8_t *r1 = a.k8 + (head * a.cap + min(j0 + g + 8, q.len - 1)) * D + (c + 4 * h) * 16;
-      const uint4 x = __ldg(reinterpret_cast<const uint4 *>(r0));
-      const uint4 y = __ldg(reinterpret_cast<const uint4 *>(r1));
-      const uint32_t wx[4] = {x.x, x.y, x.z, x.w}, wy[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        ka[h * 4 + w][0] = e4m3x2_to_f16x2(wx[w]);
-        ka[h * 4 + w][1] = e4m3x2_to_f16x2(wy[w]);
-        ka[h * 4 + w][2] = e4m3x2_to_f16x2(wx[w] >> 16);
-        ka[h * 4 + w][3] = e4m3x2_to_f16x2(wy[w] >> 16);
-      }
-    }
-  }
-  float sum0 = 0.f, sum1 = 0.f;
-  for (int rb = 0; rb < rows; rb += NT * 8) {
-    // the last token of these rows sees fewer keys than this tile's first: none does
-    const int t_last = min(rb + NT * 8, rows) - 1;
-    if (static_cast<int>(blockIdx.x) * kTile >= seen0 + t_last / a.group) continue;
-    __syncthreads();
-    if (warp < NT) {
-      uint2 f[KS];
-      RawQ<D> raw;
-      load_q_raw<D>(p, seq, kvh, rb + warp * 8 + g, rows, raw);
-      const float s = q_frags<D>(p, raw, f);
-#pragma unroll
-      for (int k = 0; k < KS; ++k) s_q[(warp * KS + k) * 32 + lane] = f[k];
-      if (c == 0) {
-        const int r = rb + warp * 8 + g;
-        s_rs[warp * 8 + g] = s;
-        const float z = r < rows ? p.lse2[head * a.group * a.T + r] : INFINITY;
-        s_z[warp * 8 + g] = z == -INFINITY ? INFINITY : z;  // rows that see nothing add nothing
-      }
-    }
-    __syncthreads();
-    if (j0 >= q.len) continue;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float x[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        const uint2 b = s_q[(nt * KS + k) * 32 + lane];
-        mma16816(x, ka[k][0], ka[k][1], ka[k][2], ka[k][3], b.x, b.y);
-      }
-      const int r = nt * 8 + 2 * c;
-      const int v0 = seen0 + (rb + r) / a.group, v1 = seen0 + (rb + r + 1) / a.group;
-      const float f0 = ks * s_rs[r], f1 = ks * s_rs[r + 1], z0 = s_z[r], z1 = s_z[r + 1];
-      if (j0 + g < v0) sum0 += ex2(x[0] * f0 - z0);
-      if (j0 + g < v1) sum0 += ex2(x[1] * f1 - z1);
-      if (j0 + g + 8 < v0) sum1 += ex2(x[2] * f0 - z0);
-      if (j0 + g + 8 < v1) sum1 += ex2(x[3] * f1 - z1);
-    }
-  }
-  sum0 += __shfl_xor_sync(0xffffffffu, sum0, 1);
-  sum0 += __shfl_xor_sync(0xffffffffu, sum0, 2);
-  sum1 += __shfl_xor_sync(0xffffffffu, sum1, 1);
-  sum1 += __shfl_xor_sync(0xffffffffu, sum1, 2);
-  if (c == 0) {
-    if (j0 + g < q.len) store_weight(a, head, j0 + g, q, sum0);
-    if (j0 + g + 8 < q.len) store_weight(a, head, j0 + g + 8, q, sum1);
-  }
-}
-
+// From the keys again, for more query rows than logits are kept of.
 template <typename T>
 __global__ void __launch_bounds__(kSimtThreads) weights_simt_kernel(const AttendArgs p) {
   __shared__ __align__(16) float s_q[kSimtRows * kMaxD];
@@ -1110,11 +1024,8 @@ bkv_status launch_cache8_attend(const Cache8AttendArgs &a, const Cache8AttendPla
   if (a.w_out && plan.x_cols == 0) {
     const unsigned heads = static_cast<unsigned>(a.n_seqs) * a.n_kv_heads;
     const unsigned tiles = static_cast<unsigned>((a.max_len + kTile - 1) / kTile);
-    if (mma && a.head_dim == 128)
-      weights_mma_kernel<128><<<dim3(tiles, heads), kSimtThreads, 0, stream>>>(p);
-    else if (mma)
-      weights_mma_kernel<64><<<dim3(tiles, heads), kSimtThreads, 0, stream>>>(p);
-    else if (dtype == BKV_BF16)
+    if (mma) return launch_weights_tc(p, stream) ? BKV_OK : BKV_ERR_CUDA;
+    if (dtype == BKV_BF16)
       weights_simt_kernel<__nv_bfloat16><<<dim3(tiles, heads), kSimtThreads, 0, stream>>>(p);
     else
       weights_simt_kernel<float><<<dim3(tiles, heads), kSimtThreads, 0, stream>>>(p);

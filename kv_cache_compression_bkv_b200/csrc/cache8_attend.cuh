@@ -183,5 +183,7 @@ __device__ __forceinline__ void store_lse(const AttendArgs &p, int seq, int kvh,
 // cache8_attend_tc.cu: bf16, head_dim 64 or 128, p.row_tiles tiles of 128 query
 // rows a CTA.
 bool launch_attend_tc(const cache8::AttendArgs &p, int row_tiles, cudaStream_t stream);
+// cache8_weights_tc.cu: the weights from lse2 and the keys, after the above.
+bool launch_weights_tc(const cache8::AttendArgs &p, cudaStream_t stream);
 
 }  // namespace bkv

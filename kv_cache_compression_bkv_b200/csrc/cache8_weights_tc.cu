@@ -1,0 +1,263 @@
+// cache8_weights_tc.cu -- attention weights over the 8-bit cache from the rows'
+// lse, for more query rows than logits are kept of (bf16 queries, head_dim 64
+// or 128): w_j = decay * w_in_j + sum_r exp(x_rj - lse_r).
+//
+// A CTA holds 128 keys of a (sequence, KV head) as the A operand, its codes
+// turned into bf16 once (exact), and walks the query rows 128 at a time: TMA
+// brings them as they are (bf16, one query head's tokens after another's; the
+// sum does not ask for the order), D[128 keys][128 rows] is formed on
+// tcgen05 into one of two TMEM accumulators, and four epilogue warps, a key a
+// lane, add exp2(s f - z_r): f, the key's factor, is the lane's own, z_r comes
+// from shared memory.  Two CTAs an SM, so that one's beginning and waits lie
+// under the other's exps.
+//
+// Bound by exp: 16384 of them a tile, 1024 cycles at 16 a cycle, against 512
+// of MMA.
+#include <cuda_bf16.h>
+
+#include "bkv_device_status.cuh"
+#include "cache8_attend.cuh"
+#include "sm100.cuh"
+#include "tma_host.h"
+
+BKV_DEFINE_STATUS_ACCESSOR(take_status_cache8_weights_tc)
+
+namespace bkv {
+namespace {
+
+using namespace cache8;
+using namespace sm100;
+
+enum : int { kWhereProd = 641, kWhereMma = 642, kWhereEpi = 643, kWhereDrain = 644 };
+
+constexpr int kThreads = 192;      // 4 epilogue warps, TMA, MMA
+constexpr int kHalf = 128 * 128;   // bytes of 128 rows x 64 bf16
+
+template <int D>
+struct WCfg {
+  static constexpr int kTileBytes = (D / 64) * kHalf;
+  static constexpr int kStages = 2;
+  static constexpr int kSmem = (1 + kStages) * kTileBytes + 1024;
+};
+
+struct WShared {
+  uint64_t full[2], empty[2], tfull[2], tempty[2], drain;
+  uint32_t tmem;
+  alignas(16) float z[2][128];  // lse of the rows of two tiles
+};
+
+// two e4m3 codes -> two bf16, exact
+__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t codes16) {
+  const float2 f = __half22float2(as_half2(e4m3x2_to_f16x2(codes16)));
+  const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2)
+    weights_tc_kernel(const AttendArgs p, const __grid_constant__ CUtensorMap q_map) {
+  using Cfg = WCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ WShared sh;
+  const Cache8AttendArgs &a = p.a;
+  const size_t head = blockIdx.y;
+  const int seq = static_cast<int>(head) / a.n_kv_heads;
+  const int kvh = static_cast<int>(head) - seq * a.n_kv_heads;
+  const SeqInfo q = seq_info(a, seq);
+  const int j0 = blockIdx.x * kTile;
+  if (q.tiles == 0 || j0 >= q.len) return;
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t *s_k = smem, *s_q = s_k + Cfg::kTileBytes;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // tiles of 128 tokens of a query head, from the first whose last token sees
+  // one of these keys
+  const int seen0 = q.len - q.n + 1;
+  const int t_tiles = (q.n + 127) / 128;
+  const int tb0 = max(0, (j0 - seen0 + 1) >> 7);
+  const int per_head = max(t_tiles - tb0, 0);
+  const int n_tiles = per_head * a.group;
+
+  if (warp == 5) {
+    tmem_alloc(smem_u32(&sh.tmem), 256);
+    tmem_relinquish();
+    if (lane == 0) {
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(smem_u32(&sh.full[i]), 1);
+        mbar_init(smem_u32(&sh.empty[i]), 1);
+        mbar_init(smem_u32(&sh.tfull[i]), 1);
+        mbar_init(smem_u32(&sh.tempty[i]), 4);
+      }
+      mbar_init(smem_u32(&sh.drain), 1);
+      fence_barrier_init();
+    }
+  }
+  if (warp < 4) {  // the keys' codes as bf16; keys past the end are zeros
+    const uint4 *src = reinterpret_cast<const uint4 *>(a.k8 + (head * a.cap + j0) * D);
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      const int id = i * 128 + threadIdx.x;
+      const int row = id / (D / 16), ch = id % (D / 16);
+      uint4 c = make_uint4(0, 0, 0, 0);
+      if (j0 + row < q.len) c = __ldg(src + id);
+      const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+      uint32_t h[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        h[2 * k] = e4m3x2_to_bf16x2(w[k]);
+        h[2 * k + 1] = e4m3x2_to_bf16x2(w[k] >> 16);
+      }
+      uint8_t *half = s_k + (ch >> 2) * kHalf;
+      *reinterpret_cast<uint4 *>(half + sw128_offset(row, (ch & 3) * 2)) =
+          make_uint4(h[0], h[1], h[2], h[3]);
+      *reinterpret_cast<uint4 *>(half + sw128_offset(row, (ch & 3) * 2 + 1)) =
+          make_uint4(h[4], h[5], h[6], h[7]);
+    }
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+
+  if (warp == 4) {
+    if (lane == 0) {
+      prefetch_tensormap(&q_map);
+      int it = 0;
+      for (; it < n_tiles; ++it) {
+        const int s = it & 1;
+        if (!mbar_wait(smem_u32(&sh.empty[s]), ((it >> 1) & 1) ^ 1, kWhereProd)) break;
+        const int g = it / per_head, t0 = (tb0 + it - g * per_head) * 128;
+        const long long row = (static_cast<long long>(seq) * a.n_q_heads + kvh * a.group + g) * a.T + t0;
+        mbar_arrive_expect_tx(smem_u32(&sh.full[s]), Cfg::kTileBytes);
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h)
+          tma_load_2d(smem_u32(s_q) + s * Cfg::kTileBytes + h * kHalf, &q_map, smem_u32(&sh.full[s]),
+                      h * 64, static_cast<int>(row));
+      }
+      // loads that no MMA waited for must not outlive the CTA
+      for (int t = max(it - 2, 0); t < it; ++t)
+        mbar_wait(smem_u32(&sh.full[t & 1]), (t >> 1) & 1, kWhereDrain);
+    }
+  } else if (warp == 5) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(128, 128);
+      for (int it = 0; it < n_tiles; ++it) {
+        const int s = it & 1;
+        if (!mbar_wait(smem_u32(&sh.full[s]), (it >> 1) & 1, kWhereMma)) break;
+        if (!mbar_wait(smem_u32(&sh.tempty[s]), ((it >> 1) & 1) ^ 1, kWhereMma)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = (k >> 2) * kHalf + (k & 3) * 32;
+          umma_f16(tmem + 128u * s, smem_desc_k_sw128(smem_u32(s_k) + off),
+                   smem_desc_k_sw128(smem_u32(s_q) + s * Cfg::kTileBytes + off), idesc, k != 0);
+        }
+        umma_commit(smem_u32(&sh.empty[s]));
+        umma_commit(smem_u32(&sh.tfull[s]));
+      }
+      umma_commit(smem_u32(&sh.drain));
+      mbar_wait(smem_u32(&sh.drain), 0, kWhereDrain);
+    }
+    __syncwarp();
+  } else {
+    const int key = j0 + threadIdx.x;
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    const float f =
+        __ldg(a.k_scale + head * (a.cap >> p.log2_block) + (min(key, q.len - 1) >> p.log2_block)) *
+        (a.scale * kLog2e);
+    const float *lse2 = p.lse2 + head * a.group * a.T;
+    auto z_of = [&](int it) {  // this thread's row of tile it
+      const int g = it / per_head, t = (tb0 + it - g * per_head) * 128 + threadIdx.x;
+      return t < q.n ? __ldg(lse2 + t * a.group + g) : 0.f;
+    };
+    bool ok = true;
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    float z_next = n_tiles > 0 ? z_of(0) : 0.f;
+    for (int it = 0; it < n_tiles; ++it) {
+      const int s = it & 1;
+      sh.z[s][threadIdx.x] = z_next;
+      if (it + 1 < n_tiles) z_next = z_of(it + 1);
+      // every epilogue warp comes here in every round, whatever its waits gave
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      if (ok && !mbar_wait_warp(smem_u32(&sh.tfull[s]), (it >> 1) & 1, kWhereEpi)) ok = false;
+      if (!ok) continue;
+      tc_fence_after();
+      const int g = it / per_head, t0 = (tb0 + it - g * per_head) * 128;
+      // rows t0 + c see the key from c = first on; tokens end at c = last
+      const int first = key - seen0 - t0 + 1, last = q.n - t0;
+      const bool masked = __any_sync(0xffffffffu, first > 0) || last < 128;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        float v[32];
+        tmem_ld_32x32b_x32(tmem + 128u * s + lanes + 32u * c, v);
+        tmem_ld_wait_regs(v);
+        if (c == 3) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sh.tempty[s]));
+        }
+        const float4 *zs = reinterpret_cast<const float4 *>(&sh.z[s][32 * c]);
+        if (!masked) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float4 z = zs[i];
+            sum[0] += ex2(fmaf(v[4 * i], f, -z.x));
+            sum[1] += ex2(fmaf(v[4 * i + 1], f, -z.y));
+            sum[2] += ex2(fmaf(v[4 * i + 2], f, -z.z));
+            sum[3] += ex2(fmaf(v[4 * i + 3], f, -z.w));
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float4 z4 = zs[i];
+            const float z[4] = {z4.x, z4.y, z4.z, z4.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int col = 32 * c + 4 * i + k;
+              const float e = ex2(fmaf(v[4 * i + k], f, -z[k]));
+              sum[k] += col >= first && col < last ? e : 0.f;
+            }
+          }
+        }
+      }
+    }
+    if (key < q.len) {
+      float total = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      // the new tokens' own rows start at zero
+      if (a.w_in && key < q.len - q.n) total = fmaf(a.decay, a.w_in[head * a.cap + key], total);
+      if (ok) a.w_out[head * a.cap + key] = total;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 256);
+  }
+}
+
+template <int D>
+bool run(const AttendArgs &p, cudaStream_t stream) {
+  static int done[64];
+  using Cfg = WCfg<D>;
+  static_assert(Cfg::kSmem + sizeof(WShared) <= 113 * 1024, "two CTAs an SM");
+  if (!ensure_smem_limit(weights_tc_kernel<D>, Cfg::kSmem, done)) return false;
+  CUtensorMap map;
+  const unsigned long long rows =
+      static_cast<unsigned long long>(p.a.n_seqs) * p.a.n_q_heads * p.a.T;
+  if (!make_bf16_rows_map(&map, p.a.q, rows, 128, D)) return false;
+  const dim3 grid(static_cast<unsigned>((p.a.max_len + kTile - 1) / kTile),
+                  static_cast<unsigned>(p.a.n_seqs) * p.a.n_kv_heads);
+  weights_tc_kernel<D><<<grid, kThreads, Cfg::kSmem, stream>>>(p, map);
+  return cudaGetLastError() == cudaSuccess;
+}
+
+}  // namespace
+
+bool launch_weights_tc(const cache8::AttendArgs &p, cudaStream_t stream) {
+  return p.a.head_dim == 128 ? run<128>(p, stream) : run<64>(p, stream);
+}
+
+}  // namespace bkv

@@ -25,14 +25,14 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   return fn;
 }
 
-// A [rows][128] bf16 tensor read in boxes of 64 columns x box_rows rows with
+// A [rows][cols] bf16 tensor read in boxes of 64 columns x box_rows rows with
 // the 128-byte swizzle (rows past the end read as zero).
 inline bool make_bf16_rows_map(CUtensorMap *map, const void *base, unsigned long long rows,
-                               int box_rows) {
+                               int box_rows, int cols = 128) {
   auto encode = tensor_map_encoder();
   if (!encode || rows == 0) return false;
-  cuuint64_t dims[2] = {128u, static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[1] = {256u};
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {2u * static_cast<cuuint64_t>(cols)};
   cuuint32_t box[2] = {64u, static_cast<cuuint32_t>(box_rows)};
   cuuint32_t estr[2] = {1u, 1u};
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides,
