@@ -738,8 +738,8 @@ __device__ __forceinline__ Parts parts_of(const Split &w, int first, int tiles) 
 }
 
 // First the CTAs that join: p.join_rows rows of a (sequence, KV head, row
-// block) each, one row at a time with every warp (few segments in many parts)
-// or a row per warp (many segments in few).  They write the rows of segments
+// block) each, one row with every warp (few rows in many parts) or a row at a
+// time per warp (many rows in few).  They write the rows of segments
 // that several CTAs computed, and the empty rows of sequences without cached
 // keys.  A row's parts are dealt to its warps in turn and the warps' sums added
 // in order, so results do not depend on timing.
@@ -748,8 +748,10 @@ __device__ __forceinline__ Parts parts_of(const Split &w, int first, int tiles) 
 // join the parts' statistics for themselves.
 // Launched while the attention kernel runs: everything before the wait reads
 // only the lengths, and every CTA waits, so that this kernel never ends first.
+// Five CTAs an SM, 48 registers: one then fits beside two of the attention
+// kernel's and has its beginning behind it when that ends.
 template <int kRows, typename T>
-__global__ void __launch_bounds__(kSimtThreads) attend_finish_kernel(const AttendArgs p) {
+__global__ void __launch_bounds__(kSimtThreads, 5) attend_finish_kernel(const AttendArgs p) {
   __shared__ float s_o[kSimtWarps][kMaxD];
   __shared__ float s_l[kSimtWarps];
   __shared__ float s_z[kMaxXRows];
@@ -760,6 +762,7 @@ __global__ void __launch_bounds__(kSimtThreads) attend_finish_kernel(const Atten
   const int per_unit = kRows / p.join_rows;
   const int joins = a.n_seqs * units * per_unit;
   const int stride = kRows * (2 + D);
+  int mine;
   // a part's statistics and output: slot 1 of the CTA the segment starts in,
   // slot 0 after it
   auto part = [&](const Parts &x, int i) {
@@ -771,7 +774,6 @@ __global__ void __launch_bounds__(kSimtThreads) attend_finish_kernel(const Atten
     const int seq = head / a.n_kv_heads;
     const SeqInfo q = seq_info(a, seq);
     const bool none = q.tiles == 0 || j0 >= q.len;
-    int mine;
     const Split w = split_of(a, units, p.ctas, &mine);
     const int before = counted_before(a, w, units, mine, seq);
     pdl_wait();
@@ -800,29 +802,36 @@ __global__ void __launch_bounds__(kSimtThreads) attend_finish_kernel(const Atten
     }
     __syncthreads();
     const int j1 = min(j0 + p.w_keys, q.len);
+    const float *xh = p.x + static_cast<size_t>(head) * p.x_len * p.x_cols;
     for (int j = j0 + threadIdx.x; j < j1; j += kSimtThreads) {
-      const float2 *x = reinterpret_cast<const float2 *>(
-          p.x + (static_cast<size_t>(head) * p.x_len + j) * p.x_cols);
-      float sum = 0.f;
+      const float *x = xh + static_cast<size_t>(j) * p.x_cols;
+      float sum = 0.f, more = 0.f;
       int r = 0;
-      for (; r + 1 < rows; r += 2) {
-        const float2 v = x[r >> 1];
-        sum += ex2(v.x - s_z[r]);
-        sum += ex2(v.y - s_z[r + 1]);
+      if ((p.x_cols & 3) == 0) {
+#pragma unroll 3
+        for (; r + 3 < rows; r += 4) {
+          const float4 v = *reinterpret_cast<const float4 *>(x + r);
+          sum += ex2(v.x - s_z[r]) + ex2(v.y - s_z[r + 1]);
+          more += ex2(v.z - s_z[r + 2]) + ex2(v.w - s_z[r + 3]);
+        }
       }
-      if (r < rows) sum += ex2(x[r >> 1].x - s_z[r]);
-      store_weight(a, head, j, q, sum);
+#pragma unroll 4
+      for (; r + 1 < rows; r += 2) {
+        const float2 v = *reinterpret_cast<const float2 *>(x + r);
+        sum += ex2(v.x - s_z[r]);
+        more += ex2(v.y - s_z[r + 1]);
+      }
+      if (r < rows) sum += ex2(x[r] - s_z[r]);
+      store_weight(a, head, j, q, sum + more);
     }
     return;
   }
   const int u = blockIdx.x / per_unit;
   const int seq = u / units, unit = u - seq * units;
   const int kvh = unit / p.row_blocks;
-  const int deal = kSimtWarps / p.join_rows;  // warps per row
-  const int row = (blockIdx.x - u * per_unit) * p.join_rows + warp / deal;
-  const int r = (unit - kvh * p.row_blocks) * kRows + row;
+  const int first = (blockIdx.x - u * per_unit) * p.join_rows;  // row of the row block
+  const int r0 = (unit - kvh * p.row_blocks) * kRows + first;
   const SeqInfo q = seq_info(a, seq);
-  int mine;
   const Split w = split_of(a, units, p.ctas, &mine);
   Parts x = {0, 0};
   if (q.tiles > 0)
@@ -833,9 +842,11 @@ __global__ void __launch_bounds__(kSimtThreads) attend_finish_kernel(const Atten
     return;
   }
   if (x.n == 1) return;  // written by its CTA
-  const bool live = r < a.group * q.n;
-  float M = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  if (live && x.n > 0) {
+  const int rows = min(p.join_rows, a.group * q.n - r0);
+  const int deal = p.join_rows == 1 ? kSimtWarps : 1;  // warps per row
+  for (int i0 = warp / deal; i0 < rows; i0 += kSimtWarps / deal) {
+    const int row = first + i0;
+    float M = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
     for (int i = lane; i < x.n; i += 32) M = fmaxf(M, part(x, i)[row]);
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
@@ -852,27 +863,26 @@ __global__ void __launch_bounds__(kSimtThreads) attend_finish_kernel(const Atten
       o[0] = fmaf(f, v.x, o[0]), o[1] = fmaf(f, v.y, o[1]);
       o[2] = fmaf(f, v.z, o[2]), o[3] = fmaf(f, v.w, o[3]);
     }
-  }
-  if (deal > 1) {
-    if (lane * 4 < D)
-      *reinterpret_cast<float4 *>(&s_o[warp][lane * 4]) = make_float4(o[0], o[1], o[2], o[3]);
-    if (lane == 0) s_l[warp] = l;
-    __syncthreads();
-    if (warp % deal != 0) return;
-    for (int i = 1; i < deal; ++i) {
-      l += s_l[warp + i];
-      if (lane * 4 < D) {
-        const float4 v = *reinterpret_cast<const float4 *>(&s_o[warp + i][lane * 4]);
-        o[0] += v.x, o[1] += v.y, o[2] += v.z, o[3] += v.w;
+    if (deal > 1) {
+      if (lane * 4 < D)
+        *reinterpret_cast<float4 *>(&s_o[warp][lane * 4]) = make_float4(o[0], o[1], o[2], o[3]);
+      if (lane == 0) s_l[warp] = l;
+      __syncthreads();  // one row: every warp comes here once
+      if (warp != 0) return;
+      for (int i = 1; i < kSimtWarps; ++i) {
+        l += s_l[i];
+        if (lane * 4 < D) {
+          const float4 v = *reinterpret_cast<const float4 *>(&s_o[i][lane * 4]);
+          o[0] += v.x, o[1] += v.y, o[2] += v.z, o[3] += v.w;
+        }
       }
     }
+    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+    if (lane * 4 < D)
+      store_out4(static_cast<T *>(a.out) + q_row(a, seq, kvh, r0 + i0) * D + lane * 4, o[0] * inv,
+                 o[1] * inv, o[2] * inv, o[3] * inv);
+    if (lane == 0) store_lse(p, seq, kvh, r0 + i0, M, l);
   }
-  if (!live) return;
-  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-  if (lane * 4 < D)
-    store_out4(static_cast<T *>(a.out) + q_row(a, seq, kvh, r) * D + lane * 4, o[0] * inv, o[1] * inv,
-               o[2] * inv, o[3] * inv);
-  if (lane == 0) store_lse(p, seq, kvh, r, M, l);
 }
 
 // From the keys again, for more query rows than logits are kept of.
@@ -925,7 +935,9 @@ bool run_mma(const AttendArgs &p, cudaStream_t s) {
 template <int kRows, typename T>
 bool run_finish(AttendArgs p, cudaStream_t s) {
   const long long segments = static_cast<long long>(p.a.n_seqs) * p.a.n_kv_heads * p.row_blocks;
-  p.join_rows = segments >= kSms ? 8 : 1;
+  // a CTA's beginning costs as much as some rows: as few CTAs as fill the SMs
+  const long long rows = segments * kRows;
+  p.join_rows = rows <= 4 * kSms ? 1 : kRows % 64 != 0 || rows <= 32 * kSms ? 8 : 64;
   long long grid = segments * (kRows / p.join_rows);
   if (p.x_cols > 0) {
     // about four CTAs an SM: the lse of a CTA's rows cost it as much as some
