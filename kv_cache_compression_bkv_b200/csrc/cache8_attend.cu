@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_mma_kernel(const AttendArg
     }
     load.next(a, w, units);
   };
-#pragma unroll
+#pragma unroll 1
   for (int s = 0; s < Cfg::kStages - 1; ++s) {
     if (load.at < run) issue(s);
     cp_async_commit();
@@ -565,37 +565,54 @@ __device__ __forceinline__ void values4(uint32_t w, float (&v)[4]) {
 constexpr int kSimtRows = 8;
 constexpr int kMaxD = 128;
 
-// The logits of 8 query rows (in shared memory, [8][D]) for one key: two lanes
-// a key, each half of the elements; both lanes get the sums.
-__device__ __forceinline__ void simt_logits(const uint8_t *key_row, int D, int half,
-                                            const float *s_q, float (&x)[kSimtRows]) {
+// The logits of 8 query rows (in shared memory, [8][D]) for one key (its codes
+// in shared or global memory): two lanes a key, each every second 16-byte chunk;
+// both get the sums.  Loops are kept short: at the sizes this path is for, a
+// tile is over in the time that fetching long unrolled code takes.
+__device__ __forceinline__ void simt_logits(const uint8_t *row, int D, int half, const float *s_q,
+                                            float (&x)[kSimtRows]) {
 #pragma unroll
   for (int r = 0; r < kSimtRows; ++r) x[r] = 0.f;
-  const int n = D / 8;  // words per half
-  for (int w = 0; w < n; ++w) {
-    float v[4];
-    values4(__ldg(reinterpret_cast<const uint32_t *>(key_row) + half * n + w), v);
-    const float *q = s_q + (half * n + w) * 4;
+#pragma unroll 1
+  for (int i = half * 16; i < D; i += 32) {
+    const uint4 c = *reinterpret_cast<const uint4 *>(row + i);
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-    for (int r = 0; r < kSimtRows; ++r) {
-      const float4 y = *reinterpret_cast<const float4 *>(q + r * D);
-      x[r] = fmaf(v[0], y.x, fmaf(v[1], y.y, fmaf(v[2], y.z, fmaf(v[3], y.w, x[r]))));
+    for (int j = 0; j < 4; ++j) {
+      float v[4];
+      values4(w[j], v);
+      const float *q = s_q + i + 4 * j;
+#pragma unroll
+      for (int r = 0; r < kSimtRows; ++r) {
+        const float4 y = *reinterpret_cast<const float4 *>(q + r * D);
+        x[r] = fmaf(v[0], y.x, fmaf(v[1], y.y, fmaf(v[2], y.z, fmaf(v[3], y.w, x[r]))));
+      }
     }
   }
 #pragma unroll
   for (int r = 0; r < kSimtRows; ++r) x[r] += __shfl_xor_sync(0xffffffffu, x[r], 1);
 }
 
+// Dynamic shared memory: queries, the warps' merge buffers, and per warp two
+// stages of 16 keys' codes (rows padded by 16 bytes against bank conflicts).
+inline __host__ __device__ int simt_stage_bytes(int D) { return 2 * kSimtKeys * (D + 16) + 16; }
+inline int simt_smem(int D) {
+  return (1 + kSimtWarps) * kSimtRows * D * 4 + kSimtWarps * 2 * simt_stage_bytes(D);
+}
+
 template <typename T>
-__global__ void __launch_bounds__(kSimtThreads) attend_simt_kernel(const AttendArgs p) {
-  __shared__ __align__(16) float s_q[kSimtRows * kMaxD];
-  __shared__ __align__(16) float s_buf[kSimtWarps * kSimtRows * kMaxD];
-  __shared__ float s_p[kSimtWarps][kSimtKeys][kSimtRows];
+__global__ void __launch_bounds__(kSimtThreads, 2) attend_simt_kernel(const AttendArgs p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(16) float s_p[kSimtWarps][kSimtKeys][kSimtRows];
   __shared__ float s_m[kSimtWarps][kSimtRows], s_l[kSimtWarps][kSimtRows];
   __shared__ float s_M[kSimtRows], s_L[kSimtRows];
   const Cache8AttendArgs &a = p.a;
   const int D = a.head_dim;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float *s_q = reinterpret_cast<float *>(smem);
+  float *s_buf = s_q + kSimtRows * D;
+  uint8_t *ring = reinterpret_cast<uint8_t *>(s_buf + kSimtWarps * kSimtRows * D) +
+                  warp * 2 * simt_stage_bytes(D);
   const int units = a.n_kv_heads * p.row_blocks;
   pdl_launch_dependents();
   int mine;
@@ -603,21 +620,50 @@ __global__ void __launch_bounds__(kSimtThreads) attend_simt_kernel(const AttendA
   const int t0 = blockIdx.x * w.run;
   if (t0 >= w.total) return;
   const int run = min(w.run, w.total - t0);
-  Cursor cur;
+  Cursor cur, ahead;
   cur.seek(a, w, units, mine, t0);
-  int seg_tiles = 0;
+  ahead = cur;
+  // the next tile's codes and scales of this warp
+  int issued = 0;
+  auto issue = [&]() {
+    const int j0 = ahead.tile * kTile + warp * kSimtKeys;
+    if (ahead.at < run && j0 < ahead.q.len) {
+      const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) +
+                           (issued & 1) * simt_stage_bytes(D);
+      const size_t head = static_cast<size_t>(ahead.seq) * a.n_kv_heads + ahead.unit / p.row_blocks;
+      const size_t off = (head * a.cap + j0) * D;
+      const int ch = D >> 4;
+#pragma unroll 1
+      for (int q = lane; q < kSimtKeys * ch; q += 32) {
+        const int key = q / ch;
+        const uint32_t to = dst + key * (D + 16) + (q - key * ch) * 16;
+        const bool there = j0 + key < ahead.q.len;
+        cp_async16(to, a.k8 + off + q * 16, there);
+        cp_async16(to + kSimtKeys * (D + 16), a.v8 + off + q * 16, there);
+      }
+      if (lane < 2)
+        cp_async4(dst + 2 * kSimtKeys * (D + 16) + lane * 4,
+                  (lane ? a.v_scale : a.k_scale) + head * (a.cap >> p.log2_block) + (j0 >> p.log2_block));
+    }
+    if (ahead.at < run) ahead.next(a, w, units);
+    ++issued;
+    cp_async_commit();
+  };
+  issue();
   float o[kSimtRows][4], m[kSimtRows], l[kSimtRows];
   bool fresh = true;
+  int seg_tiles = 0, stage = 0;
   while (cur.at < run) {
     const int kvh = cur.unit / p.row_blocks;
     const int r0 = (cur.unit - kvh * p.row_blocks) * kSimtRows;
     const size_t head = static_cast<size_t>(cur.seq) * a.n_kv_heads + kvh;
     if (fresh) {
       fresh = false;
+#pragma unroll 1
       for (int e = threadIdx.x; e < kSimtRows * D; e += kSimtThreads) {
-        const int r = r0 + e / D;
-        s_q[e] = r < a.group * cur.q.n
-                     ? load_q(static_cast<const T *>(a.q) + q_row(a, cur.seq, kvh, r) * D + e % D)
+        const int r = e / D;
+        s_q[e] = r0 + r < a.group * cur.q.n
+                     ? load_q(static_cast<const T *>(a.q) + q_row(a, cur.seq, kvh, r0 + r) * D + e - r * D)
                      : 0.f;
       }
       __syncthreads();
@@ -628,88 +674,95 @@ __global__ void __launch_bounds__(kSimtThreads) attend_simt_kernel(const AttendA
         o[r][0] = o[r][1] = o[r][2] = o[r][3] = 0.f;
       }
     }
+    issue();
+    cp_async_wait<1>();
+    __syncwarp();
     const int j0 = cur.tile * kTile + warp * kSimtKeys;
-    const int seen0 = cur.q.len - cur.q.n + 1;
     if (j0 < cur.q.len) {
-      const int j = min(j0 + (lane >> 1), cur.q.len - 1);  // rows past the end are not read
-      const size_t blk = head * (a.cap / a.block) + j0 / a.block;
-      const float f = __ldg(a.k_scale + blk) * a.scale * kLog2e, vs = __ldg(a.v_scale + blk);
+      const uint8_t *st = ring + stage * simt_stage_bytes(D);
+      const float *sc = reinterpret_cast<const float *>(st + 2 * kSimtKeys * (D + 16));
+      const float f = sc[0] * a.scale * kLog2e, vs = sc[1];
+      const int j = j0 + (lane >> 1);
       float x[kSimtRows];
-      simt_logits(a.k8 + (head * a.cap + j) * D, D, lane & 1, s_q, x);
+      simt_logits(st + (lane >> 1) * (D + 16), D, lane & 1, s_q, x);
+      const int seen0 = cur.q.len - cur.q.n + 1;
 #pragma unroll
       for (int r = 0; r < kSimtRows; ++r) {
-        x[r] = j0 + (lane >> 1) < seen0 + (r0 + r) / a.group && j0 + (lane >> 1) < cur.q.len
-                   ? x[r] * f
-                   : -INFINITY;
-        if (p.x_cols > r0 + r && (lane & 1) == 0 && j0 + (lane >> 1) < cur.q.len)
+        x[r] = j < min(seen0 + (r0 + r) / a.group, cur.q.len) ? x[r] * f : -INFINITY;
+        if (p.x_cols > r0 + r && (lane & 1) == 0 && j < cur.q.len)
           p.x[(head * p.x_len + j) * p.x_cols + r0 + r] = x[r];
         float t = x[r];
 #pragma unroll
         for (int s = 2; s < 32; s <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, s));
         if (t > m[r]) {
-          const float g = exp2f(m[r] - t);
+          const float g = ex2(m[r] - t);
           m[r] = t;
           l[r] *= g;
           o[r][0] *= g, o[r][1] *= g, o[r][2] *= g, o[r][3] *= g;
         }
-        const float e = exp2f(x[r] - (m[r] == -INFINITY ? 0.f : m[r]));
+        const float e = ex2(x[r] - (m[r] == -INFINITY ? 0.f : m[r]));
         if ((lane & 1) == 0) {
           s_p[warp][lane >> 1][r] = e * vs;
           l[r] += e;
         }
       }
       __syncwarp();
-      if (lane * 4 < D) {
-        const int keys = min(kSimtKeys, cur.q.len - j0);
-        for (int k = 0; k < keys; ++k) {
-          float v[4];
-          values4(__ldg(reinterpret_cast<const uint32_t *>(a.v8 + (head * a.cap + j0 + k) * D) + lane), v);
+      const uint8_t *vrow = st + kSimtKeys * (D + 16) + (lane * 4 < D ? lane * 4 : 0);
+#pragma unroll 2
+      for (int k = 0; k < kSimtKeys; ++k) {  // keys past the end: p = 0, codes 0
+        float v[4];
+        values4(*reinterpret_cast<const uint32_t *>(vrow + k * (D + 16)), v);
+        const float4 e0 = *reinterpret_cast<const float4 *>(&s_p[warp][k][0]);
+        const float4 e1 = *reinterpret_cast<const float4 *>(&s_p[warp][k][4]);
+        const float e[kSimtRows] = {e0.x, e0.y, e0.z, e0.w, e1.x, e1.y, e1.z, e1.w};
 #pragma unroll
-          for (int r = 0; r < kSimtRows; ++r) {
-            const float e = s_p[warp][k][r];
+        for (int r = 0; r < kSimtRows; ++r)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[r][i] = fmaf(e, v[i], o[r][i]);
-          }
-        }
+          for (int i = 0; i < 4; ++i) o[r][i] = fmaf(e[r], v[i], o[r][i]);
       }
-      __syncwarp();
     }
+    __syncwarp();  // the stage and the probabilities have been read
+    stage ^= 1;
     ++seg_tiles;
     if (cur.tile + 1 == cur.q.tiles || cur.at + 1 == run) {
 #pragma unroll
       for (int r = 0; r < kSimtRows; ++r) {
         float t = l[r];
 #pragma unroll
-        for (int s = 1; s < 32; s <<= 1) t += __shfl_xor_sync(0xffffffffu, t, s);
+        for (int s = 2; s < 32; s <<= 1) t += __shfl_xor_sync(0xffffffffu, t, s);
         if (lane == 0) {
           s_m[warp][r] = m[r];
           s_l[warp][r] = t;
         }
-        l[r] = t;
+        l[r] = t;  // in the even lanes
       }
       __syncthreads();
 #pragma unroll
       for (int r = 0; r < kSimtRows; ++r) {
-        float M = -INFINITY, L = 0.f;
-        for (int w = 0; w < kSimtWarps; ++w) M = fmaxf(M, s_m[w][r]);
-        const float f = m[r] == -INFINITY ? (l[r] != l[r] ? 1.f : 0.f) : exp2f(m[r] - M);
+        float M = -INFINITY;
+        for (int k = 0; k < kSimtWarps; ++k) M = fmaxf(M, s_m[k][r]);
+        // NaN logits leave no reference, and sums that have to stay
+        const float f = m[r] == -INFINITY ? (s_l[warp][r] != s_l[warp][r] ? 1.f : 0.f) : ex2(m[r] - M);
         if (lane * 4 < D)
           *reinterpret_cast<float4 *>(s_buf + (warp * kSimtRows + r) * D + lane * 4) =
               make_float4(o[r][0] * f, o[r][1] * f, o[r][2] * f, o[r][3] * f);
-        if (threadIdx.x == 0) {
-          for (int w = 0; w < kSimtWarps; ++w)
-            L += s_m[w][r] == -INFINITY ? s_l[w][r] : exp2f(s_m[w][r] - M) * s_l[w][r];
-          s_M[r] = M;
-          s_L[r] = L;
-        }
+      }
+      if (threadIdx.x < kSimtRows) {
+        const int r = threadIdx.x;
+        float M = -INFINITY, L = 0.f;
+        for (int k = 0; k < kSimtWarps; ++k) M = fmaxf(M, s_m[k][r]);
+        for (int k = 0; k < kSimtWarps; ++k)
+          L += s_m[k][r] == -INFINITY ? s_l[k][r] : ex2(s_m[k][r] - M) * s_l[k][r];
+        s_M[r] = M;
+        s_L[r] = L;
       }
       __syncthreads();
       const bool from_start = seg_tiles == cur.tile + 1;
       const bool to_end = cur.tile + 1 == cur.q.tiles;
       seg_tiles = 0;
-      write_segment<kSimtRows, kSimtWarps, kSimtThreads, T>(p, s_buf, kSimtRows * D, s_M, s_L, cur.seq, cur.unit,
-                                          cur.q.n, from_start && to_end, from_start ? 1 : 0,
-                                          [D](int r, int d) { return r * D + d; });
+      write_segment<kSimtRows, kSimtWarps, kSimtThreads, T>(
+          p, s_buf, kSimtRows * D, s_M, s_L, cur.seq, cur.unit, cur.q.n, from_start && to_end,
+          from_start ? 1 : 0, [D](int r, int d) { return r * D + d; });
       __syncthreads();
       fresh = true;
     }
@@ -735,6 +788,46 @@ __device__ __forceinline__ Parts parts_of(const Split &w, int first, int tiles) 
   x.c0 = first / w.run;
   x.n = (first + tiles - 1) / w.run - x.c0 + 1;
   return x;
+}
+
+// The weights of keys j0 .. j1 - 1 from their kept logits, kQuad rows at a time.
+template <int kQuad, int kBatch>
+__device__ __forceinline__ void weights_kept(const Cache8AttendArgs &a, const SeqInfo &q,
+                                             const float *xh, int x_cols, const float *s_z, int rows,
+                                             size_t head, int j0, int j1) {
+  for (int j = j0 + threadIdx.x; j < j1; j += kBatch * kSimtThreads) {
+    float sum[kBatch] = {}, old[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int ju = j + u * kSimtThreads;
+      old[u] = a.w_in && ju < min(j1, q.len - q.n) ? a.w_in[head * a.cap + ju] : 0.f;
+    }
+#pragma unroll 2
+    for (int r = 0; r < rows; r += kQuad) {  // x_cols is a multiple of kQuad
+      float v[kBatch][kQuad];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const float *x = xh + static_cast<size_t>(min(j + u * kSimtThreads, j1 - 1)) * x_cols + r;
+        if constexpr (kQuad == 4)
+          *reinterpret_cast<float4 *>(v[u]) = *reinterpret_cast<const float4 *>(x);
+        else
+          *reinterpret_cast<float2 *>(v[u]) = *reinterpret_cast<const float2 *>(x);
+      }
+#pragma unroll
+      for (int k = 0; k < kQuad; ++k) {
+        const float z = s_z[r + k];  // infinity past the last row
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) sum[u] += ex2(v[u][k] - z);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int ju = j + u * kSimtThreads;
+      // the new tokens' own rows start at zero
+      if (ju < j1)
+        a.w_out[head * a.cap + ju] = a.w_in && ju < q.len - q.n ? fmaf(a.decay, old[u], sum[u]) : sum[u];
+    }
+  }
 }
 
 // First the CTAs that join: p.join_rows rows of a (sequence, KV head, row
@@ -779,6 +872,7 @@ __global__ void __launch_bounds__(kSimtThreads, 5) attend_finish_kernel(const At
     pdl_wait();
     if (none) return;
     const int rows = a.group * q.n;
+    if (threadIdx.x < kMaxXRows && threadIdx.x >= rows) s_z[threadIdx.x] = INFINITY;
     for (int r = warp; r < rows; r += kSimtWarps) {
       const int unit = (head - seq * a.n_kv_heads) * p.row_blocks + r / kRows, row = r % kRows;
       const Parts x = parts_of(w, before + unit * (q.tiles + w.pad) + w.pad, q.tiles);
@@ -803,27 +897,11 @@ __global__ void __launch_bounds__(kSimtThreads, 5) attend_finish_kernel(const At
     __syncthreads();
     const int j1 = min(j0 + p.w_keys, q.len);
     const float *xh = p.x + static_cast<size_t>(head) * p.x_len * p.x_cols;
-    for (int j = j0 + threadIdx.x; j < j1; j += kSimtThreads) {
-      const float *x = xh + static_cast<size_t>(j) * p.x_cols;
-      float sum = 0.f, more = 0.f;
-      int r = 0;
-      if ((p.x_cols & 3) == 0) {
-#pragma unroll 3
-        for (; r + 3 < rows; r += 4) {
-          const float4 v = *reinterpret_cast<const float4 *>(x + r);
-          sum += ex2(v.x - s_z[r]) + ex2(v.y - s_z[r + 1]);
-          more += ex2(v.z - s_z[r + 2]) + ex2(v.w - s_z[r + 3]);
-        }
-      }
-#pragma unroll 4
-      for (; r + 1 < rows; r += 2) {
-        const float2 v = *reinterpret_cast<const float2 *>(x + r);
-        sum += ex2(v.x - s_z[r]);
-        more += ex2(v.y - s_z[r + 1]);
-      }
-      if (r < rows) sum += ex2(x[r] - s_z[r]);
-      store_weight(a, head, j, q, sum + more);
-    }
+    // keys a thread has in flight: what the loads of one row pair take, or of a quad
+    if ((p.x_cols & 3) == 0)
+      weights_kept<4, 2>(a, q, xh, p.x_cols, s_z, rows, head, j0, j1);
+    else
+      weights_kept<2, 4>(a, q, xh, p.x_cols, s_z, rows, head, j0, j1);
     return;
   }
   const int u = blockIdx.x / per_unit;
@@ -932,6 +1010,14 @@ bool run_mma(const AttendArgs &p, cudaStream_t s) {
   return cudaGetLastError() == cudaSuccess;
 }
 
+template <typename T>
+bool run_simt(const AttendArgs &p, cudaStream_t s) {
+  static int done[64];
+  if (!ensure_smem_limit(attend_simt_kernel<T>, simt_smem(kMaxD), done)) return false;
+  attend_simt_kernel<T><<<p.ctas, kSimtThreads, simt_smem(p.a.head_dim), s>>>(p);
+  return cudaGetLastError() == cudaSuccess;
+}
+
 template <int kRows, typename T>
 bool run_finish(AttendArgs p, cudaStream_t s) {
   const long long segments = static_cast<long long>(p.a.n_seqs) * p.a.n_kv_heads * p.row_blocks;
@@ -1026,11 +1112,9 @@ bkv_status launch_cache8_attend(const Cache8AttendArgs &a, const Cache8AttendPla
       ok = (wide ? run_mma<128, 4>(p, stream) : run_mma<64, 4>(p, stream)) &&
            run_finish<32, __nv_bfloat16>(p, stream);
   } else if (dtype == BKV_BF16) {
-    attend_simt_kernel<__nv_bfloat16><<<p.ctas, kSimtThreads, 0, stream>>>(p);
-    ok = cudaGetLastError() == cudaSuccess && run_finish<kSimtRows, __nv_bfloat16>(p, stream);
+    ok = run_simt<__nv_bfloat16>(p, stream) && run_finish<kSimtRows, __nv_bfloat16>(p, stream);
   } else {
-    attend_simt_kernel<float><<<p.ctas, kSimtThreads, 0, stream>>>(p);
-    ok = cudaGetLastError() == cudaSuccess && run_finish<kSimtRows, float>(p, stream);
+    ok = run_simt<float>(p, stream) && run_finish<kSimtRows, float>(p, stream);
   }
   if (!ok) return BKV_ERR_CUDA;
   if (a.w_out && plan.x_cols == 0) {
