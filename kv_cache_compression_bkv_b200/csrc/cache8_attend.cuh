@@ -13,7 +13,7 @@ namespace cache8 {
 
 constexpr int kTile = 128;               // keys per tile
 constexpr int kSms = 148;
-constexpr int kPad = 2;                  // what a segment costs beside its tiles, in tiles
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kMaxXRows = 32;  // query rows per KV head whose logits are kept for the weights
@@ -82,7 +82,7 @@ __device__ __forceinline__ Split split_of(const Cache8AttendArgs &a, int units, 
   tiles = warp_sum(tiles) * units;
   segments = warp_sum(segments) * units;
   Split w;
-  w.pad = tiles >= 16 * ctas ? kPad : 0;
+  w.pad = tiles >= 16 * ctas ? 2 : tiles >= 4 * ctas ? 1 : 0;
   w.total = tiles + w.pad * segments;
   w.run = max((w.total + ctas - 1) / ctas, 1);
   return w;
