@@ -27,8 +27,6 @@
 // bytes.
 #include <cuda_bf16.h>
 
-#include <type_traits>
-
 #include "bkv_device_status.cuh"
 #include "cache8_attend.cuh"
 #include "sm100.cuh"
@@ -125,7 +123,32 @@ __device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t addr, uint32_t m
   return d;
 }
 
+constexpr int kPoly = 4;          // of 16 pairs of exps, those on the FMA pipe
 constexpr int kHalf = 128 * 128;  // bytes of 128 rows x 64 f16
+
+// 2^y of a pair on the FMA pipe: y = n + f with n = round(y) by the 1.5 * 2^23
+// trick, a quartic for 2^f on [-1/2, 1/2] (least largest relative error,
+// 2.6e-6), n added into its exponent.  y is held to [-126, 127], NaN stays NaN
+// until the last addition, which makes it a finite number above 2^127.
+__device__ __forceinline__ float clamp_nan(float y) {
+  asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(y));  // -126
+  asm("min.NaN.f32 %0, %0, 0f42FE0000;" : "+f"(y));  // 127
+  return y;
+}
+__device__ __forceinline__ float2 exp2_quartic(float2 y) {
+  constexpr float kRound = 12582912.f;
+  y.x = clamp_nan(y.x);
+  y.y = clamp_nan(y.y);
+  const float2 t = __fadd2_rn(y, make_float2(kRound, kRound));
+  const float2 n = __fadd2_rn(t, make_float2(-kRound, -kRound));
+  const float2 f = __ffma2_rn(n, make_float2(-1.f, -1.f), y);
+  float2 p = __ffma2_rn(f, make_float2(0.009570102f, 0.009570102f), make_float2(0.05591786f, 0.05591786f));
+  p = __ffma2_rn(p, f, make_float2(0.24024744f, 0.24024744f));
+  p = __ffma2_rn(p, f, make_float2(0.6931218f, 0.6931218f));
+  p = __ffma2_rn(p, f, make_float2(0.9999993f, 0.9999993f));
+  return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
+                     __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
+}
 
 template <int D, int RT>
 struct TcCfg {
@@ -146,10 +169,8 @@ struct TcShared {
   float v_scale[4];   // of the last parts
 };
 
-// 16 codes as f16, times a power of two: 32 bytes at chunk pair ch of row `row`
-// of a tile; odd halves store the second chunk first, which keeps the 8 lanes
-// of a row free of bank conflicts.
-__device__ __forceinline__ void store_f16(uint8_t *tile, int row, int ch, uint4 c, __half2 f) {
+// 16 codes as f16, times a power of two: elements 0..7 and 8..15.
+__device__ __forceinline__ void convert16(uint4 c, __half2 f, uint4 *lo, uint4 *hi) {
   const uint32_t w[4] = {c.x, c.y, c.z, c.w};
   uint32_t h[8];
 #pragma unroll
@@ -157,11 +178,8 @@ __device__ __forceinline__ void store_f16(uint8_t *tile, int row, int ch, uint4 
     h[2 * i] = as_u32(__hmul2(as_half2(e4m3x2_to_f16x2(w[i])), f));
     h[2 * i + 1] = as_u32(__hmul2(as_half2(e4m3x2_to_f16x2(w[i] >> 16)), f));
   }
-  const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-  uint8_t *half = tile + (ch >> 2) * kHalf;
-  const int c2 = (ch & 3) * 2, flip = (ch >> 2) & 1;
-  *reinterpret_cast<uint4 *>(half + sw128_offset(row, c2 + flip)) = flip ? hi : lo;
-  *reinterpret_cast<uint4 *>(half + sw128_offset(row, c2 + 1 - flip)) = flip ? lo : hi;
+  *lo = make_uint4(h[0], h[1], h[2], h[3]);
+  *hi = make_uint4(h[4], h[5], h[6], h[7]);
 }
 
 template <int D, int RT>
@@ -290,6 +308,16 @@ __global__ void __launch_bounds__((TcCfg<D, RT>::kThreads), 1) attend_tc_kernel(
     constexpr int NP = (128 * CH + kThr - 1) / kThr; // pieces per thread
     constexpr int NB = RT == 2 ? 2 : 4;
     const int tid = (warp - Cfg::kSoftWarps) * 32 + lane;
+    // piece i of a thread is row row0 + i * kStep, chunk pair ch of it; kStep mod 8
+    // is 0 or 4, so the swizzle of odd pieces differs by bit 2 of the chunk or not
+    constexpr int kStep = kThr / CH;
+    static_assert(kThr % CH == 0 && kStep % 4 == 0, "rows of a thread's pieces");
+    const int row0 = tid / CH, ch = tid % CH;
+    // odd halves store their second 16 bytes first, which keeps the 8 lanes of a
+    // row free of bank conflicts
+    const int flip = (ch >> 2) & 1;
+    const uint32_t to0 = (ch >> 2) * kHalf + sw128_offset(row0, (ch & 3) * 2 + flip);
+    constexpr uint32_t swap4 = 4 << 4;
     PartIter<kRows> load_parts = parts;
     Part lx, x;
     lx.live = x.live = 0;
@@ -309,16 +337,21 @@ __global__ void __launch_bounds__((TcCfg<D, RT>::kThreads), 1) attend_tc_kernel(
       if (!more) return;
       const int j0 = (lx.tile0 + lj) * kTile;
       const size_t head = static_cast<size_t>(lx.seq) * a.n_kv_heads + lx.kvh;
-      const uint4 *src = reinterpret_cast<const uint4 *>((b & 1 ? a.v8 : a.k8) + (head * a.cap + j0) * D);
-      const int keys = lx.len - j0;
+      const uint4 *src =
+          reinterpret_cast<const uint4 *>((b & 1 ? a.v8 : a.k8) + (head * a.cap + j0) * D) + tid;
+      const int left = min(lx.len - j0, kTile) * CH - tid;  // pieces from this thread's first on
+      if (left >= (NP - 1) * kThr + 1) {
 #pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        const int q = i * kThr + tid;
-        c[b][i] = make_uint4(0, 0, 0, 0);  // keys past the end are zeros
-        if (q / CH < min(keys, kTile)) c[b][i] = __ldcs(src + q);
+        for (int i = 0; i < NP; ++i) c[b][i] = __ldcs(src + i * kThr);
+      } else {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          c[b][i] = make_uint4(0, 0, 0, 0);  // keys past the end are zeros
+          if (i * kThr < left) c[b][i] = __ldcs(src + i * kThr);
+        }
       }
       ex[b] = -127;
-      if (lane < 8 && lane * 16 < keys)
+      if (lane < 8 && j0 + lane * 16 < lx.len)
         ex[b] = exp_of(__ldg((b & 1 ? a.v_scale : a.k_scale) + head * (a.cap >> p.log2_block) +
                              ((j0 + lane * 16) >> p.log2_block)));
     };
@@ -355,14 +388,21 @@ __global__ void __launch_bounds__((TcCfg<D, RT>::kThreads), 1) attend_tc_kernel(
                                   ((t >> 1) & 1) ^ 1, kWhereConv)))
           break;
         const int top = is_v ? ref : __reduce_max_sync(0xffffffffu, ex[b]);
+        // lanes 0..7: the factor of keys 16 lane ..
+        const uint32_t factor = as_u32(__float2half2_rn(pow2f(max(ex[b] - top, -24))));
         uint8_t *tile = (is_v ? s_v : s_k) + stage * Cfg::kTileBytes;
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-          const int q = i * kThr + tid;
-          const int row = q / CH;
-          const int k = __shfl_sync(0xffffffffu, ex[b], (row >> 4) & 7) - top;
-          if (128 * CH % kThr == 0 || q < 128 * CH)
-            store_f16(tile, row, q % CH, c[b][i], __float2half2_rn(pow2f(max(k, -24))));
+          const __half2 f =
+              as_half2(__shfl_sync(0xffffffffu, factor, ((row0 + i * kStep) >> 4) & 7));
+          if (128 * CH % kThr == 0 || i < NP - 1 || row0 + i * kStep < 128)
+          {
+            uint4 lo, hi;
+            convert16(c[b][i], f, &lo, &hi);
+            const uint32_t to = (to0 ^ (kStep % 8 != 0 && (i & 1) ? swap4 : 0u)) + i * kStep * 128;
+            *reinterpret_cast<uint4 *>(tile + to) = flip ? hi : lo;
+            *reinterpret_cast<uint4 *>(tile + (to ^ 16u)) = flip ? lo : hi;
+          }
         }
         if (!is_v && tid == 0) sh.k_scale[t & 3] = pow2f(max(top, -126));
         fence_proxy_async_smem();
@@ -445,80 +485,93 @@ __global__ void __launch_bounds__((TcCfg<D, RT>::kThreads), 1) attend_tc_kernel(
           tc_fence_after();
           if (warp_rows) {
             const uint32_t s_addr = s_col(buf) + lanes;
-            const float f = q_factor * sh.k_scale[t & 3];
+            // not zero: -infinity has to stay
+            const float f = fmaxf(q_factor * sh.k_scale[t & 3], 1.17549435e-38f);
             const int j0 = (x.tile0 + j) * kTile;
             const int nvis = sees - j0;
             const bool masked = __any_sync(0xffffffffu, nvis < kTile);
+            if (masked) {  // hidden keys' logits become -infinity where they stand
+#pragma unroll 1
+              for (int c = 0; c < 4; ++c) {
+                float v[32];
+                uint32_t u[32];
+                tmem_ld_32x32b_x32(s_addr + 32u * c, v);
+                tmem_ld_wait_regs(v);
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  u[i] = __float_as_uint(c * 32 + i < nvis ? v[i] : -INFINITY);
+                tmem_st_32x32b_x32(s_addr + 32u * c, u);
+              }
+              tmem_st_wait();
+            }
             uint32_t ph[64];
             float sum = 0.f;
-            // probabilities under the row's reference; false: it has to move
-            auto pass = [&](auto with_mask) {
+            bool fine = false;
+            // probabilities under the row's reference, until it need not move; the
+            // first tile begins with the move
+            for (int round = j > 0 ? 0 : 1;; ++round) {
+              if (round > 0) {
+                float top = -INFINITY;
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                  float v[32];
+                  tmem_ld_32x32b_x32(s_addr + 32u * c, v);
+                  tmem_ld_wait_regs(v);
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) top = fmaxf(top, v[i]);
+                }
+                top = top * f - 7.f;
+                float corr = 1.f;
+                if (!fine && top > ref) {
+                  corr = ref == -INFINITY ? 0.f : ex2(ref - top);
+                  ref = top;
+                  l *= corr;
+                }
+                __syncwarp();
+                if (j > 0) {
+                  // O, once the MMAs of the tile before have added to it
+                  if (!(ok = wait_pv(j, t))) break;
+#pragma unroll 1
+                  for (int c = 0; c < D / 32; ++c) {
+                    float v[32];
+                    uint32_t u[32];
+                    tmem_ld_32x32b_x32(o_col(x_tile) + lanes + 32u * c, v);
+                    tmem_ld_wait_regs(v);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(v[i] * corr);
+                    tmem_st_32x32b_x32(o_col(x_tile) + lanes + 32u * c, u);
+                  }
+                  tmem_st_wait();
+                }
+              }
               const float ru = ref == -INFINITY ? 0.f : ref;
-              bool fine = true;
+              const float2 f2 = make_float2(f, f), r2 = make_float2(-ru, -ru);
+              fine = true;
               sum = 0.f;
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
                 float v[32];
                 tmem_ld_32x32b_x32(s_addr + 32u * c, v);
                 tmem_ld_wait_regs(v);
-                float part[4] = {0.f, 0.f, 0.f, 0.f};
+                float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                  float y0 = fmaf(v[i], f, -ru), y1 = fmaf(v[i + 1], f, -ru);
-                  if (decltype(with_mask)::value) {
-                    if (c * 32 + i >= nvis) y0 = -INFINITY;
-                    if (c * 32 + i + 1 >= nvis) y1 = -INFINITY;
-                  }
-                  const float e0 = ex2(y0), e1 = ex2(y1);
-                  part[(i >> 1) & 3] += e0 + e1;
-                  ph[c * 16 + (i >> 1)] = as_u32(__floats2half2_rn(e0, e1));
+                for (int i = 0; i < 16; ++i) {
+                  const float2 y = __ffma2_rn(make_float2(v[2 * i], v[2 * i + 1]), f2, r2);
+                  // kPoly pairs of 16 on the FMA pipe, the rest on the MUFU
+                  const float2 e = (i * kPoly) % 16 < kPoly ? exp2_quartic(y)
+                                                             : make_float2(ex2(y.x), ex2(y.y));
+                  part[i & 1] = __fadd2_rn(part[i & 1], e);
+                  ph[c * 16 + i] = as_u32(__floats2half2_rn(e.x, e.y));
                 }
-                const float s = (part[0] + part[1]) + (part[2] + part[3]);
-                fine &= s <= 32768.f;
-                sum += s;
+                const float2 both = __fadd2_rn(part[0], part[1]);
+                fine &= both.x + both.y <= 32768.f;
+                sum += both.x + both.y;
               }
-              return fine;
-            };
-            using Yes = std::true_type;
-            using No = std::false_type;
-            bool fine = false;
-            if (j > 0) fine = masked ? pass(Yes{}) : pass(No{});
-            if (__any_sync(0xffffffffu, !fine)) {
-              float top = -INFINITY;
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                float v[32];
-                tmem_ld_32x32b_x32(s_addr + 32u * c, v);
-                tmem_ld_wait_regs(v);
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  top = fmaxf(top, c * 32 + i < nvis ? v[i] * f : -INFINITY);
-              }
-              top -= 7.f;
-              float corr = 1.f;
-              if (!fine && top > ref) {
-                corr = ref == -INFINITY ? 0.f : ex2(ref - top);
-                ref = top;
-                l *= corr;
-              }
-              __syncwarp();
-              if (j > 0) {
-                // O, once the MMAs of the tile before have added to it
-                if (!(ok = wait_pv(j, t))) break;
-#pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
-                  float v[32];
-                  uint32_t u[32];
-                  tmem_ld_32x32b_x32(o_col(x_tile) + lanes + 32u * c, v);
-                  tmem_ld_wait_regs(v);
-#pragma unroll
-                  for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(v[i] * corr);
-                  tmem_st_32x32b_x32(o_col(x_tile) + lanes + 32u * c, u);
-                }
-                tmem_st_wait();
-              }
-              pass(Yes{});
+              if (round > 0 || !__any_sync(0xffffffffu, !fine)) break;
             }
+            if (!ok) break;
+            // still above the bound under its own largest logit: not a number
+            if (!fine) sum = __uint_as_float(0x7fc00000u);
             l += sum;
             __syncwarp();  // tcgen05 loads and stores are the whole warp's
             if (p.x_cols > 0) {
@@ -534,7 +587,7 @@ __global__ void __launch_bounds__((TcCfg<D, RT>::kThreads), 1) attend_tc_kernel(
                 for (int i = 0; i < 32; ++i) {
                   const int key = c * 32 + i;
                   if (r < p.x_cols && key < x.len - j0)
-                    xs[static_cast<size_t>(key) * p.x_cols] = key < nvis ? v[i] * f : -INFINITY;
+                    xs[static_cast<size_t>(key) * p.x_cols] = v[i] * f;
                 }
                 __syncwarp();
               }
@@ -553,6 +606,10 @@ __global__ void __launch_bounds__((TcCfg<D, RT>::kThreads), 1) attend_tc_kernel(
         tc_fence_after();
         vscale = sh.v_scale[seg & 3];
         ++seg;
+        if (sees <= x.tile0 * kTile) {  // the row sees none of the part's keys
+          ref = -INFINITY;
+          l = 0.f;
+        }
       }
       if (!warp_rows) continue;
       // ---- the part's end: a whole segment goes out, a part to its slot
@@ -573,7 +630,7 @@ __global__ void __launch_bounds__((TcCfg<D, RT>::kThreads), 1) attend_tc_kernel(
         }
         // rows without a visible key so far hold zeros, whatever the scale
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = x.live > 0 ? v[i] * mul : 0.f;
+        for (int i = 0; i < 32; ++i) v[i] = l != 0.f ? v[i] * mul : 0.f;
         if (row && whole) {
           __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + q_row(a, x.seq, x.kvh, r) * D + 32 * c;
 #pragma unroll
