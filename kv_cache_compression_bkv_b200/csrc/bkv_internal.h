@@ -170,7 +170,8 @@ struct Cache8AttendPlan {
   int row_blocks;    // row blocks per (sequence, KV head)
   int ctas;          // CTAs that share the key tiles
   int x_cols;        // logits kept per key for the weights pass (0: none kept)
-  size_t part_off, lse_off, x_off, bytes;  // workspace sections
+  bool expand;       // K and V are turned into f16 once, in the workspace
+  size_t part_off, lse_off, x_off, pre_off, bytes;  // workspace sections
 };
 Cache8AttendPlan plan_cache8_attend(int n_seqs, int n_q_heads, int n_kv_heads, int head_dim,
                                     int dtype, long long max_len, int T, bool weights);

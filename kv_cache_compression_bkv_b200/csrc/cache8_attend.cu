@@ -1054,6 +1054,22 @@ bool use_mma(int dtype, int head_dim) {
 
 }  // namespace
 
+namespace {
+struct PreSections {
+  size_t k, v, k_scale, v_scale, bytes;
+};
+PreSections pre_sections(int n_seqs, int n_kv_heads, int head_dim, long long max_len) {
+  const size_t heads = static_cast<size_t>(n_seqs) * n_kv_heads, len = align_up(max_len, kTile);
+  PreSections x;
+  x.k = 0;
+  x.v = align_up(heads * len * head_dim * 2, kAlign);
+  x.k_scale = 2 * x.v;
+  x.v_scale = x.k_scale + align_up(heads * (len / kTile) * 4, kAlign);
+  x.bytes = x.v_scale + align_up(heads * 4, kAlign);
+  return x;
+}
+}  // namespace
+
 Cache8AttendPlan plan_cache8_attend(int n_seqs, int n_q_heads, int n_kv_heads, int head_dim,
                                     int dtype, long long max_len, int T, bool weights) {
   Cache8AttendPlan p{};
@@ -1063,6 +1079,14 @@ Cache8AttendPlan plan_cache8_attend(int n_seqs, int n_q_heads, int n_kv_heads, i
   p.row_tiles = mma && rows > 32 ? (rows <= 128 ? 1 : 2) : 0;
   p.block_rows = p.row_tiles ? 128 * p.row_tiles : 8 * p.nt;
   p.row_blocks = static_cast<int>((rows + p.block_rows - 1) / p.block_rows);
+  // Every row block reads all of K and V.  One (up to 256 rows) turns the codes
+  // into f16 as it goes, at the cost of converter warps and shared-memory
+  // bandwidth; several share one conversion: 1024 tokens of 40/8 heads over
+  // 16384 rows, 20 row blocks, took 490 us converting and SPLIT_US with tiles
+  // expanded beforehand.
+  p.expand = p.row_tiles == 2 && p.row_blocks > 1 &&
+             static_cast<long long>(n_seqs) * n_kv_heads *
+                     static_cast<long long>(align_up(max_len, kTile)) < INT32_MAX;
   const long long tiles = (max_len + kTile - 1) / kTile * n_seqs * n_kv_heads * p.row_blocks;
   const int resident = p.row_tiles ? kSms : 2 * kSms;
   p.ctas = static_cast<int>(std::min<long long>(tiles, resident));
@@ -1073,7 +1097,8 @@ Cache8AttendPlan plan_cache8_attend(int n_seqs, int n_q_heads, int n_kv_heads, i
   p.part_off = 0;
   p.lse_off = align_up(part, kAlign);
   p.x_off = p.lse_off + align_up(lse, kAlign);
-  p.bytes = p.x_off + align_up(x, kAlign);
+  p.pre_off = p.x_off + align_up(x, kAlign);
+  p.bytes = p.pre_off + (p.expand ? pre_sections(n_seqs, n_kv_heads, head_dim, max_len).bytes : 0);
   return p;
 }
 
@@ -1091,6 +1116,16 @@ bkv_status launch_cache8_attend(const Cache8AttendArgs &a, const Cache8AttendPla
   p.part = reinterpret_cast<float *>(w + plan.part_off);
   p.lse2 = reinterpret_cast<float *>(w + plan.lse_off);
   p.x = reinterpret_cast<float *>(w + plan.x_off);
+  p.pre_k = nullptr;
+  p.pre_len = static_cast<long long>(align_up(a.max_len, kTile));
+  if (plan.expand) {
+    const PreSections x = pre_sections(a.n_seqs, a.n_kv_heads, a.head_dim, a.max_len);
+    uint8_t *e = w + plan.pre_off;
+    p.pre_k = reinterpret_cast<uint16_t *>(e + x.k);
+    p.pre_v = reinterpret_cast<uint16_t *>(e + x.v);
+    p.pre_k_scale = reinterpret_cast<float *>(e + x.k_scale);
+    p.pre_v_scale = reinterpret_cast<float *>(e + x.v_scale);
+  }
   const bool mma = use_mma(dtype, a.head_dim);
   bool ok;
   if (mma) {

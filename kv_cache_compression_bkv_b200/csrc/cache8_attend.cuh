@@ -26,6 +26,11 @@ struct AttendArgs {
   float *part;       // [ctas][2][rows][2 + head_dim]: max, sum, output
   float *lse2;       // [n_seqs][n_kv_heads][group * T], log2 units
   float *x;          // [n_seqs][n_kv_heads][x_len][x_cols], log2 units
+  // K and V as f16 tiles, [n_seqs][n_kv_heads][pre_len][head_dim], with a K
+  // scale per 128 keys and a V scale per head; NULL: the codes are read
+  uint16_t *pre_k, *pre_v;
+  float *pre_k_scale, *pre_v_scale;
+  long long pre_len;
 };
 
 __device__ __forceinline__ float ex2(float x) {

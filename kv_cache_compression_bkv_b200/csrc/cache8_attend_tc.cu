@@ -30,6 +30,7 @@
 #include "bkv_device_status.cuh"
 #include "cache8_attend.cuh"
 #include "sm100.cuh"
+#include "tma_host.h"
 
 BKV_DEFINE_STATUS_ACCESSOR(take_status_cache8_attend_tc)
 
@@ -150,14 +151,15 @@ __device__ __forceinline__ float2 exp2_quartic(float2 y) {
                      __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
 }
 
-template <int D, int RT>
+template <int D, int RT, bool kPre>
 struct TcCfg {
   static constexpr int kHalves = D / 64;
   static constexpr int kTileBytes = kHalves * kHalf;   // 128 rows (or keys) in f16
   static constexpr int kSoftWarps = 4 * RT;
-  static constexpr int kConvWarps = 11 - kSoftWarps;
+  // warps that bring K and V: converters, or one that issues TMA loads
   // 12 warps, three to a scheduler, leave 168 registers a thread (13: 128)
-  static constexpr int kThreads = 12 * 32;
+  static constexpr int kConvWarps = kPre ? 1 : 11 - kSoftWarps;
+  static constexpr int kThreads = (kSoftWarps + kConvWarps + 1) * 32;
   static constexpr int kSmem = (RT + 4) * kTileBytes + 1024;  // Q, two stages of K and V; alignment
 };
 
@@ -182,9 +184,11 @@ __device__ __forceinline__ void convert16(uint4 c, __half2 f, uint4 *lo, uint4 *
   *hi = make_uint4(h[4], h[5], h[6], h[7]);
 }
 
-template <int D, int RT>
-__global__ void __launch_bounds__((TcCfg<D, RT>::kThreads), 1) attend_tc_kernel(const AttendArgs p) {
-  using Cfg = TcCfg<D, RT>;
+template <int D, int RT, bool kPre>
+__global__ void __launch_bounds__((TcCfg<D, RT, kPre>::kThreads), 1)
+    attend_tc_kernel(const AttendArgs p, const __grid_constant__ CUtensorMap k_map,
+                     const __grid_constant__ CUtensorMap v_map) {
+  using Cfg = TcCfg<D, RT, kPre>;
   constexpr int kRows = 128 * RT;
   extern __shared__ uint8_t smem_raw[];
   __shared__ TcShared sh;
@@ -299,6 +303,41 @@ __global__ void __launch_bounds__((TcCfg<D, RT>::kThreads), 1) attend_tc_kernel(
     }
     commit(&sh.drain);
     mbar_wait_warp(smem_u32(&sh.drain), 0, kWhereDrain);
+  } else if (kPre && warp >= Cfg::kSoftWarps) {
+    // ------------------------------------------------- TMA, from f16 tiles
+    if (lane == 0) {
+      prefetch_tensormap(&k_map);
+      prefetch_tensormap(&v_map);
+    }
+    Part x;
+    int t = 0;
+    bool ok = true;
+    while (ok && parts.next(p, w, units, &x)) {
+      const long long row =
+          (static_cast<long long>(x.seq) * a.n_kv_heads + x.kvh) * p.pre_len + x.tile0 * kTile;
+      for (int j = 0; j < x.live && ok; ++j) {
+        const int stage = t & 1, y = static_cast<int>(row) + j * kTile;
+        for (int kv = 0; kv < 2 && ok; ++kv) {
+          uint64_t *full = kv ? &sh.v_full[stage] : &sh.k_full[stage];
+          if (!(ok = mbar_wait_warp(smem_u32(kv ? &sh.v_empty[stage] : &sh.k_empty[stage]),
+                                    ((t >> 1) & 1) ^ 1, kWhereConv)))
+            break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(smem_u32(full), Cfg::kTileBytes);
+#pragma unroll
+            for (int h = 0; h < Cfg::kHalves; ++h)
+              tma_load_2d(smem_u32((kv ? s_v : s_k) + stage * Cfg::kTileBytes + h * kHalf),
+                          kv ? &v_map : &k_map, smem_u32(full), h * 64, y);
+          }
+        }
+        if (ok) ++t;
+      }
+    }
+    // loads that no MMA waited for must not outlive the CTA
+    for (int i = max(t - 2, 0); i < t; ++i) {
+      mbar_wait_warp(smem_u32(&sh.k_full[i & 1]), (i >> 1) & 1, kWhereDrain);
+      mbar_wait_warp(smem_u32(&sh.v_full[i & 1]), (i >> 1) & 1, kWhereDrain);
+    }
   } else if (warp >= Cfg::kSoftWarps) {
     // ------------------------------------------------------- the converters
     // K and V of a tile in turn, each by all converter warps; NB of them are
@@ -477,8 +516,11 @@ __global__ void __launch_bounds__((TcCfg<D, RT>::kThreads), 1) attend_tc_kernel(
           if (lane == 0) mbar_arrive(smem_u32(&sh.q_full[x_tile]));
         }
         const float q_factor = vscale;
+        const size_t head = static_cast<size_t>(x.seq) * a.n_kv_heads + x.kvh;
         for (int j = 0; j < x.live; ++j, ++t) {
           const int buf = RT == 2 ? x_tile : t & 1;
+          float ks = 0.f;
+          if (kPre) ks = __ldg(p.pre_k_scale + head * (p.pre_len / kTile) + x.tile0 + j);
           if (!(ok = mbar_wait_warp(smem_u32(&sh.s_full[buf]), RT == 2 ? t & 1 : (t >> 1) & 1,
                                     kWhereSoft)))
             break;
@@ -486,7 +528,7 @@ __global__ void __launch_bounds__((TcCfg<D, RT>::kThreads), 1) attend_tc_kernel(
           if (warp_rows) {
             const uint32_t s_addr = s_col(buf) + lanes;
             // not zero: -infinity has to stay
-            const float f = fmaxf(q_factor * sh.k_scale[t & 3], 1.17549435e-38f);
+            const float f = fmaxf(q_factor * (kPre ? ks : sh.k_scale[t & 3]), 1.17549435e-38f);
             const int j0 = (x.tile0 + j) * kTile;
             const int nvis = sees - j0;
             const bool masked = __any_sync(0xffffffffu, nvis < kTile);
@@ -604,7 +646,7 @@ __global__ void __launch_bounds__((TcCfg<D, RT>::kThreads), 1) attend_tc_kernel(
         if (!ok) break;
         if (!(ok = mbar_wait_warp(smem_u32(&sh.pv_done[x_tile]), (t - 1) & 1, kWhereOut))) break;
         tc_fence_after();
-        vscale = sh.v_scale[seg & 3];
+        vscale = kPre ? __ldg(p.pre_v_scale + head) : sh.v_scale[seg & 3];
         ++seg;
         if (sees <= x.tile0 * kTile) {  // the row sees none of the part's keys
           ref = -INFINITY;
@@ -668,21 +710,85 @@ __global__ void __launch_bounds__((TcCfg<D, RT>::kThreads), 1) attend_tc_kernel(
   }
 }
 
-template <int D, int RT>
+// K and V of every sequence as f16 tiles of 128 keys (rows past the end zeros),
+// for calls whose row blocks would each convert them again: codes times the
+// power of two between the block's scale and the tile's largest (K) or the
+// head's largest (V).  A copy: 1 byte read, 2 written per element.
+template <int D>
+__global__ void __launch_bounds__(256) expand_kernel(const AttendArgs p) {
+  constexpr int CH = D / 16, NP = 128 * CH / 256;
+  const Cache8AttendArgs &a = p.a;
+  const size_t head = blockIdx.y;
+  const SeqInfo q = seq_info(a, static_cast<int>(head) / a.n_kv_heads);
+  const int tile = blockIdx.x, j0 = tile * kTile;
+  if (tile >= q.tiles) return;
+  const int lane = threadIdx.x & 31;
+  const size_t blk = head * (a.cap >> p.log2_block);
+  const size_t src = (head * a.cap + j0) * D;
+  uint4 c[2][NP];
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int id = i * 256 + threadIdx.x;
+      c[kv][i] = make_uint4(0, 0, 0, 0);
+      if (j0 + id / CH < q.len)
+        c[kv][i] = __ldcs(reinterpret_cast<const uint4 *>((kv ? a.v8 : a.k8) + src) + id);
+    }
+  int ref = -127;  // the head's largest V scale
+  for (int i = lane; i <= (q.len - 1) >> p.log2_block; i += 32)
+    ref = max(ref, exp_of(__ldg(a.v_scale + blk + i)));
+  ref = __reduce_max_sync(0xffffffffu, ref);
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv) {
+    int ex = -127;
+    if (lane < 8 && j0 + lane * 16 < q.len)
+      ex = exp_of(__ldg((kv ? a.v_scale : a.k_scale) + blk + ((j0 + lane * 16) >> p.log2_block)));
+    const int top = kv ? ref : __reduce_max_sync(0xffffffffu, ex);
+    const uint32_t factor = as_u32(__float2half2_rn(pow2f(max(ex - top, -24))));
+    uint4 *dst = reinterpret_cast<uint4 *>((kv ? p.pre_v : p.pre_k) +
+                                           (head * p.pre_len + j0) * D);
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int id = i * 256 + threadIdx.x;
+      const __half2 f = as_half2(__shfl_sync(0xffffffffu, factor, (id / CH) >> 4));
+      convert16(c[kv][i], f, &dst[2 * id], &dst[2 * id + 1]);
+    }
+    if (threadIdx.x == 0) {
+      if (kv == 0) p.pre_k_scale[head * (p.pre_len / kTile) + tile] = pow2f(max(top, -126));
+      if (kv == 1 && tile == 0) p.pre_v_scale[head] = pow2f(max(top, -126));
+    }
+  }
+}
+
+template <int D, int RT, bool kPre>
 bool run_tc(const AttendArgs &p, cudaStream_t s) {
   static int done[64];
-  using Cfg = TcCfg<D, RT>;
+  using Cfg = TcCfg<D, RT, kPre>;
   static_assert(Cfg::kSmem + sizeof(TcShared) <= 227 * 1024, "shared memory");
-  if (!ensure_smem_limit(attend_tc_kernel<D, RT>, Cfg::kSmem, done)) return false;
-  attend_tc_kernel<D, RT><<<p.ctas, Cfg::kThreads, Cfg::kSmem, s>>>(p);
+  if (!ensure_smem_limit(attend_tc_kernel<D, RT, kPre>, Cfg::kSmem, done)) return false;
+  CUtensorMap k_map{}, v_map{};
+  if (kPre) {
+    const unsigned heads = static_cast<unsigned>(p.a.n_seqs) * p.a.n_kv_heads;
+    const unsigned long long rows = static_cast<unsigned long long>(heads) * p.pre_len;
+    if (!make_bf16_rows_map(&k_map, p.pre_k, rows, 128, D) ||
+        !make_bf16_rows_map(&v_map, p.pre_v, rows, 128, D))
+      return false;
+    expand_kernel<D><<<dim3(static_cast<unsigned>(p.pre_len / kTile), heads), 256, 0, s>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return false;
+  }
+  attend_tc_kernel<D, RT, kPre><<<p.ctas, Cfg::kThreads, Cfg::kSmem, s>>>(p, k_map, v_map);
   return cudaGetLastError() == cudaSuccess;
 }
 
 }  // namespace
 
 bool launch_attend_tc(const cache8::AttendArgs &p, int row_tiles, cudaStream_t s) {
-  if (p.a.head_dim == 128) return row_tiles == 1 ? run_tc<128, 1>(p, s) : run_tc<128, 2>(p, s);
-  return row_tiles == 1 ? run_tc<64, 1>(p, s) : run_tc<64, 2>(p, s);
+  if (p.pre_k)
+    return p.a.head_dim == 128 ? run_tc<128, 2, true>(p, s) : run_tc<64, 2, true>(p, s);
+  if (p.a.head_dim == 128)
+    return row_tiles == 1 ? run_tc<128, 1, false>(p, s) : run_tc<128, 2, false>(p, s);
+  return row_tiles == 1 ? run_tc<64, 1, false>(p, s) : run_tc<64, 2, false>(p, s);
 }
 
 }  // namespace bkv
