@@ -1082,8 +1082,8 @@ Cache8AttendPlan plan_cache8_attend(int n_seqs, int n_q_heads, int n_kv_heads, i
   // Every row block reads all of K and V.  One (up to 256 rows) turns the codes
   // into f16 as it goes, at the cost of converter warps and shared-memory
   // bandwidth; several share one conversion: 1024 tokens of 40/8 heads over
-  // 16384 rows, 20 row blocks, took 490 us converting and SPLIT_US with tiles
-  // expanded beforehand.
+  // 16384 rows, 20 row blocks, took 490 us converting and 385
+  // with the tiles expanded beforehand.
   p.expand = p.row_tiles == 2 && p.row_blocks > 1 &&
              static_cast<long long>(n_seqs) * n_kv_heads *
                      static_cast<long long>(align_up(max_len, kTile)) < INT32_MAX;

@@ -124,32 +124,7 @@ __device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t addr, uint32_t m
   return d;
 }
 
-constexpr int kPoly = 4;          // of 16 pairs of exps, those on the FMA pipe
 constexpr int kHalf = 128 * 128;  // bytes of 128 rows x 64 f16
-
-// 2^y of a pair on the FMA pipe: y = n + f with n = round(y) by the 1.5 * 2^23
-// trick, a quartic for 2^f on [-1/2, 1/2] (least largest relative error,
-// 2.6e-6), n added into its exponent.  y is held to [-126, 127], NaN stays NaN
-// until the last addition, which makes it a finite number above 2^127.
-__device__ __forceinline__ float clamp_nan(float y) {
-  asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(y));  // -126
-  asm("min.NaN.f32 %0, %0, 0f42FE0000;" : "+f"(y));  // 127
-  return y;
-}
-__device__ __forceinline__ float2 exp2_quartic(float2 y) {
-  constexpr float kRound = 12582912.f;
-  y.x = clamp_nan(y.x);
-  y.y = clamp_nan(y.y);
-  const float2 t = __fadd2_rn(y, make_float2(kRound, kRound));
-  const float2 n = __fadd2_rn(t, make_float2(-kRound, -kRound));
-  const float2 f = __ffma2_rn(n, make_float2(-1.f, -1.f), y);
-  float2 p = __ffma2_rn(f, make_float2(0.009570102f, 0.009570102f), make_float2(0.05591786f, 0.05591786f));
-  p = __ffma2_rn(p, f, make_float2(0.24024744f, 0.24024744f));
-  p = __ffma2_rn(p, f, make_float2(0.6931218f, 0.6931218f));
-  p = __ffma2_rn(p, f, make_float2(0.9999993f, 0.9999993f));
-  return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
-                     __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
-}
 
 template <int D, int RT, bool kPre>
 struct TcCfg {
@@ -590,24 +565,25 @@ __global__ void __launch_bounds__((TcCfg<D, RT, kPre>::kThreads), 1)
               const float2 f2 = make_float2(f, f), r2 = make_float2(-ru, -ru);
               fine = true;
               sum = 0.f;
+              float v[2][32];  // the next columns are on their way while these are used
+              tmem_ld_32x32b_x32(s_addr, v[0]);
+              tmem_ld_wait_regs(v[0]);
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
-                float v[32];
-                tmem_ld_32x32b_x32(s_addr + 32u * c, v);
-                tmem_ld_wait_regs(v);
+                if (c < 3) tmem_ld_32x32b_x32(s_addr + 32u * (c + 1), v[(c + 1) & 1]);
                 float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                  const float2 y = __ffma2_rn(make_float2(v[2 * i], v[2 * i + 1]), f2, r2);
-                  // kPoly pairs of 16 on the FMA pipe, the rest on the MUFU
-                  const float2 e = (i * kPoly) % 16 < kPoly ? exp2_quartic(y)
-                                                             : make_float2(ex2(y.x), ex2(y.y));
+                  const float2 y =
+                      __ffma2_rn(make_float2(v[c & 1][2 * i], v[c & 1][2 * i + 1]), f2, r2);
+                  const float2 e = make_float2(ex2(y.x), ex2(y.y));
                   part[i & 1] = __fadd2_rn(part[i & 1], e);
                   ph[c * 16 + i] = as_u32(__floats2half2_rn(e.x, e.y));
                 }
                 const float2 both = __fadd2_rn(part[0], part[1]);
                 fine &= both.x + both.y <= 32768.f;
                 sum += both.x + both.y;
+                if (c < 3) tmem_ld_wait_regs(v[(c + 1) & 1]);
               }
               if (round > 0 || !__any_sync(0xffffffffu, !fine)) break;
             }
@@ -648,10 +624,6 @@ __global__ void __launch_bounds__((TcCfg<D, RT, kPre>::kThreads), 1)
         tc_fence_after();
         vscale = kPre ? __ldg(p.pre_v_scale + head) : sh.v_scale[seg & 3];
         ++seg;
-        if (sees <= x.tile0 * kTile) {  // the row sees none of the part's keys
-          ref = -INFINITY;
-          l = 0.f;
-        }
       }
       if (!warp_rows) continue;
       // ---- the part's end: a whole segment goes out, a part to its slot

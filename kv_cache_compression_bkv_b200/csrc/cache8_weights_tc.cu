@@ -43,7 +43,7 @@ struct WCfg {
 struct WShared {
   uint64_t full[2], empty[2], tfull[2], tempty[2], drain;
   uint32_t tmem;
-  alignas(16) float z[2][128];  // lse of the rows of two tiles
+  alignas(16) float z[2][128];  // minus the lse of the rows of two tiles
 };
 
 // two e4m3 codes -> two bf16, exact
@@ -168,12 +168,12 @@ __global__ void __launch_bounds__(kThreads, 2)
         __ldg(a.k_scale + head * (a.cap >> p.log2_block) + (min(key, q.len - 1) >> p.log2_block)) *
         (a.scale * kLog2e);
     const float *lse2 = p.lse2 + head * a.group * a.T;
-    auto z_of = [&](int it) {  // this thread's row of tile it
+    auto z_of = [&](int it) {  // minus the lse of this thread's row of tile it
       const int g = it / per_head, t = (tb0 + it - g * per_head) * 128 + threadIdx.x;
-      return t < q.n ? __ldg(lse2 + t * a.group + g) : 0.f;
+      return t < q.n ? -__ldg(lse2 + t * a.group + g) : 0.f;
     };
     bool ok = true;
-    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     float z_next = n_tiles > 0 ? z_of(0) : 0.f;
     for (int it = 0; it < n_tiles; ++it) {
       const int s = it & 1;
@@ -188,43 +188,44 @@ __global__ void __launch_bounds__(kThreads, 2)
       // rows t0 + c see the key from c = first on; tokens end at c = last
       const int first = key - seen0 - t0 + 1, last = q.n - t0;
       const bool masked = __any_sync(0xffffffffu, first > 0) || last < 128;
+      float buf[2][32];  // the next columns are on their way while these are used
+      tmem_ld_32x32b_x32(tmem + 128u * s + lanes, buf[0]);
+      tmem_ld_wait_regs(buf[0]);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        float v[32];
-        tmem_ld_32x32b_x32(tmem + 128u * s + lanes + 32u * c, v);
-        tmem_ld_wait_regs(v);
-        if (c == 3) {
+        const float(&v)[32] = buf[c & 1];
+        if (c < 3) {
+          tmem_ld_32x32b_x32(tmem + 128u * s + lanes + 32u * (c + 1), buf[(c + 1) & 1]);
+        } else {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&sh.tempty[s]));
         }
         const float4 *zs = reinterpret_cast<const float4 *>(&sh.z[s][32 * c]);
         if (!masked) {
+          const float2 f2 = make_float2(f, f);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const float4 z = zs[i];
-            sum[0] += ex2(fmaf(v[4 * i], f, -z.x));
-            sum[1] += ex2(fmaf(v[4 * i + 1], f, -z.y));
-            sum[2] += ex2(fmaf(v[4 * i + 2], f, -z.z));
-            sum[3] += ex2(fmaf(v[4 * i + 3], f, -z.w));
+            const float2 y0 = __ffma2_rn(make_float2(v[4 * i], v[4 * i + 1]), f2, make_float2(z.x, z.y));
+            const float2 y1 = __ffma2_rn(make_float2(v[4 * i + 2], v[4 * i + 3]), f2, make_float2(z.z, z.w));
+            sum[0] = __fadd2_rn(sum[0], make_float2(ex2(y0.x), ex2(y0.y)));
+            sum[1] = __fadd2_rn(sum[1], make_float2(ex2(y1.x), ex2(y1.y)));
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 z4 = zs[i];
-            const float z[4] = {z4.x, z4.y, z4.z, z4.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int col = 32 * c + 4 * i + k;
-              const float e = ex2(fmaf(v[4 * i + k], f, -z[k]));
-              sum[k] += col >= first && col < last ? e : 0.f;
-            }
+          for (int i = 0; i < 32; ++i) {
+            const int col = 32 * c + i;
+            const float e = ex2(fmaf(v[i], f, sh.z[s][col]));
+            sum[i & 1].x += col >= first && col < last ? e : 0.f;
           }
         }
+        if (c < 3) tmem_ld_wait_regs(buf[(c + 1) & 1]);
       }
     }
     if (key < q.len) {
-      float total = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      const float2 both = __fadd2_rn(sum[0], sum[1]);
+      float total = both.x + both.y;
       // the new tokens' own rows start at zero
       if (a.w_in && key < q.len - q.n) total = fmaf(a.decay, a.w_in[head * a.cap + key], total);
       if (ok) a.w_out[head * a.cap + key] = total;
