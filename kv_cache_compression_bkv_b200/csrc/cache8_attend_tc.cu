@@ -79,36 +79,22 @@ struct PartIter {
   }
 };
 
-// The MMAs, issued by the lane with lead != 0 under a predicate rather than a
-// branch: the whole warp computes the operands, so that they stay in uniform
-// registers.  In a branch of one lane every operand has to be moved there, and
-// an MMA took 92 cycles to issue against the 64 that it runs.  Descriptors are
-// (lo, hi) pairs; only the address in lo changes.
-__device__ __forceinline__ void umma_ss(uint32_t lead, uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
-                                        uint32_t hi, uint32_t idesc, uint32_t accumulate) {
+// True in one lane of the (converged) warp; as a predicate that the compiler
+// knows to be one thread's, it leaves the MMAs' operands in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
-      "setp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %0, 0;\n\t"
-      "mov.b64 a, {%2, %4};\n\tmov.b64 b, {%3, %4};\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%1], a, b, %5, p;\n\t}" ::"r"(lead),
-      "r"(d_tmem), "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
-      : "memory");
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
 }
-__device__ __forceinline__ void umma_ts(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
-                                        uint32_t hi, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                        uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
-      "setp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %0, 0;\n\t"
-      "mov.b64 b, {%3, %4};\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], b, %5, p;\n\t}" ::"r"(lead),
-      "r"(d_tmem), "r"(a_tmem), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-__device__ __forceinline__ void umma_commit_lead(uint32_t lead, uint32_t bar) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %0, 0;\n\t"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t}" ::"r"(lead),
-      "r"(bar)
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 
@@ -237,35 +223,39 @@ __global__ void __launch_bounds__((TcCfg<D, RT, kPre>::kThreads), 1)
     // ------------------------------------------------------------- the MMAs
     constexpr uint32_t idesc_qk = idesc_f16_f32(128, 128, false);
     constexpr uint32_t idesc_pv = idesc_f16_f32(128, D, true);
-    const uint32_t lead = lane == 0;
     const uint64_t q_desc = smem_desc_k_sw128(smem_u32(s_q)), k_desc = smem_desc_k_sw128(smem_u32(s_k));
     const uint64_t v_desc = smem_desc_mn_sw128(smem_u32(s_v), kHalf);
-    const uint32_t q_lo = static_cast<uint32_t>(q_desc), k_lo = static_cast<uint32_t>(k_desc),
-                   v_lo = static_cast<uint32_t>(v_desc);
-    const uint32_t k_hi = static_cast<uint32_t>(k_desc >> 32), v_hi = static_cast<uint32_t>(v_desc >> 32);
     auto qk = [&](int x, int t, int buf) {  // S[buf] = Q_x K(t)^T
-      const uint32_t a_lo = q_lo + x * (Cfg::kTileBytes >> 4), b_lo = k_lo + (t & 1) * (Cfg::kTileBytes >> 4);
+      if (elect_one()) {
+        const uint64_t ad = q_desc + x * (Cfg::kTileBytes >> 4), bd = k_desc + (t & 1) * (Cfg::kTileBytes >> 4);
 #pragma unroll
-      for (int s = 0; s < D / 16; ++s) {
-        const uint32_t off = ((s >> 2) * kHalf + (s & 3) * 32) >> 4;
-        umma_ss(lead, s_col(buf), a_lo + off, b_lo + off, k_hi, idesc_qk, s != 0);
+        for (int s = 0; s < D / 16; ++s) {
+          const uint32_t off = ((s >> 2) * kHalf + (s & 3) * 32) >> 4;
+          umma_f16(s_col(buf), ad + off, bd + off, idesc_qk, s != 0);
+        }
+        umma_commit(smem_u32(&sh.s_full[buf]));
       }
-      umma_commit_lead(lead, smem_u32(&sh.s_full[buf]));
+      __syncwarp();
     };
     auto pv = [&](int x, int t, int buf, bool first) {  // O_x += P[buf] V(t)
-      const uint32_t b_lo = v_lo + (t & 1) * (Cfg::kTileBytes >> 4);
+      if (elect_one()) {
+        const uint64_t bd = v_desc + (t & 1) * (Cfg::kTileBytes >> 4);
 #pragma unroll
-      for (int s = 0; s < 8; ++s)
-        umma_ts(lead, o_col(x), s_col(buf) + 8u * s, b_lo + s * (2048 >> 4), v_hi, idesc_pv,
-                !(first && s == 0));
-      umma_commit_lead(lead, smem_u32(&sh.pv_done[x]));
+        for (int s = 0; s < 8; ++s)
+          umma_ts(o_col(x), s_col(buf) + 8u * s, bd + s * (2048 >> 4), idesc_pv, !(first && s == 0));
+        umma_commit(smem_u32(&sh.pv_done[x]));
+      }
+      __syncwarp();
     };
     auto wait = [&](uint64_t *bar, int phase) {
       const bool ok = mbar_wait_warp(smem_u32(bar), phase & 1, kWhereMma);
       tc_fence_after();
       return ok;
     };
-    auto commit = [&](uint64_t *bar) { umma_commit_lead(lead, smem_u32(bar)); };
+    auto commit = [&](uint64_t *bar) {
+      if (elect_one()) umma_commit(smem_u32(bar));
+      __syncwarp();
+    };
     Part x;
     int t = 0, seg = 0;
     bool ok = true;
