@@ -39,6 +39,16 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// True in one lane of the (converged) warp; as a predicate that the compiler
+// knows to be one thread's, it leaves the MMAs' operands in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+
 // Programmatic dependent launch: the next kernel of the stream may start, and
 // the wait, in that kernel, for everything before it.
 __device__ __forceinline__ void pdl_launch_dependents() {

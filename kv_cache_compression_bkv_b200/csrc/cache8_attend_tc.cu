@@ -79,15 +79,6 @@ struct PartIter {
   }
 };
 
-// True in one lane of the (converged) warp; as a predicate that the compiler
-// knows to be one thread's, it leaves the MMAs' operands in uniform registers.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t one;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(one));
-  return one != 0;
-}
 __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
                                         uint32_t idesc, uint32_t accumulate) {
   asm volatile(

@@ -6,8 +6,8 @@
 // turned into bf16 once (exact), and walks the query rows 128 at a time: TMA
 // brings them as they are (bf16, one query head's tokens after another's; the
 // sum does not ask for the order), D[128 keys][128 rows] is formed on
-// tcgen05 into one of two TMEM accumulators, and four epilogue warps, a key a
-// lane, add exp2(s f - z_r): f, the key's factor, is the lane's own, z_r comes
+// tcgen05 into one of two TMEM accumulators, and the four epilogue warps of that
+// accumulator, a key a lane, add exp2(s f - z_r): f, the key's factor, is the lane's own, z_r comes
 // from shared memory.  Two CTAs an SM, so that one's beginning and waits lie
 // under the other's exps.
 //
@@ -30,7 +30,8 @@ using namespace sm100;
 
 enum : int { kWhereProd = 641, kWhereMma = 642, kWhereEpi = 643, kWhereDrain = 644 };
 
-constexpr int kThreads = 192;      // 4 epilogue warps, TMA, MMA
+constexpr int kEpiWarps = 8;       // four per accumulator
+constexpr int kThreads = (kEpiWarps + 2) * 32;  // and TMA, MMA
 constexpr int kHalf = 128 * 128;   // bytes of 128 rows x 64 bf16
 
 template <int D>
@@ -44,6 +45,7 @@ struct WShared {
   uint64_t full[2], empty[2], tfull[2], tempty[2], drain;
   uint32_t tmem;
   alignas(16) float z[2][128];  // minus the lse of the rows of two tiles
+  float sum[128];               // the odd tiles' part of the keys' sums
 };
 
 // two e4m3 codes -> two bf16, exact
@@ -79,7 +81,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int per_head = max(t_tiles - tb0, 0);
   const int n_tiles = per_head * a.group;
 
-  if (warp == 5) {
+  if (warp == kEpiWarps + 1) {
     tmem_alloc(smem_u32(&sh.tmem), 256);
     tmem_relinquish();
     if (lane == 0) {
@@ -93,11 +95,11 @@ __global__ void __launch_bounds__(kThreads, 2)
       fence_barrier_init();
     }
   }
-  if (warp < 4) {  // the keys' codes as bf16; keys past the end are zeros
+  if (warp < kEpiWarps) {  // the keys' codes as bf16; keys past the end are zeros
     const uint4 *src = reinterpret_cast<const uint4 *>(a.k8 + (head * a.cap + j0) * D);
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
-      const int id = i * 128 + threadIdx.x;
+    for (int i = 0; i < D / 32; ++i) {
+      const int id = i * 256 + threadIdx.x;
       const int row = id / (D / 16), ch = id % (D / 16);
       uint4 c = make_uint4(0, 0, 0, 0);
       if (j0 + row < q.len) c = __ldg(src + id);
@@ -121,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
 
-  if (warp == 4) {
+  if (warp == kEpiWarps) {
     if (lane == 0) {
       prefetch_tensormap(&q_map);
       int it = 0;
@@ -140,47 +142,51 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int t = max(it - 2, 0); t < it; ++t)
         mbar_wait(smem_u32(&sh.full[t & 1]), (t >> 1) & 1, kWhereDrain);
     }
-  } else if (warp == 5) {
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_bf16_f32(128, 128);
-      for (int it = 0; it < n_tiles; ++it) {
-        const int s = it & 1;
-        if (!mbar_wait(smem_u32(&sh.full[s]), (it >> 1) & 1, kWhereMma)) break;
-        if (!mbar_wait(smem_u32(&sh.tempty[s]), ((it >> 1) & 1) ^ 1, kWhereMma)) break;
-        tc_fence_after();
+  } else if (warp == kEpiWarps + 1) {
+    constexpr uint32_t idesc = idesc_bf16_f32(128, 128);
+    const uint64_t k_desc = smem_desc_k_sw128(smem_u32(s_k)), q_desc = smem_desc_k_sw128(smem_u32(s_q));
+    for (int it = 0; it < n_tiles; ++it) {
+      const int s = it & 1;
+      if (!mbar_wait_warp(smem_u32(&sh.full[s]), (it >> 1) & 1, kWhereMma)) break;
+      if (!mbar_wait_warp(smem_u32(&sh.tempty[s]), ((it >> 1) & 1) ^ 1, kWhereMma)) break;
+      tc_fence_after();
+      if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (k >> 2) * kHalf + (k & 3) * 32;
-          umma_f16(tmem + 128u * s, smem_desc_k_sw128(smem_u32(s_k) + off),
-                   smem_desc_k_sw128(smem_u32(s_q) + s * Cfg::kTileBytes + off), idesc, k != 0);
+          const uint32_t off = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
+          umma_f16(tmem + 128u * s, k_desc + off, q_desc + s * (Cfg::kTileBytes >> 4) + off, idesc,
+                   k != 0);
         }
         umma_commit(smem_u32(&sh.empty[s]));
         umma_commit(smem_u32(&sh.tfull[s]));
       }
-      umma_commit(smem_u32(&sh.drain));
-      mbar_wait(smem_u32(&sh.drain), 0, kWhereDrain);
+      __syncwarp();
     }
+    if (elect_one()) umma_commit(smem_u32(&sh.drain));
     __syncwarp();
+    mbar_wait_warp(smem_u32(&sh.drain), 0, kWhereDrain);
   } else {
-    const int key = j0 + threadIdx.x;
-    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    const int s = warp >> 2, row = threadIdx.x & 127;  // accumulator, and tiles s, s + 2, ..
+    const int key = j0 + row;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const float f =
         __ldg(a.k_scale + head * (a.cap >> p.log2_block) + (min(key, q.len - 1) >> p.log2_block)) *
         (a.scale * kLog2e);
     const float *lse2 = p.lse2 + head * a.group * a.T;
     auto z_of = [&](int it) {  // minus the lse of this thread's row of tile it
-      const int g = it / per_head, t = (tb0 + it - g * per_head) * 128 + threadIdx.x;
+      const int g = it / per_head, t = (tb0 + it - g * per_head) * 128 + row;
       return t < q.n ? -__ldg(lse2 + t * a.group + g) : 0.f;
     };
     bool ok = true;
     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-    float z_next = n_tiles > 0 ? z_of(0) : 0.f;
-    for (int it = 0; it < n_tiles; ++it) {
-      const int s = it & 1;
-      sh.z[s][threadIdx.x] = z_next;
-      if (it + 1 < n_tiles) z_next = z_of(it + 1);
-      // every epilogue warp comes here in every round, whatever its waits gave
-      asm volatile("bar.sync 1, 128;" ::: "memory");
+    float z_next = s < n_tiles ? z_of(s) : 0.f;
+    for (int it = s; it < n_tiles; it += 2) {
+      // every warp of the four comes to both barriers in every round, whatever
+      // its waits gave: the tile before's rows have been read, this one's are there
+      asm volatile("bar.sync %0, 128;" ::"r"(1 + s) : "memory");
+      sh.z[s][row] = z_next;
+      if (it + 2 < n_tiles) z_next = z_of(it + 2);
+      asm volatile("bar.sync %0, 128;" ::"r"(1 + s) : "memory");
       if (ok && !mbar_wait_warp(smem_u32(&sh.tfull[s]), (it >> 1) & 1, kWhereEpi)) ok = false;
       if (!ok) continue;
       tc_fence_after();
@@ -188,15 +194,12 @@ __global__ void __launch_bounds__(kThreads, 2)
       // rows t0 + c see the key from c = first on; tokens end at c = last
       const int first = key - seen0 - t0 + 1, last = q.n - t0;
       const bool masked = __any_sync(0xffffffffu, first > 0) || last < 128;
-      float buf[2][32];  // the next columns are on their way while these are used
-      tmem_ld_32x32b_x32(tmem + 128u * s + lanes, buf[0]);
-      tmem_ld_wait_regs(buf[0]);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const float(&v)[32] = buf[c & 1];
-        if (c < 3) {
-          tmem_ld_32x32b_x32(tmem + 128u * s + lanes + 32u * (c + 1), buf[(c + 1) & 1]);
-        } else {
+        float v[32];
+        tmem_ld_32x32b_x32(tmem + 128u * s + lanes + 32u * c, v);
+        tmem_ld_wait_regs(v);
+        if (c == 3) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&sh.tempty[s]));
@@ -220,12 +223,14 @@ __global__ void __launch_bounds__(kThreads, 2)
             sum[i & 1].x += col >= first && col < last ? e : 0.f;
           }
         }
-        if (c < 3) tmem_ld_wait_regs(buf[(c + 1) & 1]);
       }
     }
-    if (key < q.len) {
-      const float2 both = __fadd2_rn(sum[0], sum[1]);
-      float total = both.x + both.y;
+    const float2 both = __fadd2_rn(sum[0], sum[1]);
+    float total = both.x + both.y;
+    if (s == 1) sh.sum[row] = ok ? total : __uint_as_float(0x7fc00000u);
+    asm volatile("bar.sync 3, 256;" ::: "memory");
+    if (s == 0 && key < q.len) {
+      total += sh.sum[row];
       // the new tokens' own rows start at zero
       if (a.w_in && key < q.len - q.n) total = fmaf(a.decay, a.w_in[head * a.cap + key], total);
       if (ok) a.w_out[head * a.cap + key] = total;
@@ -233,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 5) {
+  if (warp == kEpiWarps + 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 256);
   }
