@@ -82,8 +82,7 @@ __device__ __forceinline__ void write_segment(const AttendArgs &p, const float *
   if (threadIdx.x < kRows) {
     const int r = threadIdx.x;
     if (!whole) {
-      part[r] = m[r];
-      part[kRows + r] = l[r];
+      *reinterpret_cast<float2 *>(part + 2 * r) = make_float2(m[r], l[r]);
     } else if (r0 + r < rows) {
       store_lse(p, seq, kvh, r0 + r, m[r], l[r]);
     }
@@ -107,9 +106,18 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool there) {
+// Codes are read once a call: first to go from L2, where the kept logits and the
+// parts wait for the join.
+__device__ __forceinline__ uint64_t evict_first() {
+  uint64_t policy;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+  return policy;
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool there,
+                                           uint64_t policy) {
   const int n = there ? 16 : 0;  // 0: the 16 bytes are filled with zeros, nothing is read
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst),
+               "l"(src), "r"(n), "l"(policy)
                : "memory");
 }
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
@@ -224,6 +232,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_mma_kernel(const AttendArg
                         warp * Cfg::kStages * Cfg::kStageBytes;
   const uint8_t *ring_ptr = smem + warp * Cfg::kStages * Cfg::kStageBytes;
 
+  const uint64_t policy = evict_first();
   // ---- loads: this lane's 16-byte pieces of a tile, with the swizzles that
   // make both reads below free of bank conflicts
   constexpr int PIECES = kKeys * CH / 32;
@@ -264,8 +273,8 @@ __global__ void __launch_bounds__(kThreads, 2) attend_mma_kernel(const AttendArg
       for (int i = 0; i < PIECES; ++i) {
         const bool ok = lrow + i * (32 / CH) < there;
         const uint32_t vd = D == 128 ? v_dst0 ^ ((i & 1) << 6) : v_dst0;
-        cp_async16(dst + k_dst + i * 512, k_src + off + i * 512, ok);
-        cp_async16(dst + vd + i * 512, v_src + off + i * 512, ok);
+        cp_async16(dst + k_dst + i * 512, k_src + off + i * 512, ok, policy);
+        cp_async16(dst + vd + i * 512, v_src + off + i * 512, ok, policy);
       }
       if (lane < 4 && (lane >> 1) * 16 < there)
         cp_async4(dst + 2 * kKeys * D + lane * 4, sc_src + ((j0 + (lane >> 1) * 16) >> p.log2_block));
@@ -623,6 +632,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) attend_simt_kernel(const Atte
   Cursor cur, ahead;
   cur.seek(a, w, units, mine, t0);
   ahead = cur;
+  const uint64_t policy = evict_first();
   // the next tile's codes and scales of this warp
   int issued = 0;
   auto issue = [&]() {
@@ -638,8 +648,8 @@ __global__ void __launch_bounds__(kSimtThreads, 2) attend_simt_kernel(const Atte
         const int key = q / ch;
         const uint32_t to = dst + key * (D + 16) + (q - key * ch) * 16;
         const bool there = j0 + key < ahead.q.len;
-        cp_async16(to, a.k8 + off + q * 16, there);
-        cp_async16(to + kSimtKeys * (D + 16), a.v8 + off + q * 16, there);
+        cp_async16(to, a.k8 + off + q * 16, there, policy);
+        cp_async16(to + kSimtKeys * (D + 16), a.v8 + off + q * 16, there, policy);
       }
       if (lane < 2)
         cp_async4(dst + 2 * kSimtKeys * (D + 16) + lane * 4,
@@ -779,6 +789,26 @@ __device__ __forceinline__ void store_weight(const Cache8AttendArgs &a, size_t h
   a.w_out[head * a.cap + j] = sum;
 }
 
+// The reference and sum of a row over its parts, by a whole warp: a lane takes
+// every 32nd part, then the lanes' pairs are joined.  stat(i): part i's pair.  A
+// pair without a reference is of no keys, or of NaN logits, whose NaN sums stay.
+__device__ __forceinline__ float2 join_pairs(float2 a, float2 b) {
+  const float M = fmaxf(a.x, b.x);
+  return make_float2(M, (a.x == -INFINITY ? a.y : ex2(a.x - M) * a.y) +
+                            (b.x == -INFINITY ? b.y : ex2(b.x - M) * b.y));
+}
+template <typename Stat>
+__device__ __forceinline__ float2 join_row(int parts, Stat &&stat) {
+  float2 s = make_float2(-INFINITY, 0.f);
+#pragma unroll 2
+  for (int i = threadIdx.x & 31; i < parts; i += 32) s = join_pairs(s, stat(i));
+#pragma unroll 1
+  for (int o = 16; o > 0; o >>= 1)
+    s = join_pairs(s, make_float2(__shfl_xor_sync(0xffffffffu, s.x, o),
+                                  __shfl_xor_sync(0xffffffffu, s.y, o)));
+  return s;
+}
+
 // The parts of a segment: the CTAs c0 .. c0 + n - 1 (n = 1: whole).
 struct Parts {
   int c0, n;
@@ -846,7 +876,6 @@ __device__ __forceinline__ void weights_kept(const Cache8AttendArgs &a, const Se
 template <int kRows, typename T>
 __global__ void __launch_bounds__(kSimtThreads, 5) attend_finish_kernel(const AttendArgs p) {
   __shared__ float s_o[kSimtWarps][kMaxD];
-  __shared__ float s_l[kSimtWarps];
   __shared__ float s_z[kMaxXRows];
   const Cache8AttendArgs &a = p.a;
   const int D = a.head_dim;
@@ -880,16 +909,10 @@ __global__ void __launch_bounds__(kSimtThreads, 5) attend_finish_kernel(const At
       if (x.n == 1) {
         z = p.lse2[static_cast<size_t>(head) * a.group * a.T + r];
       } else {
-        float M = -INFINITY, L = 0.f;
-        for (int i = lane; i < x.n; i += 32) M = fmaxf(M, part(x, i)[row]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        for (int i = lane; i < x.n; i += 32) {
-          const float mi = part(x, i)[row], li = part(x, i)[kRows + row];
-          L += mi == -INFINITY ? li : exp2f(mi - M) * li;
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+        const float2 ml = join_row(x.n, [&](int i) {
+          return *reinterpret_cast<const float2 *>(part(x, i) + 2 * row);
+        });
+        const float M = ml.x, L = ml.y;
         z = L > 0.f || L != L ? M + log2f(L) : -INFINITY;
       }
       if (lane == 0) s_z[r] = z == -INFINITY ? INFINITY : z;  // rows that see nothing add nothing
@@ -924,31 +947,27 @@ __global__ void __launch_bounds__(kSimtThreads, 5) attend_finish_kernel(const At
   const int deal = p.join_rows == 1 ? kSimtWarps : 1;  // warps per row
   for (int i0 = warp / deal; i0 < rows; i0 += kSimtWarps / deal) {
     const int row = first + i0;
-    float M = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int i = lane; i < x.n; i += 32) M = fmaxf(M, part(x, i)[row]);
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
+    const float2 ml = join_row(x.n, [&](int i) {
+      return *reinterpret_cast<const float2 *>(part(x, i) + 2 * row);
+    });
+    const float M = ml.x, l = ml.y;
+    float o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
     for (int i = warp % deal; i < x.n; i += deal) {
       const float *s = part(x, i);
-      const float mi = s[row], li = s[kRows + row];
+      const float mi = s[2 * row];
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (lane * 4 < D) v = *reinterpret_cast<const float4 *>(s + 2 * kRows + row * D + lane * 4);
-      // a part without keys for this row is zeros; NaN logits leave it without a
-      // reference and with NaN sums, which have to stay
-      const float f = mi == -INFINITY ? 1.f : exp2f(mi - M);
-      l = fmaf(f, li, l);
+      const float f = mi == -INFINITY ? 1.f : ex2(mi - M);  // no reference: zeros, or NaN
       o[0] = fmaf(f, v.x, o[0]), o[1] = fmaf(f, v.y, o[1]);
       o[2] = fmaf(f, v.z, o[2]), o[3] = fmaf(f, v.w, o[3]);
     }
     if (deal > 1) {
       if (lane * 4 < D)
         *reinterpret_cast<float4 *>(&s_o[warp][lane * 4]) = make_float4(o[0], o[1], o[2], o[3]);
-      if (lane == 0) s_l[warp] = l;
       __syncthreads();  // one row: every warp comes here once
       if (warp != 0) return;
       for (int i = 1; i < kSimtWarps; ++i) {
-        l += s_l[i];
         if (lane * 4 < D) {
           const float4 v = *reinterpret_cast<const float4 *>(&s_o[i][lane * 4]);
           o[0] += v.x, o[1] += v.y, o[2] += v.z, o[3] += v.w;

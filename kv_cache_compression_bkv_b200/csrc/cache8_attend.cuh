@@ -23,7 +23,9 @@ struct AttendArgs {
   int row_blocks, ctas, x_cols, log2_block, join_rows;
   int w_keys, w_chunks;  // keys per weights CTA, and its CTAs per (sequence, KV head)
   long long x_len;   // keys per (sequence, KV head) in x
-  float *part;       // [ctas][2][rows][2 + head_dim]: max, sum, output
+  // [ctas][2]: the two ends' segments of a CTA's run, each (reference, sum)
+  // [rows], then unnormalised outputs [rows][head_dim]
+  float *part;
   float *lse2;       // [n_seqs][n_kv_heads][group * T], log2 units
   float *x;          // [n_seqs][n_kv_heads][x_len][x_cols], log2 units
   // K and V as f16 tiles, [n_seqs][n_kv_heads][pre_len][head_dim], with a K

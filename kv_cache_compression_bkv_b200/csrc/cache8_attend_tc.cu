@@ -670,10 +670,7 @@ __global__ void __launch_bounds__((TcCfg<D, RT, kPre>::kThreads), 1)
       __syncwarp();
       tc_fence_before();
       if (row && whole) store_lse(p, x.seq, x.kvh, r, ref, l);
-      if (row && !whole) {
-        part[pr] = ref;
-        part[kRows + pr] = l;
-      }
+      if (row && !whole) *reinterpret_cast<float2 *>(part + 2 * pr) = make_float2(ref, l);
       __syncwarp();
     }
   }
