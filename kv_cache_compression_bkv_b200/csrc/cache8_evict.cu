@@ -104,16 +104,20 @@ __device__ __forceinline__ uint32_t find_bin(uint32_t *s_hist, uint32_t *s_warp,
   return s_bin[0];
 }
 
-// Calls f(v, candidate) for the ranked weight of every position, by whole
-// warps; four positions a lane and step, kBatch steps' loads in flight.
-template <typename F>
-__device__ __forceinline__ void for_weights(const float *w, int L, int lo, int hi, F &&f) {
-  constexpr int kBatch = 8;
+// Calls f(t, v) for the ranked weights of the row that are candidates, and
+// done(first position, bits) after every kBatch * 4 of a lane, with the bits t
+// for which f returned true: bit t is position first + 4 * kSelThreads * (t / 4)
+// + t % 4.  Loads of a batch are in flight together; range checks only in the
+// chunks of 128 positions where the candidates begin or end.
+constexpr int kBatch = 4;
+template <typename F, typename Done>
+__device__ __forceinline__ void for_weights(const float *w, int L, int lo, int hi, F &&f, Done &&done) {
   const unsigned quads = (static_cast<unsigned>(L) + 3) >> 2;  // a row is allocated to whole quads
   const unsigned first = threadIdx.x & ~31u, lane = threadIdx.x & 31u;
   const unsigned l = static_cast<unsigned>(lo), h = static_cast<unsigned>(hi);
   for (unsigned q0 = first; q0 < quads; q0 += kBatch * kSelThreads) {
     float4 v[kBatch];
+    uint32_t bits = 0;
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       const unsigned q = q0 + u * kSelThreads + lane;
@@ -123,23 +127,19 @@ __device__ __forceinline__ void for_weights(const float *w, int L, int lo, int h
     for (int u = 0; u < kBatch; ++u) {
       const unsigned j0 = 4 * (q0 + u * kSelThreads);  // this warp's 128 positions
       if (j0 >= h || j0 + 128 <= l) continue;
-      if (j0 >= l && j0 + 128 <= h) {
-        f(ranked(v[u].x), true);
-        f(ranked(v[u].y), true);
-        f(ranked(v[u].z), true);
-        f(ranked(v[u].w), true);
-      } else {
-        const unsigned j = j0 + 4 * lane;
-        f(ranked(v[u].x), j >= l && j < h);
-        f(ranked(v[u].y), j + 1 >= l && j + 1 < h);
-        f(ranked(v[u].z), j + 2 >= l && j + 2 < h);
-        f(ranked(v[u].w), j + 3 >= l && j + 3 < h);
+      const float y[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+      const bool inner = j0 >= l && j0 + 128 <= h;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const unsigned j = j0 + 4 * lane + i;
+        if ((inner || (j >= l && j < h)) && f(ranked(y[i]))) bits |= 1u << (4 * u + i);
       }
     }
+    done(4 * (q0 + lane), bits);
   }
 }
 
-__global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Cache8EvictArgs a) {
+__global__ void __launch_bounds__(kSelThreads, 3) evict_select_kernel(const Cache8EvictArgs a) {
   __shared__ __align__(16) uint32_t s_hist[kBins];
   __shared__ uint32_t s_list[kListMax];
   __shared__ uint32_t s_warp[kSelWarps];
@@ -171,20 +171,29 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Cach
     for (int b = tid; b < kBins; b += kSelThreads) s_hist[b] = 0;
     if (tid == 0) s_count = 0;
     __syncthreads();
-    for_weights(w, L, lo, hi, [&](float v, bool cand) {
-      if (cand) atomicAdd(&s_hist[bin_of(v)], 1u);
-    });
+    for_weights(
+        w, L, lo, hi,
+        [&](float v) {
+          atomicAdd(&s_hist[bin_of(v)], 1u);
+          return false;
+        },
+        [](unsigned, uint32_t) {});
     __syncthreads();
     const uint32_t raw = find_bin<true>(s_hist, s_warp, s_bin, &need);
-    // the bin's keys, listed, and their next 11 bits counted
-    for_weights(w, L, lo, hi, [&](float v, bool cand) {
-      if (cand && bin_of(v) == raw) {
-        const uint32_t k = order_key(v);
-        atomicAdd(&s_hist[(k >> 10) & 2047u], 1u);
-        const uint32_t at = atomicAdd(&s_count, 1u);
-        if (at < kListMax) s_list[at] = k;
-      }
-    });
+    // the bin's keys, listed, and their next 11 bits counted: found first, then
+    // read again one by one, a few of a lane's 16
+    for_weights(
+        w, L, lo, hi, [&](float v) { return bin_of(v) == raw; },
+        [&](unsigned j, uint32_t bits) {
+          while (bits) {
+            const int t = __ffs(bits) - 1;
+            bits &= bits - 1;
+            const uint32_t k = order_key(ranked(__ldg(w + j + 4 * kSelThreads * (t >> 2) + (t & 3))));
+            atomicAdd(&s_hist[(k >> 10) & 2047u], 1u);
+            const uint32_t at = atomicAdd(&s_count, 1u);
+            if (at < kListMax) s_list[at] = k;
+          }
+        });
     __syncthreads();
     const uint32_t top = raw < 1024 ? 1024 + raw : 2047 - raw;  // the bin's keys' top bits
     const uint32_t mid = (top << 11) | find_bin<false>(s_hist, s_warp, s_bin, &need);
@@ -193,10 +202,14 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Cach
       for (uint32_t i = tid; i < n; i += kSelThreads)
         if ((s_list[i] >> 10) == mid) atomicAdd(&s_hist[s_list[i] & 1023u], 1u);
     } else {  // a crowded bin: the row again
-      for_weights(w, L, lo, hi, [&](float v, bool cand) {
-        const uint32_t k = order_key(v);
-        if (cand && (k >> 10) == mid) atomicAdd(&s_hist[k & 1023u], 1u);
-      });
+      for_weights(
+          w, L, lo, hi,
+          [&](float v) {
+            const uint32_t k = order_key(v);
+            if ((k >> 10) == mid) atomicAdd(&s_hist[k & 1023u], 1u);
+            return false;
+          },
+          [](unsigned, uint32_t) {});
     }
     __syncthreads();
     thr = key_value((mid << 10) | find_bin<false>(s_hist, s_warp, s_bin, &need));
@@ -212,24 +225,30 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Cach
     uint32_t keep = 0, tie = 0;
     const bool inner = ties > 0 && jw >= l && jw + 1024 <= h;
     if (inner || jw < static_cast<unsigned>(L)) {
-      float4 v[8];
+#pragma unroll 1
+      for (int t0 = 0; t0 < 8; t0 += 4) {  // four loads in flight, within 40 registers
+        float4 v[4];
 #pragma unroll
-      for (int t = 0; t < 8; ++t)  // a row is allocated to whole quads
-        if (inner || j0 + 128 * t < static_cast<unsigned>(L))
-          v[t] = __ldg(reinterpret_cast<const float4 *>(w + j0 + 128 * t));
+        for (int t = 0; t < 4; ++t)  // a row is allocated to whole quads
+          if (inner || j0 + 128 * (t0 + t) < static_cast<unsigned>(L))
+            v[t] = __ldg(reinterpret_cast<const float4 *>(w + j0 + 128 * (t0 + t)));
+        uint32_t k = 0, e = 0;
 #pragma unroll
-      for (int t = 0; t < 8; ++t) {
-        const float y[4] = {v[t].x, v[t].y, v[t].z, v[t].w};
+        for (int t = 0; t < 4; ++t) {
+          const float y[4] = {v[t].x, v[t].y, v[t].z, v[t].w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float x = fmaxf(y[i], -INFINITY);
-          if (x > thr) keep |= 1u << (4 * t + i);
-          if (x == thr) tie |= 1u << (4 * t + i);
+          for (int i = 0; i < 4; ++i) {
+            const float x = fmaxf(y[i], -INFINITY);
+            if (x > thr) k |= 1u << (4 * t + i);
+            if (x == thr) e |= 1u << (4 * t + i);
+          }
         }
+        keep |= k << (4 * t0);
+        tie |= e << (4 * t0);
       }
       if (!inner) {  // the sink and the recent rows, and what lies past the end
         uint32_t cand = 0, there = 0;
-#pragma unroll
+#pragma unroll 1
         for (int t = 0; t < 32; ++t) {
           const unsigned j = j0 + 128 * (t >> 2) + (t & 3);
           if (j < static_cast<unsigned>(L)) there |= 1u << t;
