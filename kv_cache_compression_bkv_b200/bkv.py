@@ -70,6 +70,7 @@ class StepArgs(ctypes.Structure):
                 ("ring_pos", ctypes.c_int64), ("aux_stream", ctypes.c_void_p)]
 
 STEP_EVENTS = 6
+_RAW_STREAM = torch._C._cuda_getCurrentRawStream
 
 
 def _load() -> ctypes.CDLL:
@@ -111,6 +112,7 @@ def _load() -> ctypes.CDLL:
 
 
 LIB = _load()
+_APPEND8, _ATTEND8, _EVICT8 = LIB.bkv_cache8_append, LIB.bkv_cache8_attend, LIB.bkv_cache8_evict
 
 
 def _status_text(status: int) -> str:
@@ -129,7 +131,7 @@ def _ptr(t: torch.Tensor | None):
 def _stream(stream) -> int:
     if stream is None:
         # the current stream's handle; a Stream object would cost 3 us to make
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return _RAW_STREAM(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -315,12 +317,25 @@ def bkv_cache8_workspace_size(geom: Geometry8, max_len: int, T: int, K: int,
     return int(LIB.bkv_cache8_workspace_size(geom._ref, max_len, T, K, int(weights)))
 
 
+# These calls are a decode step's, and their time on the host counts: pointers go
+# in as integers, and the stream's handle is taken without a Stream object.
+
+def _opt(t: torch.Tensor | None):
+    return t if t is None else t.data_ptr()
+
+
+def _nbytes(t: torch.Tensor | None) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
 def bkv_cache8_append(geom: Geometry8, k8, v8, k_scale, v_scale, lens, k_new, v_new, T: int,
                       n_new=None, stream=None) -> None:
     """Quantise the newest rows of every sequence into the cache (lens counts them)."""
-    _check(LIB.bkv_cache8_append(geom._ref, _ptr(k8), _ptr(v8), _ptr(k_scale), _ptr(v_scale),
-                                 _ptr(lens), _ptr(k_new), _ptr(v_new), T, _ptr(n_new),
-                                 _stream(stream)), "bkv_cache8_append")
+    st = _APPEND8(geom._ref, k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                  lens.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), T, _opt(n_new),
+                  _stream(stream))
+    if st:
+        raise BkvError(st, "bkv_cache8_append")
 
 
 def bkv_cache8_attend(geom: Geometry8, k8, v8, k_scale, v_scale, lens, max_len: int, q, T: int,
@@ -328,12 +343,12 @@ def bkv_cache8_attend(geom: Geometry8, k8, v8, k_scale, v_scale, lens, max_len: 
                       workspace, stream=None) -> None:
     """Attention of the newest tokens over the cache, with the rows' attention
     weights where weights_out is given; lse, weights_in and weights_out may be None."""
-    _check(LIB.bkv_cache8_attend(geom._ref, _ptr(k8), _ptr(v8), _ptr(k_scale), _ptr(v_scale),
-                                 _ptr(lens), max_len, _ptr(q), T, _ptr(n_new), scale, _ptr(out),
-                                 _ptr(lse), _ptr(weights_in), _ptr(weights_out), decay,
-                                 _ptr(workspace),
-                                 0 if workspace is None else workspace.numel() * workspace.element_size(),
-                                 _stream(stream)), "bkv_cache8_attend")
+    st = _ATTEND8(geom._ref, k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                  lens.data_ptr(), max_len, q.data_ptr(), T, _opt(n_new), scale, out.data_ptr(),
+                  _opt(lse), _opt(weights_in), _opt(weights_out), decay, _opt(workspace),
+                  _nbytes(workspace), _stream(stream))
+    if st:
+        raise BkvError(st, "bkv_cache8_attend")
 
 
 def bkv_cache8_evict(geom: Geometry8, k8, v8, k_scale, v_scale, weights, lens, max_len: int,
@@ -342,12 +357,13 @@ def bkv_cache8_evict(geom: Geometry8, k8, v8, k_scale, v_scale, weights, lens, m
                      stream=None) -> None:
     """Keep the first sink, the last recent and the heaviest other rows, K in all,
     in dst (in place when dst's buffers are the source's)."""
-    _check(LIB.bkv_cache8_evict(geom._ref, _ptr(k8), _ptr(v8), _ptr(k_scale), _ptr(v_scale),
-                                _ptr(weights), _ptr(lens), max_len, K, sink, recent, dst._ref,
-                                _ptr(k8_dst), _ptr(v8_dst), _ptr(k_scale_dst), _ptr(v_scale_dst),
-                                _ptr(weights_dst), _ptr(idx), _ptr(new_lens), _ptr(workspace),
-                                0 if workspace is None else workspace.numel() * workspace.element_size(),
-                                _stream(stream)), "bkv_cache8_evict")
+    st = _EVICT8(geom._ref, k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                 weights.data_ptr(), lens.data_ptr(), max_len, K, sink, recent, dst._ref,
+                 k8_dst.data_ptr(), v8_dst.data_ptr(), k_scale_dst.data_ptr(),
+                 v_scale_dst.data_ptr(), _opt(weights_dst), _opt(idx), _opt(new_lens),
+                 _opt(workspace), _nbytes(workspace), _stream(stream))
+    if st:
+        raise BkvError(st, "bkv_cache8_evict")
 
 
 def bkv_selftest_wait_timeout(limit_ns: int, outcome, stream=None) -> None:

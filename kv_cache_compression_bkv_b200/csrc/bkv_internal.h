@@ -144,9 +144,10 @@ struct Cache8AppendArgs {
   const int32_t *lens, *n_new; // lengths with the new rows; NULL n_new: T for all
   int n_seqs, n_kv_heads, head_dim, block, T;
   int blocks_per_seq;          // blocks that T rows can touch
+  int runs_per_seq;            // CTAs for them; filled by the launcher
   long long cap;
 };
-bkv_status launch_cache8_append(const Cache8AppendArgs &a, int dtype, cudaStream_t stream);
+bkv_status launch_cache8_append(Cache8AppendArgs a, int dtype, cudaStream_t stream);
 
 struct Cache8AttendArgs {
   const uint8_t *k8, *v8;

@@ -1095,6 +1095,9 @@ Cache8AttendPlan plan_cache8_attend(int n_seqs, int n_q_heads, int n_kv_heads, i
   const long long rows = static_cast<long long>(n_q_heads / n_kv_heads) * T;
   const bool mma = use_mma(dtype, head_dim);
   p.nt = !mma || rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 24 ? 3 : 4;
+  // Measured on both sides: 8 sequences to 8192 rows of 32/8 heads, 40 query rows
+  // a KV head 70 us on tcgen05 and 107 us on mma.sync, 128 rows 87 and 184; 24
+  // rows with weights (a key's logits are then kept) 109 and 48.
   p.row_tiles = mma && rows > 32 ? (rows <= 128 ? 1 : 2) : 0;
   p.block_rows = p.row_tiles ? 128 * p.row_tiles : 8 * p.nt;
   p.row_blocks = static_cast<int>((rows + p.block_rows - 1) / p.block_rows);
