@@ -85,13 +85,6 @@ struct Piece<__nv_bfloat16> {
   }
 };
 
-// A value that is not finite becomes a NaN code.
-__device__ __forceinline__ float storable(float x, float inv, bool odd) {
-  const float y = x * inv;
-  if (odd && (__float_as_uint(x) & 0x7fffffffu) >= 0x7f800000u) return __uint_as_float(0x7fc00000u);
-  return y;
-}
-
 // kPieces: 16-element pieces per thread, as few as the sizes allow, so that
 // more CTAs are resident and more loads in flight.  kRun: blocks a CTA takes
 // one after another, the next one's rows loading while one is written; the
@@ -172,9 +165,14 @@ __global__ void __launch_bounds__(kMaxThreads) append_kernel(const Cache8AppendA
         uint32_t w[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          w[k] = to_e4m3x2(storable(now[i].at(4 * k), inv, odd), storable(now[i].at(4 * k + 1), inv, odd)) |
-                 (to_e4m3x2(storable(now[i].at(4 * k + 2), inv, odd),
-                            storable(now[i].at(4 * k + 3), inv, odd)) << 16);
+          w[k] = to_e4m3x2(now[i].at(4 * k) * inv, now[i].at(4 * k + 1) * inv) |
+                 (to_e4m3x2(now[i].at(4 * k + 2) * inv, now[i].at(4 * k + 3) * inv) << 16);
+        if (odd) {  // elements that are not finite become NaN codes
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            if ((__float_as_uint(now[i].at(k)) & 0x7fffffffu) >= 0x7f800000u)
+              w[k >> 2] |= 0x7fu << (8 * (k & 3));
+        }
         reinterpret_cast<uint4 *>(codes)[static_cast<size_t>(r0 - base) * pr + p] =
             make_uint4(w[0], w[1], w[2], w[3]);
       }
