@@ -29,8 +29,7 @@ STATUS = {0: "BKV_OK", 1: "BKV_ERR_INVALID_ARG", 2: "BKV_ERR_UNSUPPORTED",
 EXPORTS = ("bkv_workspace_size", "bkv_score", "bkv_select_topk", "bkv_compact",
            "bkv_update_beacons", "bkv_compress_step", "bkv_read_device_status",
            "bkv_status_string", "bkv_score_noalloc", "bkv_score_mean", "bkv_compact_inplace",
-           "bkv_selftest_wait_timeout", "bkv_cache8_workspace_size", "bkv_cache8_append",
-           "bkv_cache8_attend", "bkv_cache8_evict")
+           "bkv_selftest_wait_timeout")
 SCORE_NOALLOC_SCRATCH_BYTES = 32 << 20
 
 
@@ -320,10 +319,6 @@ def bkv_cache8_workspace_size(geom: Geometry8, max_len: int, T: int, K: int,
 # These calls are a decode step's, and their time on the host counts: pointers go
 # in as integers, and the stream's handle is taken without a Stream object.
 
-def _opt(t: torch.Tensor | None):
-    return t if t is None else t.data_ptr()
-
-
 def _nbytes(t: torch.Tensor | None) -> int:
     return 0 if t is None else t.numel() * t.element_size()
 
@@ -332,7 +327,7 @@ def bkv_cache8_append(geom: Geometry8, k8, v8, k_scale, v_scale, lens, k_new, v_
                       n_new=None, stream=None) -> None:
     """Quantise the newest rows of every sequence into the cache (lens counts them)."""
     st = _APPEND8(geom._ref, k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                  lens.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), T, _opt(n_new),
+                  lens.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), T, _ptr(n_new),
                   _stream(stream))
     if st:
         raise BkvError(st, "bkv_cache8_append")
@@ -344,8 +339,8 @@ def bkv_cache8_attend(geom: Geometry8, k8, v8, k_scale, v_scale, lens, max_len: 
     """Attention of the newest tokens over the cache, with the rows' attention
     weights where weights_out is given; lse, weights_in and weights_out may be None."""
     st = _ATTEND8(geom._ref, k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                  lens.data_ptr(), max_len, q.data_ptr(), T, _opt(n_new), scale, out.data_ptr(),
-                  _opt(lse), _opt(weights_in), _opt(weights_out), decay, _opt(workspace),
+                  lens.data_ptr(), max_len, q.data_ptr(), T, _ptr(n_new), scale, out.data_ptr(),
+                  _ptr(lse), _ptr(weights_in), _ptr(weights_out), decay, _ptr(workspace),
                   _nbytes(workspace), _stream(stream))
     if st:
         raise BkvError(st, "bkv_cache8_attend")
@@ -360,8 +355,8 @@ def bkv_cache8_evict(geom: Geometry8, k8, v8, k_scale, v_scale, weights, lens, m
     st = _EVICT8(geom._ref, k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                  weights.data_ptr(), lens.data_ptr(), max_len, K, sink, recent, dst._ref,
                  k8_dst.data_ptr(), v8_dst.data_ptr(), k_scale_dst.data_ptr(),
-                 v_scale_dst.data_ptr(), _opt(weights_dst), _opt(idx), _opt(new_lens),
-                 _opt(workspace), _nbytes(workspace), _stream(stream))
+                 v_scale_dst.data_ptr(), _ptr(weights_dst), _ptr(idx), _ptr(new_lens),
+                 _ptr(workspace), _nbytes(workspace), _stream(stream))
     if st:
         raise BkvError(st, "bkv_cache8_evict")
 
@@ -369,8 +364,7 @@ def bkv_cache8_evict(geom: Geometry8, k8, v8, k_scale, v_scale, weights, lens, m
 def bkv_selftest_wait_timeout(limit_ns: int, outcome, stream=None) -> None:
     """Make one bounded device-side wait give up on purpose (diagnostic)."""
     _check(LIB.bkv_selftest_wait_timeout(limit_ns, _ptr(outcome), _stream(stream)),
-           "bkv_selftest_wait_timeout", "bkv_cache8_workspace_size", "bkv_cache8_append",
-           "bkv_cache8_attend", "bkv_cache8_evict")
+           "bkv_selftest_wait_timeout")
 
 
 def bkv_read_device_status(stream=None) -> tuple[int, int]:
