@@ -29,7 +29,8 @@ STATUS = {0: "BKV_OK", 1: "BKV_ERR_INVALID_ARG", 2: "BKV_ERR_UNSUPPORTED",
 EXPORTS = ("bkv_workspace_size", "bkv_score", "bkv_select_topk", "bkv_compact",
            "bkv_update_beacons", "bkv_compress_step", "bkv_read_device_status",
            "bkv_status_string", "bkv_score_noalloc", "bkv_score_mean", "bkv_compact_inplace",
-           "bkv_selftest_wait_timeout")
+           "bkv_selftest_wait_timeout", "bkv_cache8_workspace_size", "bkv_cache8_append",
+           "bkv_cache8_attend", "bkv_cache8_evict")
 SCORE_NOALLOC_SCRATCH_BYTES = 32 << 20
 
 

@@ -18,7 +18,6 @@ namespace bkv {
 namespace cache8 {
 
 constexpr int kMinExp = -117;    // 448 * 2^-117 and 2^-9 * 2^-117 are normal floats
-constexpr uint32_t kNaN4 = 0x7f7f7f7fu;
 
 // The exponent of the scale of a block whose largest magnitude is `amax`
 // (finite, >= 0): 448 = 1.75 * 2^8, so with amax = m 2^k the exponent is k - 8
@@ -79,6 +78,34 @@ __device__ __forceinline__ uint4 rescale16(uint4 c, int k) {
   // below 2^-24 every code becomes zero
   const __half2 f = __float2half2_rn(pow2f(max(k, -24)));
   return make_uint4(rescale4(c.x, f), rescale4(c.y, f), rescale4(c.z, f), rescale4(c.w, f));
+}
+
+// Bit 7 of each byte that is a NaN code.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t codes) {
+  return ((codes & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+}
+__device__ __forceinline__ bool has_nan16(uint4 c) {
+  return (nan_bytes(c.x) | nan_bytes(c.y) | nan_bytes(c.z) | nan_bytes(c.w)) != 0;
+}
+// NaN codes of a key that not every query row sees become zeros: a product with a
+// probability of zero would carry them to every row.
+__device__ __forceinline__ uint32_t without_nan4(uint32_t codes) {
+  return codes & ~((nan_bytes(codes) >> 7) * 0xffu);
+}
+__device__ __forceinline__ uint4 without_nan16(uint4 c) {
+  return make_uint4(without_nan4(c.x), without_nan4(c.y), without_nan4(c.z), without_nan4(c.w));
+}
+// The same, with put(i) called for each such element i of the 16.
+template <typename Put>
+__device__ __forceinline__ void hide_nan16(uint4 *codes, Put &&put) {
+  if (!has_nan16(*codes)) return;
+  uint8_t *byte = reinterpret_cast<uint8_t *>(codes);
+#pragma unroll 1
+  for (int i = 0; i < 16; ++i)
+    if ((byte[i] & 0x7f) == 0x7f) {
+      byte[i] = 0;
+      put(i);
+    }
 }
 
 __device__ __forceinline__ __half2 absmax4(uint32_t codes, __half2 m) {

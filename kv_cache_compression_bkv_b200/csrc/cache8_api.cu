@@ -10,7 +10,8 @@
 namespace bkv {
 namespace {
 
-constexpr long long kMaxRows = (1LL << 31) - 1;
+// cached rows, below 2^31 by more than any kernel steps past a length
+constexpr long long kMaxRows = (1LL << 31) - 65536;
 constexpr long long kMaxHeads = 65535;  // (sequence, KV head) pairs: a grid dimension
 
 bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }

@@ -56,15 +56,19 @@ constexpr int kSimtKeys = 16;
 
 // The end of a CTA's part of a segment: kBufs buffers of unnormalised outputs
 // (summed here; element (r, d) of a buffer at off(r, d)) and the row statistics
-// m, l.  A whole segment goes out, a part to the CTA's slot.
+// m, l.  A whole segment goes out, a part to the CTA's slot.  first[d]: the
+// lowest key whose NaN in V was left out (hide_nan16), for the rows that see it,
+// where first[D] says that there are any; so does the result.
 template <int kRows, int kBufs, int kCta, typename T, typename Off>
-__device__ __forceinline__ void write_segment(const AttendArgs &p, const float *buf, int buf_stride,
-                                              const float *m, const float *l, int seq, int unit,
-                                              int n, bool whole, int slot, Off &&off) {
+__device__ __forceinline__ bool write_segment(const AttendArgs &p, const float *buf, int buf_stride,
+                                              const float *m, const float *l, const int *first,
+                                              int seq, int unit, const SeqInfo &q, bool whole,
+                                              int slot, Off &&off) {
   const Cache8AttendArgs &a = p.a;
   const int D = a.head_dim;
   const int kvh = unit / p.row_blocks, r0 = (unit - kvh * p.row_blocks) * kRows;
-  const int rows = a.group * n;
+  const int rows = a.group * q.n;
+  const bool nans = first[D] != 0;
   float *part = p.part + (static_cast<size_t>(blockIdx.x) * 2 + slot) * (kRows * (2 + D));
   for (int e = threadIdx.x; e < kRows * D; e += kCta) {
     const int r = e / D, d = e - r * D;
@@ -79,6 +83,19 @@ __device__ __forceinline__ void write_segment(const AttendArgs &p, const float *
                 l[r] > 0.f || l[r] != l[r] ? v / l[r] : 0.f);
     }
   }
+  if (nans) {  // the same elements again
+#pragma unroll 1
+    for (int e = threadIdx.x; e < kRows * D; e += kCta) {
+      const int r = e / D, d = e - r * D;
+      if (first[d] >= q.len - q.n + 1 + (r0 + r) / a.group) continue;
+      const float v = __uint_as_float(0x7fc00000u);
+      if (!whole) {
+        part[2 * kRows + e] = v;
+      } else if (r0 + r < rows) {
+        store_out(static_cast<T *>(a.out) + q_row(a, seq, kvh, r0 + r) * D + d, v);
+      }
+    }
+  }
   if (threadIdx.x < kRows) {
     const int r = threadIdx.x;
     if (!whole) {
@@ -87,6 +104,7 @@ __device__ __forceinline__ void write_segment(const AttendArgs &p, const float *
       store_lse(p, seq, kvh, r0 + r, m[r], l[r]);
     }
   }
+  return nans;
 }
 
 // --------------------------------------------------- tensor-core kernel (bf16)
@@ -200,7 +218,7 @@ struct MmaCfg {
   static constexpr int kRing = kWarps * kStages * kStageBytes;
   static constexpr int kBuf = kRows * D;                  // floats per merge buffer
   static constexpr int kQ = NT == 1 ? 0 : NT * (D / 16) * 32 * 8;
-  static constexpr int kStat = (2 * kWarps * kRows + 3 * kRows) * 4;
+  static constexpr int kStat = (2 * kWarps * kRows + 3 * kRows + D + 1) * 4;
   static constexpr int kSmem = kRing + 2 * kBuf * 4 + kQ + kStat;
 };
 
@@ -216,6 +234,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_mma_kernel(const AttendArg
   float *s_m = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(s_q) + Cfg::kQ);
   float *s_l = s_m + kWarps * Cfg::kRows;
   float *s_M = s_l + kWarps * Cfg::kRows, *s_L = s_M + Cfg::kRows, *s_rs = s_L + Cfg::kRows;
+  int *s_first = reinterpret_cast<int *>(s_rs + Cfg::kRows);  // see write_segment
 
   const Cache8AttendArgs &a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -286,6 +305,12 @@ __global__ void __launch_bounds__(kThreads, 2) attend_mma_kernel(const AttendArg
     if (load.at < run) issue(s);
     cp_async_commit();
   }
+  auto reset_first = [&]() {
+    if (threadIdx.x < D) s_first[threadIdx.x] = INT32_MAX;
+    if (threadIdx.x == 0) s_first[D] = 0;
+    __syncthreads();
+  };
+  reset_first();
 
   // ---- what a lane reads
   const int key0 = ((g >> 1) << 2) | (g & 1);  // and key0 + 2: rows g and g + 8 of an m-tile
@@ -461,6 +486,18 @@ __global__ void __launch_bounds__(kThreads, 2) attend_mma_kernel(const AttendArg
           b[nt][t][1] = transpose8x8(as_u32(__floats2half2_rn(p2 * vr, p3 * vr)));
         }
       }
+      const int hidden = hidden_from(cur.q);
+      if (j0 + kKeys > hidden) {  // keys that not every token sees: this lane's pieces
+#pragma unroll 1
+        for (int i = max(hidden - j0 - lrow + 32 / CH - 1, 0) / (32 / CH); i < PIECES; ++i) {
+          const uint32_t at = (D == 128 ? v_dst0 ^ ((i & 1) << 6) : v_dst0) + i * 512;
+          hide_nan16(reinterpret_cast<uint4 *>(smem + (st - smem) + at), [&](int e) {
+            s_first[D] = 1;
+            atomicMin(&s_first[lch * 16 + e], j0 + lrow + i * (32 / CH));
+          });
+        }
+        __syncwarp();
+      }
       // ---- outputs: V^T (A) by ldmatrix, 16 elements x 32 keys an m-tile
       const uint32_t vbase = ring + stage * Cfg::kStageBytes + kKeys * D + lane * D;
       const uint32_t vsw = D == 128 ? (lane & 7) << 4 : ((lane >> 1) & 3) << 4;
@@ -546,13 +583,14 @@ __global__ void __launch_bounds__(kThreads, 2) attend_mma_kernel(const AttendArg
             for (int i = 0; i < 4; ++i) bf[at(mt, nt, i)] += o[mt][nt][i] * f[nt][i & 1];
       }
       __syncthreads();
-      write_segment<Cfg::kRows, 2, kThreads, __nv_bfloat16>(
-          p, s_buf, Cfg::kBuf, s_M, s_L, cur.seq, cur.unit, cur.q.n, from_start && to_end,
+      const bool nans = write_segment<Cfg::kRows, 2, kThreads, __nv_bfloat16>(
+          p, s_buf, Cfg::kBuf, s_M, s_L, s_first, cur.seq, cur.unit, cur.q, from_start && to_end,
           from_start ? 1 : 0, [](int r, int d) {
             return (((d >> 4) * NT + (r >> 3)) * 4 + ((d >> 3) & 1) * 2 + (r & 1)) * 32 +
                    (d & 7) * 4 + ((r & 7) >> 1);
           });
       __syncthreads();
+      if (nans) reset_first();
       fresh = true;
     }
     cur.next(a, w, units);
@@ -615,6 +653,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) attend_simt_kernel(const Atte
   __shared__ __align__(16) float s_p[kSimtWarps][kSimtKeys][kSimtRows];
   __shared__ float s_m[kSimtWarps][kSimtRows], s_l[kSimtWarps][kSimtRows];
   __shared__ float s_M[kSimtRows], s_L[kSimtRows];
+  __shared__ int s_first[kMaxD + 1];  // see write_segment
   const Cache8AttendArgs &a = p.a;
   const int D = a.head_dim;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -660,6 +699,12 @@ __global__ void __launch_bounds__(kSimtThreads, 2) attend_simt_kernel(const Atte
     cp_async_commit();
   };
   issue();
+  auto reset_first = [&]() {
+    if (threadIdx.x < D) s_first[threadIdx.x] = INT32_MAX;
+    if (threadIdx.x == 0) s_first[D] = 0;
+    __syncthreads();
+  };
+  reset_first();
   float o[kSimtRows][4], m[kSimtRows], l[kSimtRows];
   bool fresh = true;
   int seg_tiles = 0, stage = 0;
@@ -716,6 +761,21 @@ __global__ void __launch_bounds__(kSimtThreads, 2) attend_simt_kernel(const Atte
           l[r] += e;
         }
       }
+      const int hidden = hidden_from(cur.q);
+      if (j0 + kSimtKeys > hidden) {  // keys that not every token sees
+        const int ch = D >> 4;
+#pragma unroll 1
+        for (int q = lane; q < kSimtKeys * ch; q += 32) {
+          const int key = q / ch, e0 = (q - key * ch) * 16;
+          if (j0 + key < hidden) continue;
+          hide_nan16(reinterpret_cast<uint4 *>(ring + stage * simt_stage_bytes(D) +
+                                               (kSimtKeys + key) * (D + 16) + e0),
+                     [&](int e) {
+                       s_first[D] = 1;
+                       atomicMin(&s_first[e0 + e], j0 + key);
+                     });
+        }
+      }
       __syncwarp();
       const uint8_t *vrow = st + kSimtKeys * (D + 16) + (lane * 4 < D ? lane * 4 : 0);
 #pragma unroll 2
@@ -770,10 +830,11 @@ __global__ void __launch_bounds__(kSimtThreads, 2) attend_simt_kernel(const Atte
       const bool from_start = seg_tiles == cur.tile + 1;
       const bool to_end = cur.tile + 1 == cur.q.tiles;
       seg_tiles = 0;
-      write_segment<kSimtRows, kSimtWarps, kSimtThreads, T>(
-          p, s_buf, kSimtRows * D, s_M, s_L, cur.seq, cur.unit, cur.q.n, from_start && to_end,
+      const bool nans = write_segment<kSimtRows, kSimtWarps, kSimtThreads, T>(
+          p, s_buf, kSimtRows * D, s_M, s_L, s_first, cur.seq, cur.unit, cur.q, from_start && to_end,
           from_start ? 1 : 0, [D](int r, int d) { return r * D + d; });
       __syncthreads();
+      if (nans) reset_first();
       fresh = true;
     }
     cur.next(a, w, units);
@@ -884,6 +945,7 @@ __global__ void __launch_bounds__(kSimtThreads, 5) attend_finish_kernel(const At
   const int per_unit = kRows / p.join_rows;
   const int joins = a.n_seqs * units * per_unit;
   const int stride = kRows * (2 + D);
+  pdl_launch_dependents();
   int mine;
   // a part's statistics and output: slot 1 of the CTA the segment starts in,
   // slot 0 after it
@@ -1155,7 +1217,8 @@ bkv_status launch_cache8_attend(const Cache8AttendArgs &a, const Cache8AttendPla
     if (plan.row_tiles)
       ok = launch_attend_tc(p, plan.row_tiles, stream) &&
            (plan.row_tiles == 1 ? run_finish<128, __nv_bfloat16>(p, stream)
-                                : run_finish<256, __nv_bfloat16>(p, stream));
+                                : run_finish<256, __nv_bfloat16>(p, stream)) &&
+           (a.T == 1 || launch_mark_nan(p, stream));
     else if (plan.nt == 1)
       ok = (wide ? run_mma<128, 1>(p, stream) : run_mma<64, 1>(p, stream)) &&
            run_finish<8, __nv_bfloat16>(p, stream);

@@ -168,6 +168,11 @@ struct Cursor {
   }
 };
 
+// The first key that not every one of the call's tokens sees.
+__device__ __forceinline__ int hidden_from(const SeqInfo &q) {
+  return q.n > 1 ? q.len - q.n + 1 : INT32_MAX;
+}
+
 // Where row r of a (sequence, KV head) lives in q and out, in rows.
 __device__ __forceinline__ size_t q_row(const Cache8AttendArgs &a, int seq, int kvh, int r) {
   const int t = r / a.group, g = r - t * a.group;
@@ -200,6 +205,8 @@ __device__ __forceinline__ void store_lse(const AttendArgs &p, int seq, int kvh,
 // cache8_attend_tc.cu: bf16, head_dim 64 or 128, p.row_tiles tiles of 128 query
 // rows a CTA.
 bool launch_attend_tc(const cache8::AttendArgs &p, int row_tiles, cudaStream_t stream);
+// After the join: the outputs that a NaN in V reaches, for T > 1.
+bool launch_mark_nan(const cache8::AttendArgs &p, cudaStream_t stream);
 // cache8_weights_tc.cu: the weights from lse2 and the keys, after the above.
 bool launch_weights_tc(const cache8::AttendArgs &p, cudaStream_t stream);
 

@@ -408,6 +408,12 @@ __global__ void __launch_bounds__((TcCfg<D, RT, kPre>::kThreads), 1)
         // lanes 0..7: the factor of keys 16 lane ..
         const uint32_t factor = as_u32(__float2half2_rn(pow2f(max(ex[b] - top, -24))));
         uint8_t *tile = (is_v ? s_v : s_k) + stage * Cfg::kTileBytes;
+        const int hidden = x.len - x.n + 1 - (x.tile0 + cj) * kTile;  // row of the tile
+        if (is_v && x.n > 1 && hidden < kTile) {
+#pragma unroll
+          for (int i = 0; i < NP; ++i)
+            if (row0 + i * kStep >= hidden) c[b][i] = without_nan16(c[b][i]);
+        }
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
           const __half2 f =
@@ -457,15 +463,16 @@ __global__ void __launch_bounds__((TcCfg<D, RT, kPre>::kThreads), 1)
       float ref = -INFINITY, l = 0.f, vscale = 0.f;
       if (x.live > 0) {
         // queries: f16 under a power of two per 32 rows, largest in [2^14, 2^15)
+        // (read twice: once in registers costs spills in the loop below, 112 -> 119 us
+        // for 8 sequences to 8192 rows of 32/8 heads, 64 tokens)
         {
-          uint4 v[D / 8];
           uint32_t amax = 0;
           const uint4 *src = reinterpret_cast<const uint4 *>(
               static_cast<const __nv_bfloat16 *>(a.q) + (row ? q_row(a, x.seq, x.kvh, r) * D : 0));
-#pragma unroll
+#pragma unroll 8
           for (int i = 0; i < D / 8; ++i) {
-            v[i] = row ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-            const uint32_t y[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            const uint4 v = row ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+            const uint32_t y[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const uint32_t lo = (y[k] & 0x7fffu) << 16, hi = y[k] & 0x7fff0000u;
@@ -477,9 +484,10 @@ __global__ void __launch_bounds__((TcCfg<D, RT, kPre>::kThreads), 1)
           const int e = amax == 0 ? 0 : max(static_cast<int>(amax >> 23) - 127, -112);
           const float up = pow2f(14 - e);
           uint8_t *tile = s_q + x_tile * Cfg::kTileBytes;
-#pragma unroll
+#pragma unroll 8
           for (int i = 0; i < D / 8; ++i) {
-            const uint32_t y[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            const uint4 v = row ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+            const uint32_t y[4] = {v.x, v.y, v.z, v.w};
             uint32_t h[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -595,24 +603,6 @@ __global__ void __launch_bounds__((TcCfg<D, RT, kPre>::kThreads), 1)
             if (!fine) sum = __uint_as_float(0x7fc00000u);
             l += sum;
             __syncwarp();  // tcgen05 loads and stores are the whole warp's
-            if (p.x_cols > 0) {
-              // the logits, for the weights: rows side by side for each key
-              float *xs = p.x + ((static_cast<size_t>(x.seq) * a.n_kv_heads + x.kvh) * p.x_len + j0) *
-                                    p.x_cols + r;
-#pragma unroll 1
-              for (int c = 0; c < 4; ++c) {
-                float v[32];
-                tmem_ld_32x32b_x32(s_addr + 32u * c, v);
-                tmem_ld_wait_regs(v);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                  const int key = c * 32 + i;
-                  if (r < p.x_cols && key < x.len - j0)
-                    xs[static_cast<size_t>(key) * p.x_cols] = v[i] * f;
-                }
-                __syncwarp();
-              }
-            }
             tmem_st_32x32b_x32(s_addr, ph);
             tmem_st_32x32b_x32(s_addr + 32u, ph + 32);
             tmem_st_wait();
@@ -707,6 +697,12 @@ __global__ void __launch_bounds__(256) expand_kernel(const AttendArgs p) {
       if (j0 + id / CH < q.len)
         c[kv][i] = __ldcs(reinterpret_cast<const uint4 *>((kv ? a.v8 : a.k8) + src) + id);
     }
+  const int hidden = hidden_from(q);
+  if (j0 + kTile > hidden) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i)
+      if (j0 + (i * 256 + threadIdx.x) / CH >= hidden) c[1][i] = without_nan16(c[1][i]);
+  }
   int ref = -127;  // the head's largest V scale
   for (int i = lane; i <= (q.len - 1) >> p.log2_block; i += 32)
     ref = max(ref, exp_of(__ldg(a.v_scale + blk + i)));
@@ -733,6 +729,42 @@ __global__ void __launch_bounds__(256) expand_kernel(const AttendArgs p) {
   }
 }
 
+// The outputs that a NaN in V reaches where the kernel above left it out: those,
+// in the NaN's element, of the tokens that see its row, among the call's own
+// tokens' rows but the first.  The rows are looked through while the kernels
+// before end.
+template <int D>
+__global__ void __launch_bounds__(256) mark_nan_kernel(const AttendArgs p) {
+  constexpr int CH = D / 16, NP = 128 * CH / 256;
+  const Cache8AttendArgs &a = p.a;
+  const size_t head = blockIdx.y;
+  const int seq = static_cast<int>(head) / a.n_kv_heads;
+  const SeqInfo q = seq_info(a, seq);
+  const int j0 = max(q.len - q.n + 1, 0) + static_cast<int>(blockIdx.x) * 128;
+  const bool none = q.tiles == 0 || j0 >= q.len;
+  const uint4 *src = reinterpret_cast<const uint4 *>(a.v8 + (head * a.cap + j0) * D);
+  auto load = [&](int i) {
+    const int id = i * 256 + threadIdx.x;
+    return !none && j0 + id / CH < q.len ? __ldg(src + id) : make_uint4(0, 0, 0, 0);
+  };
+  bool any = false;
+#pragma unroll
+  for (int i = 0; i < NP; ++i) any |= has_nan16(load(i));
+  pdl_wait();
+  if (!any) return;
+  for (int i = 0; i < NP; ++i) {
+    uint4 c = load(i);
+    const int id = i * 256 + threadIdx.x, j = j0 + id / CH;
+    hide_nan16(&c, [&](int e) {
+      for (int t = j - (q.len - q.n); t < q.n; ++t)
+        for (int g = 0; g < a.group; ++g)
+          static_cast<__nv_bfloat16 *>(a.out)[q_row(a, seq, static_cast<int>(head) - seq * a.n_kv_heads,
+                                                    t * a.group + g) * D + id % CH * 16 + e] =
+              __float2bfloat16(__uint_as_float(0x7fc00000u));
+    });
+  }
+}
+
 template <int D, int RT, bool kPre>
 bool run_tc(const AttendArgs &p, cudaStream_t s) {
   static int done[64];
@@ -753,7 +785,28 @@ bool run_tc(const AttendArgs &p, cudaStream_t s) {
   return cudaGetLastError() == cudaSuccess;
 }
 
+template <int D>
+bool run_mark_nan(const AttendArgs &p, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((p.a.T + 126) / 128),
+                     static_cast<unsigned>(p.a.n_seqs) * p.a.n_kv_heads);
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, mark_nan_kernel<D>, p) == cudaSuccess) return true;
+  cudaGetLastError();
+  return false;
+}
+
 }  // namespace
+
+bool launch_mark_nan(const cache8::AttendArgs &p, cudaStream_t s) {
+  return p.a.head_dim == 128 ? run_mark_nan<128>(p, s) : run_mark_nan<64>(p, s);
+}
 
 bool launch_attend_tc(const cache8::AttendArgs &p, int row_tiles, cudaStream_t s) {
   if (p.pre_k)

@@ -618,3 +618,74 @@ def test_two_streams_at_once():
     for (o, w, _), (ao, aw) in zip(both, alone):
         assert same(o, ao) and same(w, aw)
     check_clean()
+
+
+def nan_case(dtype, S, Hq, H, d, block, T, lens, n_new, poke):
+    """Outputs, lse and weights with and without NaN codes at poke: (which,
+    sequence, KV head, row, elements)."""
+    g = gen(700)
+    cap = (max(lens) + block - 1) // block * block
+    rc = ref.Cache(S, H, cap, d, block)
+    x = torch.randn(2, S, H, cap, d, generator=g)
+    rc.append([cap] * S, [cap] * S, x[0], x[1])
+    q = torch.randn(S, Hq, T, d, generator=g).to(DT[dtype]).cuda()
+    res = []
+    for bad in (False, True):
+        dev = Dev(S, Hq, H, cap, d, block, dtype)
+        dev.fill(rc, lens)
+        for c, s, h, j, elements in poke if bad else ():
+            for e in elements:
+                dev.codes[c][s, h, j, e] = POISON | (0x80 if e % 2 else 0)
+        out, lse = torch.full_like(q, 7.0), torch.full((S, Hq, T), 7.0, device="cuda")
+        w = torch.full((S, H, cap), 7.0, device="cuda")
+        ws = torch.full((bkv.bkv_cache8_workspace_size(dev.geom, cap, T, 0, True),), 0xff,
+                        dtype=torch.uint8, device="cuda")
+        bkv.bkv_cache8_attend(dev.geom, *dev.bufs, i32(lens), cap, q, T,
+                              None if n_new is None else i32(n_new), 0.0, out, lse, None, w, 1.0, ws)
+        check_clean()
+        res.append((out.double().cpu(), lse.double().cpu(), w.double().cpu()))
+    return res
+
+
+NANS = [
+    # dtype, S, Hq, H, d, block, T, lens, n_new: every kernel, one tile and many
+    ("f32", 2, 4, 2, 96, 16, 5, [40, 900], None),
+    ("bf16", 2, 2, 2, 64, 32, 7, [40, 300], [7, 5]),
+    ("bf16", 2, 4, 2, 128, 64, 4, [133, 700], None),
+    ("bf16", 2, 8, 2, 128, 16, 5, [133, 700], [5, 4]),
+    ("bf16", 2, 8, 2, 64, 16, 8, [40, 300], None),
+    ("bf16", 2, 2, 1, 128, 64, 64, [130, 400], [64, 40]),
+    ("bf16", 1, 2, 1, 64, 32, 50, [50], None),
+    ("bf16", 2, 2, 1, 64, 32, 100, [260, 900], [90, 100]),
+    ("bf16", 2, 2, 1, 128, 32, 128, [260, 900], [128, 77]),
+    ("bf16", 1, 1, 1, 128, 128, 200, [20300], None),
+    ("bf16", 2, 2, 1, 128, 32, 300, [300, 900], [300, 201]),
+    ("bf16", 1, 3, 1, 64, 64, 300, [2000], None),
+]
+
+
+@pytest.mark.parametrize("i", range(len(NANS)))
+def test_attend_nan_in_a_new_row_reaches_the_tokens_that_see_it(i):
+    """NaN in K and V rows among the call's own tokens: every other output is
+    the same bits as without."""
+    dtype, S, Hq, H, d, block, T, lens, n_new = NANS[i]
+    G = Hq // H
+    for c in "vk":
+        poke, hit = [], torch.zeros(S, Hq, T, d, dtype=torch.bool)
+        for s, L in enumerate(lens):
+            n = n_new[s] if n_new else T
+            rows = {L - 1: [0, 17, d - 1], L - n // 2: [3, 17], L - n + 1: [16, 31], L - n // 3: [40]}
+            for j, elements in rows.items():
+                h = (s + j) % H
+                poke.append((c, s, h, j, elements))
+                t0 = j - (L - n)                     # the first token that sees row j
+                cols = elements if c == "v" else range(d)
+                for e in cols:
+                    hit[s, h * G:(h + 1) * G, max(t0, 0):n, e] = True
+        (o0, z0, w0), (o1, z1, w1) = nan_case(dtype, S, Hq, H, d, block, T, lens, n_new, poke)
+        assert bool(o0.isfinite().all())
+        assert same(o1, torch.where(hit, math.nan, o0))
+        if c == "v":
+            assert same(z1, z0) and same(w1, w0)
+        else:
+            assert same(z1, torch.where(hit[..., 0], math.nan, z0))
