@@ -315,9 +315,11 @@ bkv_status bkv_score_noalloc(const bkv_cache_desc *desc, const void *k,
  *
  * Supported: dtype (of new rows, queries and outputs) bf16 or f32, head_dim a
  * multiple of 16 up to 128, block 16, 32, 64 or 128, capacity a multiple of
- * block, n_seqs * n_kv_heads at most 65535.  Codes, new rows, queries,
- * outputs and weights are 16-byte aligned, the rest 4-byte.  Attention uses the tensor
- * cores for bf16 with head_dim 64 or 128 and the CUDA cores otherwise. */
+ * block, n_seqs * n_kv_heads at most 65535, and times capacity at most
+ * 2^31 - 65536.  Codes, new rows, queries, outputs and weights are 16-byte
+ * aligned, the rest 4-byte; every tensor is dense, in the order given.
+ * Attention uses the tensor cores for bf16 with head_dim 64 or 128 and the CUDA
+ * cores otherwise. */
 typedef struct {
   int32_t n_seqs;
   int32_t n_q_heads;   /* multiple of n_kv_heads */
@@ -330,8 +332,12 @@ typedef struct {
 
 /* Bytes of workspace for bkv_cache8_attend with T tokens (T = 0: not called;
  * weights != 0: with weights_out) and bkv_cache8_evict with budget K (K = 0:
- * not called) over lengths up to max_len.  0 for invalid arguments.  Calls
- * that can overlap on the GPU need a workspace each. */
+ * not called) over lengths up to max_len.  0 for invalid arguments.  It grows
+ * with max_len and K but not always with T (calls of more than 256 query rows
+ * a KV head hold K and V in 16 bits, calls of up to 32 with weights their
+ * logits): for calls of several T, the largest of their sizes.  Calls that can
+ * overlap on the GPU need a workspace each; calls in one stream, and captured
+ * graphs replayed one after another, may share one. */
 size_t bkv_cache8_workspace_size(const bkv_cache8_desc *desc, int64_t max_len,
                                  int32_t T, int64_t K, int32_t weights);
 
@@ -366,10 +372,16 @@ bkv_status bkv_cache8_append(const bkv_cache8_desc *desc, void *k8, void *v8,
  *               j >= lens[s] are left as they were
  *   weights_in  device, like weights_out, optional (NULL: zeros); may be
  *               weights_out itself
- * Products are summed in f32, f32 queries on the CUDA cores.  With bf16 the
- * probabilities are rounded to f16 for the second product (2^-11); the
- * weights and lse come from f32.  Results do not depend on timing: sums run
- * in an order fixed by the lengths.
+ * Products are summed in f32, f32 queries on the CUDA cores.  On the tensor
+ * cores the operands are f16 under powers of two: queries exact but for elements
+ * 2^-32 under the largest of their row (of 32 rows, where a KV head has more);
+ * codes exact for up to 32 rows, and above that but for parts under 2^-24 of the
+ * largest scale, K's among 128 rows and V's among those that a CTA takes;
+ * probabilities rounded (2^-11, down to 2^-25 of the largest).  The weights and
+ * lse come from f32.  A logit above f32's range counts as NaN.
+ * A NaN in K makes the outputs and lse of the tokens that see its row NaN, and
+ * what they add to the weights; a NaN in V only its element of their outputs.
+ * Results do not depend on timing: sums run in an order fixed by the lengths.
  * Requires 1 <= max_len <= capacity, 1 <= T. */
 bkv_status bkv_cache8_attend(const bkv_cache8_desc *desc, const void *k8,
                              const void *v8, const float *k_scale,

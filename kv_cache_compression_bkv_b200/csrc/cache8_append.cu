@@ -1,14 +1,18 @@
 // cache8_append.cu -- new K/V rows quantised into the 8-bit cache.
 //
 // One CTA per (block of rows touched, sequence, KV head, K or V), or per run of
-// blocks.  The block's
-// new rows are read once into registers, their largest magnitude is reduced
-// over the CTA, the block's scale follows from it (and from the scale of the
-// rows the block already holds, which never shrinks), and the codes are
-// written.  Only when the scale grows are the older rows of the block read,
-// moved to the new scale and written back.  A block belongs to one CTA, so no
-// two CTAs touch a scale.  Bound by HBM for whole prompts; one decode step is
-// a launch and three dependent loads (length, scale and row, codes).
+// four blocks.  A block's new rows are read once into registers, their largest
+// magnitude is reduced over the CTA, the block's scale follows from it (and from
+// the scale of the rows the block already holds, which never shrinks), and the
+// codes are written.  Only when the scale grows are the older rows of the block
+// read, moved to the new scale and written back.  A block belongs to one CTA, so
+// no two CTAs touch a scale.
+//
+// Whole prompts are bound by HBM: 4 of 8192 rows, 8 heads of 128 in bf16, 201 MB
+// in 37 us, 84% of the measured copy rate (40 us with a select per element for
+// those that are not finite, 43 with a CTA per block, 85 with a thread per
+// element).  One decode step is a launch and three dependent loads (length, scale
+// and row, codes): 2.5 us in a graph, 5 us as a call, which is its time on the host.
 #include <cuda_bf16.h>
 
 #include <algorithm>

@@ -14,24 +14,36 @@
 // the workspace and attend_finish_kernel joins the parts in their order.  The
 // lengths are read on the device; the host needs only their upper bound.
 //
-// attend_mma_kernel (bf16, head_dim 64 or 128): decode is bound by the codes'
-// bytes, so each of the 8 warps streams its own 16 keys of every tile through
-// a private cp.async ring (no CTA barrier in the loop) and holds its own
-// softmax statistics and output.  Codes become f16, exactly, two at a time
-// (cvt.rn.f16x2.e4m3x2).  K is the A operand of mma.m16n8k16 and the 8 query
-// rows the B operand, so a group of up to 8 query heads costs no padding; V is
+// attend_mma_kernel (bf16, head_dim 64 or 128, up to 32 query rows a KV head):
+// decode is bound by the codes' bytes, so each of the 4 warps streams its own 32
+// keys of every tile through a private cp.async ring (no CTA barrier in the
+// loop) and holds its own softmax statistics and output.  Codes become f16,
+// exactly, two at a time (cvt.rn.f16x2.e4m3x2).  K is the A operand of
+// mma.m16n8k16 and 8 query rows the B operand, so a group of up to 8 query heads
+// costs no padding; more rows are more n-tiles (NT) under the same codes.  V is
 // read transposed by ldmatrix.b8 and is the A operand of the second product.
 // Both products' reduction indices are permuted so that the four consecutive
 // bytes a lane holds are its fragment as they are: element order inside a
 // contraction is free.  Queries become f16 under a power-of-two factor per
-// row, exact but for elements 2^-24 and more below the row's largest.
+// row, exact but for elements 2^-32 and more below the row's largest (f16 holds
+// bf16's 8 bits down to 2^-17, the largest is put at 2^14).
+//   The f16 product, not the 8-bit one: the e4m3 mma.sync took longer here (one
+// ragged batch 165 us against 147), and tcgen05 pads 8 rows to 128.
 //   The probabilities are rounded to f16 (2^-11, summed in f32 before that),
 // multiplied by the block's V scale over the largest one met so far.
-//   The softmax reference of a row moves only when a logit exceeds it by more
-// than 8 (in log2): one vote per tile instead of a max over lanes.
+//   The softmax reference of a row is put 7 (in log2) under the largest logit and
+// moves only when a logit passes it by 15, so that probabilities stay under
+// 2^15: one vote per tile instead of a max over lanes.
+//   Measured: 32 sequences of 517 .. 16384 rows, 32/8 heads of 128, one token, in
+// 109 us, 5.1 TB/s of codes, 79% of the measured copy rate.  What is left is the
+// GPU's memory channels, which serve its parts unevenly (CTAs of equal runs end
+// 40 to 58 us into a shorter call; 2 to 6 times as many, shorter runs were
+// slower, 131 us), and the join.
 //
 // attend_simt_kernel (f32, and other head sizes): the same split with f32
 // products on the CUDA cores.
+//
+// More query rows: cache8_attend_tc.cu.
 #include <cuda_bf16.h>
 
 #include <algorithm>

@@ -63,6 +63,16 @@ def test_bad_geometry(i):
     assert LIB.bkv_cache8_workspace_size(ctypes.byref(d), 64, 1, 64, 1) == 0
 
 
+def test_row_limit():
+    """Positions stay in 32 bits with room for what a kernel rounds up to."""
+    most = (1 << 31) - 65536
+    assert evict(desc(S=1, Hq=1, Hkv=1, cap=most + 64, block=64), max_len=most + 64) == INVALID
+    d = desc(S=1, Hq=1, Hkv=1, cap=most, block=64)
+    assert LIB.bkv_cache8_workspace_size(ctypes.byref(d), most, 1, 0, 0) > 0
+    d = desc(S=2, Hq=1, Hkv=1, cap=most, block=64)
+    assert LIB.bkv_cache8_workspace_size(ctypes.byref(d), most, 1, 0, 0) == 0
+
+
 def test_null_desc():
     assert append(None) == attend(None) == evict(None) == INVALID
     assert LIB.bkv_cache8_workspace_size(None, 64, 1, 64, 1) == 0

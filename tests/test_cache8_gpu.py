@@ -689,3 +689,155 @@ def test_attend_nan_in_a_new_row_reaches_the_tokens_that_see_it(i):
             assert same(z1, z0) and same(w1, w0)
         else:
             assert same(z1, torch.where(hit[..., 0], math.nan, z0))
+
+
+MANY_ROWS = [
+    # dtype, S, Hq, H, d, block, T, lens, n_new, weights: more than 32 query rows a
+    # KV head (one and two row tiles, expanded tiles), parts of segments
+    ("bf16", 1, 5, 1, 128, 64, 7, [30011], None, True),            # 35 rows, over every CTA
+    ("bf16", 3, 2, 1, 64, 128, 64, [20000, 64, 5001], [64, 64, 17], True),
+    ("bf16", 2, 2, 2, 128, 16, 128, [9000, 130], [100, 128], "fresh"),
+    ("bf16", 1, 3, 1, 128, 32, 80, [25000], None, False),          # 240 rows, two row tiles
+    ("bf16", 4, 4, 2, 64, 16, 64, [64, 0, 12000, 700], [64, 0, 1, 33], True),
+    ("bf16", 2, 2, 1, 128, 64, 129, [129, 6000], [129, 128], True),
+    ("bf16", 2, 1, 1, 128, 128, 513, [9000, 513], [513, 300], True),   # expanded tiles
+    ("bf16", 3, 4, 2, 64, 32, 70, [5000, 1, 71], [70, 1, 70], True),
+    ("bf16", 2, 5, 1, 128, 16, 60, [40, 20], [60, 20], True),      # rows that see nothing
+    ("bf16", 1, 40, 1, 128, 64, 1, [15000], None, True),           # a wide group, one token
+    ("bf16", 40, 2, 1, 64, 16, 20, [(61 * i) % 333 for i in range(40)],
+     [min(i % 21, 20) for i in range(40)], True),
+    # up to 32 rows, many tiles a CTA
+    ("bf16", 1, 12, 1, 128, 64, 1, [90001], None, True),
+    ("bf16", 1, 3, 1, 64, 32, 7, [60000], None, True),
+    ("bf16", 1, 8, 1, 128, 16, 4, [50000], None, "fresh"),
+]
+
+
+@pytest.mark.parametrize("i", range(len(MANY_ROWS)))
+def test_attend_many_rows(i):
+    dtype, S, Hq, H, d, block, T, lens, n_new, weights = MANY_ROWS[i]
+    run_attend(dtype, S, Hq, H, d, block, T, lens, n_new, weights, 800 + i, decay=0.875)
+
+
+def test_attend_many_rows_large_logits_and_scales_far_apart():
+    """Softmax references that move while the outputs stand in TMEM, and K and V
+    scales of one tile binades apart."""
+    def shape(x):
+        for b in range(0, x.shape[3], 16):
+            x[1, :, :, b:b + 16] *= 0.0 if b % 80 == 0 else 2.0 ** ((b // 16 * 7) % 30 - 15)
+            x[0, :, :, b:b + 16] *= 2.0 ** ((b // 16 * 5) % 9 - 6)
+    for Hq, T in ((10, 5), (6, 40), (2, 200)):
+        run_attend("bf16", 2, Hq, 1, 128, 64, T, [700, 2000], None, True, 820, q_mag=20.0)
+        run_attend("bf16", 1, Hq, 1, 64, 16, T, [900], None, True, 821, shape_values=shape)
+
+
+@pytest.mark.parametrize("T", [3, 12, 50, 200])
+def test_captured_chunk_replays_with_new_lengths(T):
+    """A padded call of several tokens in a graph: replays with other lengths,
+    counts and rows equal the eager calls bit for bit, the workspace shared with
+    another captured call in between."""
+    S, Hq, H, d, cap = 3, 4, 2, 128, 1024
+    res = []
+    for graphed in (False, True):
+        g = gen(830)
+        dev = Dev(S, Hq, H, cap, d, 32, "bf16")
+        ws = torch.empty(max(bkv.bkv_cache8_workspace_size(dev.geom, cap, t, 0, True) for t in (1, T)),
+                         dtype=torch.uint8, device="cuda")
+        lens, n_new = i32([0] * S), i32([0] * S)
+        kn, vn = (torch.zeros(S, H, T, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        q = torch.zeros(S, Hq, T, d, dtype=torch.bfloat16, device="cuda")
+        q1 = torch.zeros(S, Hq, 1, d, dtype=torch.bfloat16, device="cuda")
+        out, out1 = torch.zeros_like(q), torch.zeros_like(q1)
+        dev.weights.zero_()
+
+        def chunk():
+            lens.add_(n_new)
+            bkv.bkv_cache8_append(dev.geom, *dev.bufs, lens, kn, vn, T, n_new)
+            bkv.bkv_cache8_attend(dev.geom, *dev.bufs, lens, cap, q, T, n_new, 0.0, out, None,
+                                  dev.weights, dev.weights, 1.0, ws)
+
+        def one():
+            bkv.bkv_cache8_attend(dev.geom, *dev.bufs, lens, cap, q1, 1, None, 0.0, out1, None,
+                                  None, None, 1.0, ws)
+
+        if graphed:
+            torch.cuda.synchronize()
+            side = torch.cuda.Stream()
+            gc, go = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+            with torch.cuda.graph(gc, stream=side):
+                chunk()
+            with torch.cuda.graph(go, stream=side):
+                one()
+        outs = []
+        for i in range(4):
+            for t in (kn, vn, q, q1):
+                t.copy_(torch.randn(t.shape, generator=g))
+            n_new.copy_(torch.tensor([T, (i * 7) % (T + 1), 1 if i else T], dtype=torch.int32))
+            gc.replay() if graphed else chunk()
+            go.replay() if graphed else one()
+            outs += [out.clone(), out1.clone()]
+        torch.cuda.synchronize()
+        res.append(outs + [dev.weights[s, :, :int(lens[s])].clone() for s in range(S)] + [lens.clone()])
+    check_clean()
+    for a, b in zip(*res):
+        assert same(a, b)
+
+
+def test_offsets_past_32_bits():
+    """A head of more than 2^32 codes, all zeros but its last rows: these appended,
+    attended to and kept by an eviction.
+
+    Every zero key has logit 0, so with n0 of them the denominators are n0 plus the
+    last rows' terms.  Bounds as in attend_bounds, and for the denominator a lane's
+    sum of at most cap / 128 / 296 tiles x 8 terms, below 2^13 steps of 2^-24."""
+    d, block, T = 128, 64, 40
+    cap = (1 << 25) + 128
+    codes = {n: torch.zeros(1, 1, cap, d, dtype=torch.uint8, device="cuda") for n in "kv"}
+    scale = {n: torch.full((1, 1, cap // block), 2.0 ** -10, device="cuda") for n in "kv"}
+    bufs = codes["k"], codes["v"], scale["k"], scale["v"]
+    geom = bkv.geometry8_of(codes["k"], scale["k"], 2, torch.bfloat16)
+    g = gen(840)
+    k, v = (torch.randn(1, 1, T, d, generator=g).bfloat16() for _ in range(2))
+    lens = i32([cap])
+    bkv.bkv_cache8_append(geom, *bufs, lens, k.cuda(), v.cuda(), T)
+    rc = ref.Cache(1, 1, block, d, block)
+    rc.append([T], [T], k, v)
+    for n in "kv":
+        assert float(scale[n][0, 0, -1]) == float(rc.scale[n][0, 0, 0])
+        assert same(ref.decode(codes[n][0, 0, cap - T:]), rc.code[n][0, 0, :T])
+        assert not bool(codes[n][0, 0, cap - block:cap - T].any())
+    kv, vv = rc.values("k", 0, 0, T), rc.values("v", 0, 0, T)
+    w = torch.zeros(1, 1, cap, device="cuda")
+    ws = torch.empty(max(bkv.bkv_cache8_workspace_size(geom, cap, t, 1024, True) for t in (1, 2, 20)),
+                     dtype=torch.uint8, device="cuda")
+    for T2 in (1, 2, 20):
+        q = torch.randn(1, 2, T2, d, generator=g).bfloat16()
+        out = torch.empty_like(q, device="cuda")
+        bkv.bkv_cache8_attend(geom, *bufs, lens, cap, q.cuda(), T2, None, 0.0, out, None, None, w, 1.0, ws)
+        z = q[0].double() @ kv.T / math.sqrt(d)
+        see = torch.arange(T)[None, None] <= T - T2 + torch.arange(T2)[None, :, None]
+        p = torch.where(see, z.exp(), 0.0)
+        p = p / (p.sum(-1, keepdim=True) + cap - T)
+        eps = (d + 4) * 2.0 ** -22 / math.sqrt(d) * (q[0].double().abs() @ kv.abs().T)
+        rel = 2.0 * eps.amax(-1, keepdim=True) + 2.0 ** -19 + 2.0 ** -11
+        av = p @ vv.abs()
+        tol = (rel + 2.0 ** -20 + 2.0 ** -11) * av + T * 2.0 ** -25 * 448 * float(rc.scale["v"][0, 0, 0]) * \
+            p.amax(-1, keepdim=True)
+        o = p @ vv
+        err = (out[0].double().cpu() - o).abs()
+        assert bool((err <= tol + ref.U_BF16 * (o.abs() + tol)).all()), float((err / o.abs()).max())
+        want = p.sum((0, 1))
+        got = w[0, 0, cap - T:].double().cpu()
+        assert bool(((got - want).abs() <= ((rel + 2.0 ** -20) * p).sum((0, 1)) + 2 * T2 * 2.0 ** -24 * want).all())
+    w.zero_()
+    inner = torch.randperm(cap - 64, generator=g)[:970] + 14
+    keep = torch.cat([inner, torch.arange(cap - 40, cap - 10)])
+    w[0, 0, keep.cuda()] = 1.0 + torch.rand(1000, generator=g).cuda()
+    idx, nl = torch.full((1, 1, 1024), -3, dtype=torch.int32, device="cuda"), i32([-1])
+    bkv.bkv_cache8_evict(geom, *bufs, w, lens, cap, 1024, 14, 10, geom, *bufs, w, idx, nl, ws)
+    check_clean()
+    assert nl.tolist() == [1024]
+    assert idx[0, 0].tolist() == sorted(list(range(14)) + keep.tolist() + list(range(cap - 10, cap)))
+    for n in "kv":
+        assert float(scale[n][0, 0, 15]) == float(rc.scale[n][0, 0, 0])
+        assert same(ref.decode(codes[n][0, 0, 1024 - T:1024]), rc.code[n][0, 0, :T])
