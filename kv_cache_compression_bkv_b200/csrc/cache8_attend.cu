@@ -70,7 +70,8 @@ constexpr int kSimtKeys = 16;
 // (summed here; element (r, d) of a buffer at off(r, d)) and the row statistics
 // m, l.  A whole segment goes out, a part to the CTA's slot.  first[d]: the
 // lowest key whose NaN in V was left out (hide_nan16), for the rows that see it,
-// where first[D] says that there are any; so does the result.
+// where first[D] says that there are any; so does the result.  (With one token
+// every row sees every key, and first is not looked at.)
 template <int kRows, int kBufs, int kCta, typename T, typename Off>
 __device__ __forceinline__ bool write_segment(const AttendArgs &p, const float *buf, int buf_stride,
                                               const float *m, const float *l, const int *first,
@@ -80,7 +81,7 @@ __device__ __forceinline__ bool write_segment(const AttendArgs &p, const float *
   const int D = a.head_dim;
   const int kvh = unit / p.row_blocks, r0 = (unit - kvh * p.row_blocks) * kRows;
   const int rows = a.group * q.n;
-  const bool nans = first[D] != 0;
+  const bool nans = a.T > 1 && first[D] != 0;
   float *part = p.part + (static_cast<size_t>(blockIdx.x) * 2 + slot) * (kRows * (2 + D));
   for (int e = threadIdx.x; e < kRows * D; e += kCta) {
     const int r = e / D, d = e - r * D;
@@ -322,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_mma_kernel(const AttendArg
     if (threadIdx.x == 0) s_first[D] = 0;
     __syncthreads();
   };
-  reset_first();
+  if (a.T > 1) reset_first();
 
   // ---- what a lane reads
   const int key0 = ((g >> 1) << 2) | (g & 1);  // and key0 + 2: rows g and g + 8 of an m-tile
@@ -716,7 +717,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) attend_simt_kernel(const Atte
     if (threadIdx.x == 0) s_first[D] = 0;
     __syncthreads();
   };
-  reset_first();
+  if (a.T > 1) reset_first();
   float o[kSimtRows][4], m[kSimtRows], l[kSimtRows];
   bool fresh = true;
   int seg_tiles = 0, stage = 0;
