@@ -119,5 +119,40 @@ __device__ __forceinline__ float absmax16(uint4 c) {
   return fmaxf(__low2float(m), __high2float(m));
 }
 
+// Programmatic dependent launch.  A kernel launched so may start while the one
+// before it in the stream runs, once every CTA of that has passed
+// pdl_launch_dependents or ended; pdl_wait holds it until that one has ended and
+// its writes are there.  Every CTA waits before it ends, so that a kernel never
+// ends before one that it follows; and a kernel that others may follow at once
+// waits before it lets them start, so that what these read before their own wait
+// (lengths) is complete.  One decode step's attention (28/4 heads, 8192 rows) 14.4 ->
+// 13.5 us, eviction of one layer 16.4 -> 14.7, four prompts appended 36.9 -> 35.5.
+__device__ __forceinline__ void pdl_launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// cluster: CTAs per cluster, 1 for none
+template <typename Args>
+bool launch_programmatic(void (*kernel)(const Args), dim3 grid, int threads, size_t smem, int cluster,
+                         cudaStream_t stream, const Args &args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, args) == cudaSuccess) return true;
+  cudaGetLastError();
+  return false;
+}
+
 }  // namespace cache8
 }  // namespace bkv

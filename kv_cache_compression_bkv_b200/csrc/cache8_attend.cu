@@ -253,6 +253,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_mma_kernel(const AttendArg
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
   const int units = a.n_kv_heads * p.row_blocks;
+  pdl_wait();
   pdl_launch_dependents();
   int mine;
   const Split w = split_of(a, units, p.ctas, &mine);
@@ -675,6 +676,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) attend_simt_kernel(const Atte
   uint8_t *ring = reinterpret_cast<uint8_t *>(s_buf + kSimtWarps * kSimtRows * D) +
                   warp * 2 * simt_stage_bytes(D);
   const int units = a.n_kv_heads * p.row_blocks;
+  pdl_wait();
   pdl_launch_dependents();
   int mine;
   const Split w = split_of(a, units, p.ctas, &mine);
@@ -1147,16 +1149,15 @@ bool run_mma(const AttendArgs &p, cudaStream_t s) {
   using Cfg = MmaCfg<D, NT>;
   static_assert(Cfg::kSmem <= 113 * 1024, "shared memory");
   if (!ensure_smem_limit(attend_mma_kernel<D, NT>, Cfg::kSmem, done)) return false;
-  attend_mma_kernel<D, NT><<<p.ctas, kThreads, Cfg::kSmem, s>>>(p);
-  return cudaGetLastError() == cudaSuccess;
+  return launch_programmatic(attend_mma_kernel<D, NT>, dim3(p.ctas), kThreads, Cfg::kSmem, 1, s, p);
 }
 
 template <typename T>
 bool run_simt(const AttendArgs &p, cudaStream_t s) {
   static int done[64];
   if (!ensure_smem_limit(attend_simt_kernel<T>, simt_smem(kMaxD), done)) return false;
-  attend_simt_kernel<T><<<p.ctas, kSimtThreads, simt_smem(p.a.head_dim), s>>>(p);
-  return cudaGetLastError() == cudaSuccess;
+  return launch_programmatic(attend_simt_kernel<T>, dim3(p.ctas), kSimtThreads,
+                             simt_smem(p.a.head_dim), 1, s, p);
 }
 
 template <int kRows, typename T>
@@ -1175,18 +1176,8 @@ bool run_finish(AttendArgs p, cudaStream_t s) {
     p.w_chunks = static_cast<int>((p.a.max_len + p.w_keys - 1) / p.w_keys);
     grid += heads * p.w_chunks;
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(kSimtThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, attend_finish_kernel<kRows, T>, p) == cudaSuccess) return true;
-  cudaGetLastError();
-  return false;
+  return launch_programmatic(attend_finish_kernel<kRows, T>, dim3(static_cast<unsigned>(grid)),
+                             kSimtThreads, 0, 1, s, p);
 }
 
 bool use_mma(int dtype, int head_dim) {

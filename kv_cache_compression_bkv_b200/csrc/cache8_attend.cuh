@@ -51,13 +51,6 @@ __device__ __forceinline__ bool elect_one() {
   return one != 0;
 }
 
-// Programmatic dependent launch: the next kernel of the stream may start, and
-// the wait, in that kernel, for everything before it.
-__device__ __forceinline__ void pdl_launch_dependents() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // ------------------------------------------------------------ the work split
 
 struct SeqInfo {

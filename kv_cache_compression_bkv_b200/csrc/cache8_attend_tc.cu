@@ -800,19 +800,9 @@ bool run_tc(const AttendArgs &p, cudaStream_t s) {
 
 template <int D>
 bool run_mark_nan(const AttendArgs &p, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((p.a.T + 126) / 128),
-                     static_cast<unsigned>(p.a.n_seqs) * p.a.n_kv_heads);
-  cfg.blockDim = dim3(256);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, mark_nan_kernel<D>, p) == cudaSuccess) return true;
-  cudaGetLastError();
-  return false;
+  const dim3 grid(static_cast<unsigned>((p.a.T + 126) / 128),
+                  static_cast<unsigned>(p.a.n_seqs) * p.a.n_kv_heads);
+  return launch_programmatic(mark_nan_kernel<D>, grid, 256, 0, 1, s, p);
 }
 
 }  // namespace

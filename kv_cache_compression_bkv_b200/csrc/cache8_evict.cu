@@ -148,7 +148,8 @@ __global__ void __launch_bounds__(kSelThreads, 3) evict_select_kernel(const Cach
   __shared__ uint32_t s_list[kListMax];
   __shared__ uint32_t s_warp[kSelWarps];
   __shared__ uint32_t s_bin[2], s_count;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  pdl_wait();
+  pdl_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int head = blockIdx.x, seq = head / a.n_kv_heads;
   const int L = a.lens[seq];
@@ -326,8 +327,10 @@ __global__ void __launch_bounds__(kThreads) evict_compact_kernel(const Cache8Evi
   const int head = blockIdx.x / a.ctas_per_head;
   const int part = blockIdx.x - head * a.ctas_per_head;  // in place: the rank in the cluster
   const int seq = head / a.n_kv_heads;
-  // launched while the select kernel ends: nothing of its is read before this
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // launched while the select kernel ends: nothing of its is read before this.
+  // The next kernel starts when this one ends: its CTAs beside the last of these
+  // cost more than they win (36 layers of 8192 rows 120 us, and 117)
+  pdl_wait();
   const int n = a.kept[seq];
   if (part == 0 && tid == 0 && head - seq * a.n_kv_heads == 0 && n >= 0 && a.new_lens)
     a.new_lens[seq] = n;
@@ -434,28 +437,16 @@ bkv_status launch_cache8_evict(Cache8EvictArgs a, bool in_place, cudaStream_t st
   if (injected_launch_failure()) return BKV_ERR_CUDA;
   a.log2_block = a.block == 16 ? 4 : a.block == 32 ? 5 : a.block == 64 ? 6 : 7;
   const unsigned heads = static_cast<unsigned>(a.n_seqs) * a.n_kv_heads;
-  evict_select_kernel<<<heads, kSelThreads, 0, stream>>>(a);
-  if (cudaGetLastError() != cudaSuccess) return BKV_ERR_CUDA;
+  if (!launch_programmatic(evict_select_kernel, dim3(heads), kSelThreads, 0, 1, stream, a))
+    return BKV_ERR_CUDA;
   const long long rows = std::min<long long>(a.K, a.max_len);
   long long per = (rows + kRows - 1) / kRows;
   if (in_place) per = per >= 8 ? 8 : per >= 4 ? 4 : per >= 2 ? 2 : 1;  // the cluster's CTAs
   a.ctas_per_head = static_cast<int>(per);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(heads * per));
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = static_cast<unsigned>(per);
-  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = in_place ? 2 : 1;
+  const dim3 grid(static_cast<unsigned>(heads * per));
   auto kernel = in_place ? compact_kernel_for<true>(a.head_dim) : compact_kernel_for<false>(a.head_dim);
-  if (cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess) return BKV_OK;
-  cudaGetLastError();
-  return BKV_ERR_CUDA;
+  const int cluster = in_place ? static_cast<int>(per) : 1;
+  return launch_programmatic(kernel, grid, kThreads, 0, cluster, stream, a) ? BKV_OK : BKV_ERR_CUDA;
 }
 
 }  // namespace bkv

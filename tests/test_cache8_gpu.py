@@ -874,3 +874,103 @@ def test_attend_workspace_of_16_byte_alignment(dtype, T):
         res.append((out, w))
     assert bool(res[0][0].isfinite().all())
     assert same(res[0][0], res[1][0]) and same(res[0][1], res[1][1])
+
+
+def test_calls_follow_copies_and_joined_streams_in_a_graph():
+    """A captured step whose calls follow a memset, a copy and an event of another
+    stream instead of kernels, replayed back to back."""
+    S, Hq, H, d, cap = 2, 8, 2, 128, 512
+    dev = Dev(S, Hq, H, cap, d, 32, "bf16")
+    want = Dev(S, Hq, H, cap, d, 32, "bf16")
+    g = gen(870)
+    n = 24
+    k, v, q = (torch.randn(n, S, h, 1, d, generator=g).bfloat16().cuda() for h in (H, H, Hq))
+    all_lens = torch.tensor([[i + 1, 2 * i + 1] for i in range(n)], dtype=torch.int32).pin_memory()
+    ws = torch.empty(bkv.bkv_cache8_workspace_size(dev.geom, cap, 1, 300, True), dtype=torch.uint8,
+                     device="cuda")
+    res = []
+    for c, graphed in ((want, False), (dev, True)):
+        lens = i32([0, 0])
+        kn, vn, qn = torch.empty_like(k[0]), torch.empty_like(v[0]), torch.empty_like(q[0])
+        out = torch.empty_like(qn)
+        w = torch.zeros(S, H, cap, device="cuda")
+        host = torch.zeros(2, dtype=torch.int32).pin_memory()
+        torch.cuda.synchronize()
+
+        def step(side):
+            lens.copy_(host, non_blocking=True)          # a copy straight before the append
+            bkv.bkv_cache8_append(c.geom, *c.bufs, lens, kn, vn, 1, i32_one)
+            if side is not None:                         # a join straight before attend
+                side.wait_stream(torch.cuda.current_stream())
+                with torch.cuda.stream(side):
+                    out.zero_()
+                torch.cuda.current_stream().wait_stream(side)
+            bkv.bkv_cache8_attend(c.geom, *c.bufs, lens, cap, qn, 1, i32_one, 0.0, out, None, w, w,
+                                  1.0, ws)
+            out2.copy_(out)
+
+        i32_one = i32([1, 1])
+        out2 = torch.empty_like(out)
+        if graphed:
+            st, other = torch.cuda.Stream(), torch.cuda.Stream()
+            gr = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(gr, stream=st):
+                step(other)
+        outs = []
+        for i in range(n):
+            torch.cuda.synchronize()
+            host.copy_(all_lens[i])
+            # sequence 1 gets every second row only: the rows between stay zero codes
+            kn.copy_(k[i]), vn.copy_(v[i]), qn.copy_(q[i])
+            c.codes["k"][1].masked_fill_(c.codes["k"][1] == POISON, 0)
+            c.codes["v"][1].masked_fill_(c.codes["v"][1] == POISON, 0)
+            c.scale["k"][1].nan_to_num_(2.0 ** -8), c.scale["v"][1].nan_to_num_(2.0 ** -8)
+            w.nan_to_num_(0.0)
+            gr.replay() if graphed else step(None)
+            outs.append(out2.clone())
+        torch.cuda.synchronize()
+        res.append([torch.stack(outs), w, *c.bufs])
+    check_clean()
+    assert bool(res[0][0].isfinite().all())
+    for a, b in zip(*res):
+        assert same(a, b)
+
+
+def test_a_loop_without_a_pause():
+    """Append, attend and evict back to back, each call's input the one before's
+    output, against the same calls with a synchronisation after each."""
+    S, Hq, H, d, cap = 3, 8, 2, 128, 512
+    res = []
+    for pause in (False, True):
+        g = gen(880)
+        dev = Dev(S, Hq, H, cap, d, 32, "bf16")
+        ws = torch.empty(bkv.bkv_cache8_workspace_size(dev.geom, cap, 1, 100, True), dtype=torch.uint8,
+                         device="cuda")
+        k, v = (torch.randn(S, H, 128, d, generator=g).bfloat16().cuda() for _ in range(2))
+        q = torch.randn(S, Hq, 1, d, generator=g).bfloat16().cuda()
+        lens, one = i32([128, 90, 101]), i32([1, 1, 1])
+        dev.weights.zero_()
+        out = torch.zeros_like(q)
+        kn, vn = k[:, :, :1].contiguous(), v[:, :, :1].contiguous()
+        wait = torch.cuda.synchronize if pause else lambda: None
+        bkv.bkv_cache8_append(dev.geom, *dev.bufs, lens, k, v, 128, i32([128, 90, 101]))
+        for i in range(60):
+            # the output of a call is the next one's query and new row
+            bkv.bkv_cache8_attend(dev.geom, *dev.bufs, lens, cap, q, 1, None, 0.0, out, None,
+                                  dev.weights, dev.weights, 0.9, ws)
+            wait()
+            bkv.bkv_cache8_attend(dev.geom, *dev.bufs, lens, cap, out, 1, None, 0.0, q, None,
+                                  dev.weights, dev.weights, 0.9, ws)
+            wait()
+            bkv.bkv_cache8_append(dev.geom, *dev.bufs, lens, kn, vn, 1, one)
+            wait()
+            bkv.bkv_cache8_evict(dev.geom, *dev.bufs, dev.weights, lens, cap, 100 - i % 7, 4, 16,
+                                 dev.geom, *dev.bufs, dev.weights, None, lens, ws)
+            wait()
+        torch.cuda.synchronize()
+        n = int(lens[0])
+        res.append([q, out, lens] + [dev.codes[c][:, :, :n].clone() for c in "kv"] +
+                   [dev.weights[:, :, :min(lens.tolist())].clone()])
+    check_clean()
+    for a, b in zip(*res):
+        assert same(a, b)
