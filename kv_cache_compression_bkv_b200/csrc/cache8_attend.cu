@@ -1207,7 +1207,10 @@ Cache8AttendPlan plan_cache8_attend(int n_seqs, int n_q_heads, int n_kv_heads, i
   Cache8AttendPlan p{};
   const long long rows = static_cast<long long>(n_q_heads / n_kv_heads) * T;
   const bool mma = use_mma(dtype, head_dim);
-  p.nt = !mma || rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 24 ? 3 : 4;
+  // 25 to 32 rows of 128 elements do not fit the registers: two row blocks of 16
+  // read the codes twice and take 61 us (with weights 88) where one of 32 took 74
+  // (115): 8 sequences of 8192 rows, 32/8 heads, 8 tokens
+  p.nt = !mma || rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 24 ? 3 : head_dim == 128 ? 2 : 4;
   // Measured on both sides: 8 sequences to 8192 rows of 32/8 heads, 40 query rows
   // a KV head 70 us on tcgen05 and 107 us on mma.sync, 128 rows 87 and 184; 24
   // rows with weights (a key's logits are then kept) 109 and 48.
@@ -1283,8 +1286,7 @@ bkv_status launch_cache8_attend(const Cache8AttendArgs &a, const Cache8AttendPla
       ok = (wide ? run_mma<128, 3>(p, stream) : run_mma<64, 3>(p, stream)) &&
            run_finish<24, __nv_bfloat16>(p, stream);
     else
-      ok = (wide ? run_mma<128, 4>(p, stream) : run_mma<64, 4>(p, stream)) &&
-           run_finish<32, __nv_bfloat16>(p, stream);
+      ok = run_mma<64, 4>(p, stream) && run_finish<32, __nv_bfloat16>(p, stream);
   } else if (dtype == BKV_BF16) {
     ok = run_simt<__nv_bfloat16>(p, stream) && run_finish<kSimtRows, __nv_bfloat16>(p, stream);
   } else {

@@ -974,3 +974,21 @@ def test_a_loop_without_a_pause():
     check_clean()
     for a, b in zip(*res):
         assert same(a, b)
+
+
+@pytest.mark.parametrize("Hq,T,n_new", [(4, 8, [8, 5, 1]), (7, 4, [4, 3, 0]), (13, 2, None), (31, 1, None)])
+def test_attend_two_row_blocks(Hq, T, n_new):
+    """25 to 32 query rows of 128 elements, a row block that may have none."""
+    run_attend("bf16", 3, Hq, 1, 128, 32, T, [3000, 257, 90], n_new, True, 900, decay=0.5)
+    run_attend("bf16", 3, Hq, 1, 128, 32, T, [700, 8, 0], n_new, "fresh", 901)
+
+
+def test_attend_nan_in_a_new_row_and_two_row_blocks():
+    S, Hq, T, d, lens = 2, 4, 7, 128, [130, 700]
+    poke = [("v", 0, 0, 126, [3, 90]), ("v", 1, 0, 699, [0]), ("v", 1, 0, 694, [127])]
+    hit = torch.zeros(S, Hq, T, d, dtype=torch.bool)
+    for _, s, _, j, elements in poke:
+        for e in elements:
+            hit[s, :, j - (lens[s] - T):, e] = True
+    (o0, z0, w0), (o1, z1, w1) = nan_case("bf16", S, Hq, 1, d, 16, T, lens, None, poke)
+    assert same(o1, torch.where(hit, math.nan, o0)) and same(z1, z0) and same(w1, w0)
