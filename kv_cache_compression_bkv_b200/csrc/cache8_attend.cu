@@ -47,6 +47,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "bkv_device_status.cuh"
 #include "bkv_internal.h"
@@ -623,17 +624,18 @@ __device__ __forceinline__ void values4(uint32_t w, float (&v)[4]) {
   v[0] = lo.x, v[1] = lo.y, v[2] = hi.x, v[3] = hi.y;
 }
 
-constexpr int kSimtRows = 8;
+constexpr int kSimtRows = 8;  // query rows at a time, in weights_simt_kernel
 constexpr int kMaxD = 128;
 
-// The logits of 8 query rows (in shared memory, [8][D]) for one key (its codes
+// The logits of R query rows (in shared memory, [R][D]) for one key (its codes
 // in shared or global memory): two lanes a key, each every second 16-byte chunk;
 // both get the sums.  Loops are kept short: at the sizes this path is for, a
 // tile is over in the time that fetching long unrolled code takes.
+template <int R>
 __device__ __forceinline__ void simt_logits(const uint8_t *row, int D, int half, const float *s_q,
-                                            float (&x)[kSimtRows]) {
+                                            float (&x)[R]) {
 #pragma unroll
-  for (int r = 0; r < kSimtRows; ++r) x[r] = 0.f;
+  for (int r = 0; r < R; ++r) x[r] = 0.f;
 #pragma unroll 1
   for (int i = half * 16; i < D; i += 32) {
     const uint4 c = *reinterpret_cast<const uint4 *>(row + i);
@@ -644,36 +646,40 @@ __device__ __forceinline__ void simt_logits(const uint8_t *row, int D, int half,
       values4(w[j], v);
       const float *q = s_q + i + 4 * j;
 #pragma unroll
-      for (int r = 0; r < kSimtRows; ++r) {
+      for (int r = 0; r < R; ++r) {
         const float4 y = *reinterpret_cast<const float4 *>(q + r * D);
         x[r] = fmaf(v[0], y.x, fmaf(v[1], y.y, fmaf(v[2], y.z, fmaf(v[3], y.w, x[r]))));
       }
     }
   }
 #pragma unroll
-  for (int r = 0; r < kSimtRows; ++r) x[r] += __shfl_xor_sync(0xffffffffu, x[r], 1);
+  for (int r = 0; r < R; ++r) x[r] += __shfl_xor_sync(0xffffffffu, x[r], 1);
 }
 
 // Dynamic shared memory: queries, the warps' merge buffers, and per warp two
 // stages of 16 keys' codes (rows padded by 16 bytes against bank conflicts).
 inline __host__ __device__ int simt_stage_bytes(int D) { return 2 * kSimtKeys * (D + 16) + 16; }
-inline int simt_smem(int D) {
-  return (1 + kSimtWarps) * kSimtRows * D * 4 + kSimtWarps * 2 * simt_stage_bytes(D);
+inline int simt_smem(int D, int R) {
+  return (1 + kSimtWarps) * R * D * 4 + kSimtWarps * 2 * simt_stage_bytes(D);
 }
 
-template <typename T>
+// R: query rows a row block has room for, 2, 4 or 8: the least that holds a KV head's,
+// since empty ones cost as much as others.  f32, one token: 11 sequences of 1271
+// rows, 16/8 heads of 128, 20 us with 2 and 50 with 8; 3 of 24153 rows, 2/1 heads of
+// 96, 19 and 29.
+template <typename T, int R>
 __global__ void __launch_bounds__(kSimtThreads, 2) attend_simt_kernel(const AttendArgs p) {
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(16) float s_p[kSimtWarps][kSimtKeys][kSimtRows];
-  __shared__ float s_m[kSimtWarps][kSimtRows], s_l[kSimtWarps][kSimtRows];
-  __shared__ float s_M[kSimtRows], s_L[kSimtRows];
+  __shared__ __align__(16) float s_p[kSimtWarps][kSimtKeys][R];
+  __shared__ float s_m[kSimtWarps][R], s_l[kSimtWarps][R];
+  __shared__ float s_M[R], s_L[R];
   __shared__ int s_first[kMaxD + 1];  // see write_segment
   const Cache8AttendArgs &a = p.a;
   const int D = a.head_dim;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float *s_q = reinterpret_cast<float *>(smem);
-  float *s_buf = s_q + kSimtRows * D;
-  uint8_t *ring = reinterpret_cast<uint8_t *>(s_buf + kSimtWarps * kSimtRows * D) +
+  float *s_buf = s_q + R * D;
+  uint8_t *ring = reinterpret_cast<uint8_t *>(s_buf + kSimtWarps * R * D) +
                   warp * 2 * simt_stage_bytes(D);
   const int units = a.n_kv_heads * p.row_blocks;
   pdl_wait();
@@ -720,17 +726,17 @@ __global__ void __launch_bounds__(kSimtThreads, 2) attend_simt_kernel(const Atte
     __syncthreads();
   };
   if (a.T > 1) reset_first();
-  float o[kSimtRows][4], m[kSimtRows], l[kSimtRows];
+  float o[R][4], m[R], l[R];
   bool fresh = true;
   int seg_tiles = 0, stage = 0;
   while (cur.at < run) {
     const int kvh = cur.unit / p.row_blocks;
-    const int r0 = (cur.unit - kvh * p.row_blocks) * kSimtRows;
+    const int r0 = (cur.unit - kvh * p.row_blocks) * R;
     const size_t head = static_cast<size_t>(cur.seq) * a.n_kv_heads + kvh;
     if (fresh) {
       fresh = false;
 #pragma unroll 1
-      for (int e = threadIdx.x; e < kSimtRows * D; e += kSimtThreads) {
+      for (int e = threadIdx.x; e < R * D; e += kSimtThreads) {
         const int r = e / D;
         s_q[e] = r0 + r < a.group * cur.q.n
                      ? load_q(static_cast<const T *>(a.q) + q_row(a, cur.seq, kvh, r0 + r) * D + e - r * D)
@@ -738,7 +744,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) attend_simt_kernel(const Atte
       }
       __syncthreads();
 #pragma unroll
-      for (int r = 0; r < kSimtRows; ++r) {
+      for (int r = 0; r < R; ++r) {
         m[r] = -INFINITY;
         l[r] = 0.f;
         o[r][0] = o[r][1] = o[r][2] = o[r][3] = 0.f;
@@ -753,11 +759,11 @@ __global__ void __launch_bounds__(kSimtThreads, 2) attend_simt_kernel(const Atte
       const float *sc = reinterpret_cast<const float *>(st + 2 * kSimtKeys * (D + 16));
       const float f = sc[0] * a.scale * kLog2e, vs = sc[1];
       const int j = j0 + (lane >> 1);
-      float x[kSimtRows];
-      simt_logits(st + (lane >> 1) * (D + 16), D, lane & 1, s_q, x);
+      float x[R];
+      simt_logits<R>(st + (lane >> 1) * (D + 16), D, lane & 1, s_q, x);
       const int seen0 = cur.q.len - cur.q.n + 1;
 #pragma unroll
-      for (int r = 0; r < kSimtRows; ++r) {
+      for (int r = 0; r < R; ++r) {
         x[r] = j < min(seen0 + (r0 + r) / a.group, cur.q.len) ? x[r] * f : -INFINITY;
         if (p.x_cols > r0 + r && (lane & 1) == 0 && j < cur.q.len)
           p.x[(head * p.x_len + j) * p.x_cols + r0 + r] = x[r];
@@ -797,11 +803,16 @@ __global__ void __launch_bounds__(kSimtThreads, 2) attend_simt_kernel(const Atte
       for (int k = 0; k < kSimtKeys; ++k) {  // keys past the end: p = 0, codes 0
         float v[4];
         values4(*reinterpret_cast<const uint32_t *>(vrow + k * (D + 16)), v);
-        const float4 e0 = *reinterpret_cast<const float4 *>(&s_p[warp][k][0]);
-        const float4 e1 = *reinterpret_cast<const float4 *>(&s_p[warp][k][4]);
-        const float e[kSimtRows] = {e0.x, e0.y, e0.z, e0.w, e1.x, e1.y, e1.z, e1.w};
+        alignas(16) float e[R];
+        if constexpr (R == 2) {
+          *reinterpret_cast<float2 *>(e) = *reinterpret_cast<const float2 *>(&s_p[warp][k][0]);
+        } else {
 #pragma unroll
-        for (int r = 0; r < kSimtRows; ++r)
+          for (int r = 0; r < R; r += 4)
+            *reinterpret_cast<float4 *>(e + r) = *reinterpret_cast<const float4 *>(&s_p[warp][k][r]);
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r)
 #pragma unroll
           for (int i = 0; i < 4; ++i) o[r][i] = fmaf(e[r], v[i], o[r][i]);
       }
@@ -811,7 +822,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) attend_simt_kernel(const Atte
     ++seg_tiles;
     if (cur.tile + 1 == cur.q.tiles || cur.at + 1 == run) {
 #pragma unroll
-      for (int r = 0; r < kSimtRows; ++r) {
+      for (int r = 0; r < R; ++r) {
         float t = l[r];
 #pragma unroll
         for (int s = 2; s < 32; s <<= 1) t += __shfl_xor_sync(0xffffffffu, t, s);
@@ -823,16 +834,16 @@ __global__ void __launch_bounds__(kSimtThreads, 2) attend_simt_kernel(const Atte
       }
       __syncthreads();
 #pragma unroll
-      for (int r = 0; r < kSimtRows; ++r) {
+      for (int r = 0; r < R; ++r) {
         float M = -INFINITY;
         for (int k = 0; k < kSimtWarps; ++k) M = fmaxf(M, s_m[k][r]);
         // NaN logits leave no reference, and sums that have to stay
         const float f = m[r] == -INFINITY ? (s_l[warp][r] != s_l[warp][r] ? 1.f : 0.f) : ex2(m[r] - M);
         if (lane * 4 < D)
-          *reinterpret_cast<float4 *>(s_buf + (warp * kSimtRows + r) * D + lane * 4) =
+          *reinterpret_cast<float4 *>(s_buf + (warp * R + r) * D + lane * 4) =
               make_float4(o[r][0] * f, o[r][1] * f, o[r][2] * f, o[r][3] * f);
       }
-      if (threadIdx.x < kSimtRows) {
+      if (threadIdx.x < R) {
         const int r = threadIdx.x;
         float M = -INFINITY, L = 0.f;
         for (int k = 0; k < kSimtWarps; ++k) M = fmaxf(M, s_m[k][r]);
@@ -845,8 +856,8 @@ __global__ void __launch_bounds__(kSimtThreads, 2) attend_simt_kernel(const Atte
       const bool from_start = seg_tiles == cur.tile + 1;
       const bool to_end = cur.tile + 1 == cur.q.tiles;
       seg_tiles = 0;
-      const bool nans = write_segment<kSimtRows, kSimtWarps, kSimtThreads, T>(
-          p, s_buf, kSimtRows * D, s_M, s_L, s_first, cur.seq, cur.unit, cur.q, from_start && to_end,
+      const bool nans = write_segment<R, kSimtWarps, kSimtThreads, T>(
+          p, s_buf, R * D, s_M, s_L, s_first, cur.seq, cur.unit, cur.q, from_start && to_end,
           from_start ? 1 : 0, [D](int r, int d) { return r * D + d; });
       __syncthreads();
       if (nans) reset_first();
@@ -1201,20 +1212,12 @@ bool run_mma(const AttendArgs &p, cudaStream_t s) {
   return launch_programmatic(attend_mma_kernel<D, NT>, dim3(p.ctas), kThreads, Cfg::kSmem, 1, s, p);
 }
 
-template <typename T>
-bool run_simt(const AttendArgs &p, cudaStream_t s) {
-  static int done[64];
-  if (!ensure_smem_limit(attend_simt_kernel<T>, simt_smem(kMaxD), done)) return false;
-  return launch_programmatic(attend_simt_kernel<T>, dim3(p.ctas), kSimtThreads,
-                             simt_smem(p.a.head_dim), 1, s, p);
-}
-
 template <int kRows, typename T>
 bool run_finish(AttendArgs p, cudaStream_t s) {
   const long long segments = static_cast<long long>(p.a.n_seqs) * p.a.n_kv_heads * p.row_blocks;
   // a CTA's beginning costs as much as some rows: as few CTAs as fill the SMs
   const long long rows = segments * kRows;
-  p.join_rows = rows <= 4 * kSms ? 1 : kRows % 64 != 0 || rows <= 32 * kSms ? 8 : 64;
+  p.join_rows = rows <= 4 * kSms ? 1 : kRows % 64 != 0 || rows <= 32 * kSms ? std::min(kRows, 8) : 64;
   long long grid = segments * (kRows / p.join_rows);
   if (p.x_cols > 0) {
     // about four CTAs an SM: the lse of a CTA's rows cost it as much as some
@@ -1227,6 +1230,21 @@ bool run_finish(AttendArgs p, cudaStream_t s) {
   }
   return launch_programmatic(attend_finish_kernel<kRows, T>, dim3(static_cast<unsigned>(grid)),
                              kSimtThreads, 0, 1, s, p);
+}
+
+template <typename T>
+bool run_simt(const AttendArgs &p, int block_rows, cudaStream_t s) {
+  auto run = [&](auto rows) {
+    constexpr int R = decltype(rows)::value;
+    static int done[64];
+    if (!ensure_smem_limit(attend_simt_kernel<T, R>, simt_smem(kMaxD, R), done)) return false;
+    return launch_programmatic(attend_simt_kernel<T, R>, dim3(p.ctas), kSimtThreads,
+                               simt_smem(p.a.head_dim, R), 1, s, p) &&
+           run_finish<R, T>(p, s);
+  };
+  return block_rows == 2   ? run(std::integral_constant<int, 2>())
+         : block_rows == 4 ? run(std::integral_constant<int, 4>())
+                           : run(std::integral_constant<int, 8>());
 }
 
 bool use_mma(int dtype, int head_dim) {
@@ -1265,6 +1283,7 @@ Cache8AttendPlan plan_cache8_attend(int n_seqs, int n_q_heads, int n_kv_heads, i
   // rows with weights (a key's logits are then kept) 109 and 48.
   p.row_tiles = mma && rows > 32 ? (rows <= 128 ? 1 : 2) : 0;
   p.block_rows = p.row_tiles ? 128 * p.row_tiles : 8 * p.nt;
+  if (!mma) p.block_rows = rows <= 2 ? 2 : rows <= 4 ? 4 : 8;
   p.row_blocks = static_cast<int>((rows + p.block_rows - 1) / p.block_rows);
   // Every row block reads all of K and V.  One (up to 256 rows) turns the codes
   // into f16 as it goes, at the cost of converter warps and shared-memory
@@ -1337,9 +1356,9 @@ bkv_status launch_cache8_attend(const Cache8AttendArgs &a, const Cache8AttendPla
     else
       ok = run_mma<64, 4>(p, stream) && run_finish<32, __nv_bfloat16>(p, stream);
   } else if (dtype == BKV_BF16) {
-    ok = run_simt<__nv_bfloat16>(p, stream) && run_finish<kSimtRows, __nv_bfloat16>(p, stream);
+    ok = run_simt<__nv_bfloat16>(p, plan.block_rows, stream);
   } else {
-    ok = run_simt<float>(p, stream) && run_finish<kSimtRows, float>(p, stream);
+    ok = run_simt<float>(p, plan.block_rows, stream);
   }
   if (!ok) return BKV_ERR_CUDA;
   if (a.w_out && plan.x_cols == 0) {

@@ -992,3 +992,23 @@ def test_attend_nan_in_a_new_row_and_two_row_blocks():
             hit[s, :, j - (lens[s] - T):, e] = True
     (o0, z0, w0), (o1, z1, w1) = nan_case("bf16", S, Hq, 1, d, 16, T, lens, None, poke)
     assert same(o1, torch.where(hit, math.nan, o0)) and same(z1, z0) and same(w1, w0)
+
+
+@pytest.mark.parametrize("dtype,d", [("f32", 96), ("bf16", 112), ("f32", 16), ("f32", 128)])
+@pytest.mark.parametrize("Hq,T,n_new", [(1, 1, None), (2, 1, None), (1, 3, [3, 2, 0]), (4, 1, None),
+                                        (2, 2, [2, 1, 2]), (1, 5, [5, 4, 1])])
+def test_attend_few_rows_on_cuda_cores(dtype, d, Hq, T, n_new):
+    """Row blocks of 2, 4 and 8 rows, full and not."""
+    run_attend(dtype, 3, Hq, 1, d, 16, T, [5, 700, 4001], n_new, True, 910, decay=0.5)
+
+
+def test_attend_nan_in_a_new_row_of_few():
+    for Hq, T in ((1, 2), (2, 2), (1, 4)):
+        poke = [("v", 0, 0, 699, [3, 90]), ("v", 1, 0, 128, [0])]
+        lens = [700, 129]
+        hit = torch.zeros(2, Hq, T, 96, dtype=torch.bool)
+        for _, s, _, j, elements in poke:
+            for e in elements:
+                hit[s, :, j - (lens[s] - T):, e] = True
+        (o0, z0, w0), (o1, z1, w1) = nan_case("f32", 2, Hq, 1, 96, 16, T, lens, None, poke)
+        assert same(o1, torch.where(hit, math.nan, o0)) and same(z1, z0) and same(w1, w0)
