@@ -133,9 +133,9 @@ __device__ __forceinline__ void pdl_launch_dependents() {
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // cluster: CTAs per cluster, 1 for none
-template <typename Args>
-bool launch_programmatic(void (*kernel)(const Args), dim3 grid, int threads, size_t smem, int cluster,
-                         cudaStream_t stream, const Args &args) {
+template <typename... Params, typename... Args>
+bool launch_programmatic(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, int cluster,
+                         cudaStream_t stream, const Args &...args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
@@ -149,7 +149,7 @@ bool launch_programmatic(void (*kernel)(const Args), dim3 grid, int threads, siz
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, args) == cudaSuccess) return true;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess) return true;
   cudaGetLastError();
   return false;
 }

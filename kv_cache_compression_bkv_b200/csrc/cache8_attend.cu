@@ -1126,6 +1126,7 @@ template <typename T>
 __global__ void __launch_bounds__(kSimtThreads) weights_simt_kernel(const AttendArgs p) {
   __shared__ __align__(16) float s_q[2][kSimtRows * kMaxD];
   __shared__ float s_z[2][kSimtRows];
+  pdl_wait();
   const Cache8AttendArgs &a = p.a;
   const int D = a.head_dim;
   const size_t head = blockIdx.y;
@@ -1365,11 +1366,9 @@ bkv_status launch_cache8_attend(const Cache8AttendArgs &a, const Cache8AttendPla
     const unsigned heads = static_cast<unsigned>(a.n_seqs) * a.n_kv_heads;
     const unsigned tiles = static_cast<unsigned>((a.max_len + kTile - 1) / kTile);
     if (mma) return launch_weights_tc(p, stream) ? BKV_OK : BKV_ERR_CUDA;
-    if (dtype == BKV_BF16)
-      weights_simt_kernel<__nv_bfloat16><<<dim3(tiles, heads), kSimtThreads, 0, stream>>>(p);
-    else
-      weights_simt_kernel<float><<<dim3(tiles, heads), kSimtThreads, 0, stream>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return BKV_ERR_CUDA;
+    auto kernel = dtype == BKV_BF16 ? weights_simt_kernel<__nv_bfloat16> : weights_simt_kernel<float>;
+    if (!launch_programmatic(kernel, dim3(tiles, heads), kSimtThreads, 0, 1, stream, p))
+      return BKV_ERR_CUDA;
   }
   return BKV_OK;
 }

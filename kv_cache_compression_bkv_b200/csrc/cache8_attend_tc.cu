@@ -175,6 +175,7 @@ __global__ void __launch_bounds__((TcCfg<D, RT, kPre>::kThreads), 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t *s_q = smem, *s_k = s_q + RT * Cfg::kTileBytes, *s_v = s_k + 2 * Cfg::kTileBytes;
 
+  pdl_wait();
   pdl_launch_dependents();
   const Cache8AttendArgs &a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -690,6 +691,8 @@ __device__ __forceinline__ void store32(uint4 *to, uint4 lo, uint4 hi) {
 template <int D>
 __global__ void __launch_bounds__(256) expand_kernel(const AttendArgs p) {
   constexpr int CH = D / 16, NP = 128 * CH / 256;
+  pdl_wait();
+  pdl_launch_dependents();
   const Cache8AttendArgs &a = p.a;
   const size_t head = blockIdx.y;
   const SeqInfo q = seq_info(a, static_cast<int>(head) / a.n_kv_heads);
@@ -791,11 +794,12 @@ bool run_tc(const AttendArgs &p, cudaStream_t s) {
     if (!make_bf16_rows_map(&k_map, p.pre_k, rows, 128, D) ||
         !make_bf16_rows_map(&v_map, p.pre_v, rows, 128, D))
       return false;
-    expand_kernel<D><<<dim3(static_cast<unsigned>(p.pre_len / kTile), heads), 256, 0, s>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return false;
+    if (!launch_programmatic(expand_kernel<D>, dim3(static_cast<unsigned>(p.pre_len / kTile), heads),
+                             256, 0, 1, s, p))
+      return false;
   }
-  attend_tc_kernel<D, RT, kPre><<<p.ctas, Cfg::kThreads, Cfg::kSmem, s>>>(p, k_map, v_map);
-  return cudaGetLastError() == cudaSuccess;
+  return launch_programmatic(attend_tc_kernel<D, RT, kPre>, dim3(p.ctas), Cfg::kThreads, Cfg::kSmem,
+                             1, s, p, k_map, v_map);
 }
 
 template <int D>

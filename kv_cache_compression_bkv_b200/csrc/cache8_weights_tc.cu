@@ -64,6 +64,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   using Cfg = WCfg<D>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ WShared sh;
+  pdl_wait();
   const Cache8AttendArgs &a = p.a;
   const size_t head = blockIdx.y;
   const int seq = static_cast<int>(head) / a.n_kv_heads;
@@ -259,8 +260,7 @@ bool run(const AttendArgs &p, cudaStream_t stream) {
   if (!make_bf16_rows_map(&map, p.a.q, rows, 128, D)) return false;
   const dim3 grid(static_cast<unsigned>((p.a.max_len + kTile - 1) / kTile),
                   static_cast<unsigned>(p.a.n_seqs) * p.a.n_kv_heads);
-  weights_tc_kernel<D><<<grid, kThreads, Cfg::kSmem, stream>>>(p, map);
-  return cudaGetLastError() == cudaSuccess;
+  return launch_programmatic(weights_tc_kernel<D>, grid, kThreads, Cfg::kSmem, 1, stream, p, map);
 }
 
 }  // namespace
