@@ -5,7 +5,9 @@
 // A CTA holds 128 keys of a (sequence, KV head) as the A operand, its codes
 // turned into bf16 once (exact), and walks the query rows 128 at a time: TMA
 // brings them as they are (bf16, one query head's tokens after another's; the
-// sum does not ask for the order), D[128 keys][128 rows] is formed on
+// sum does not ask for the order), 128 tokens of a head, or where T is below 128 as
+// many heads' as follow each other (8 sequences to 8192 rows, 32/8 heads, 10 tokens:
+// 92 us a head at a time, 46 so).  D[128 keys][128 rows] is formed on
 // tcgen05 into one of two TMEM accumulators, and the four epilogue warps of that
 // accumulator, a key a lane, add exp2(s f - z_r): f, the key's factor, is the
 // lane's own, z_r comes from shared memory.  Two CTAs an SM, so that one's
@@ -48,6 +50,7 @@ struct WShared {
   uint64_t full[2], empty[2], tfull[2], tempty[2], drain;
   uint32_t tmem;
   alignas(16) float z[2][128];  // minus the lse of the rows of two tiles
+  int token[2][128];            // and their tokens, INT32_MIN for none
   float sum[128];               // the odd tiles' part of the keys' sums
 };
 
@@ -58,7 +61,8 @@ __device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t codes16) {
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-template <int D>
+// kFlat: T < 128, tiles over the heads' tokens
+template <int D, bool kFlat>
 __global__ void __launch_bounds__(kThreads, 2)
     weights_tc_kernel(const AttendArgs p, const __grid_constant__ CUtensorMap q_map) {
   using Cfg = WCfg<D>;
@@ -78,12 +82,12 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   // tiles of 128 tokens of a query head, from the first whose last token sees
-  // one of these keys
+  // one of these keys; of 128 rows over the heads' tokens for few tokens
   const int seen0 = q.len - q.n + 1;
   const int t_tiles = (q.n + 127) / 128;
   const int tb0 = max(0, (j0 - seen0 + 1) >> 7);
   const int per_head = max(t_tiles - tb0, 0);
-  const int n_tiles = per_head * a.group;
+  const int n_tiles = kFlat ? (a.group * a.T + 127) / 128 : per_head * a.group;
 
   if (warp == kEpiWarps + 1) {
     tmem_alloc(smem_u32(&sh.tmem), 256);
@@ -134,8 +138,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (; it < n_tiles; ++it) {
         const int s = it & 1;
         if (!mbar_wait(smem_u32(&sh.empty[s]), ((it >> 1) & 1) ^ 1, kWhereProd)) break;
-        const int g = it / per_head, t0 = (tb0 + it - g * per_head) * 128;
-        const long long row = (static_cast<long long>(seq) * a.n_q_heads + kvh * a.group + g) * a.T + t0;
+        const int g = kFlat ? 0 : it / per_head;
+        const int r0 = kFlat ? it * 128 : g * a.T + (tb0 + it - g * per_head) * 128;
+        const long long row = (static_cast<long long>(seq) * a.n_q_heads + kvh * a.group) * a.T + r0;
         mbar_arrive_expect_tx(smem_u32(&sh.full[s]), Cfg::kTileBytes);
 #pragma unroll
         for (int h = 0; h < D / 64; ++h)
@@ -177,33 +182,42 @@ __global__ void __launch_bounds__(kThreads, 2)
         __ldg(a.k_scale + head * (a.cap >> p.log2_block) + (min(key, q.len - 1) >> p.log2_block)) *
         (a.scale * kLog2e);
     const float *lse2 = p.lse2 + head * a.group * a.T;
-    auto z_of = [&](int it) {  // minus the lse of this thread's row of tile it
-      const int g = it / per_head, t = (tb0 + it - g * per_head) * 128 + row;
-      return t < q.n ? -__ldg(lse2 + t * a.group + g) : 0.f;
+    float z_next = 0.f;
+    int t_next = INT32_MIN;
+    auto row_of = [&](int it) {  // this thread's row of tile it
+      const int r = it * 128 + row, g = kFlat ? r / a.T : it / per_head;
+      const int t = kFlat ? r - g * a.T : (tb0 + it - g * per_head) * 128 + row;
+      const bool there = g < a.group && t < q.n;
+      z_next = there ? -__ldg(lse2 + t * a.group + g) : 0.f;
+      t_next = there ? t : INT32_MIN;
     };
     bool ok = true;
     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-    float z_next = s < n_tiles ? z_of(s) : 0.f;
+    if (s < n_tiles) row_of(s);
     for (int it = s; it < n_tiles; it += 2) {
       // every warp of the four comes to both barriers in every round, whatever
       // its waits gave: the tile before's rows have been read, this one's are there
       asm volatile("bar.sync %0, 128;" ::"r"(1 + s) : "memory");
       sh.z[s][row] = z_next;
-      if (it + 2 < n_tiles) z_next = z_of(it + 2);
+      sh.token[s][row] = t_next;
+      if (it + 2 < n_tiles) row_of(it + 2);
       asm volatile("bar.sync %0, 128;" ::"r"(1 + s) : "memory");
       if (ok && !mbar_wait_warp(smem_u32(&sh.tfull[s]), (it >> 1) & 1, kWhereEpi)) ok = false;
       if (!ok) continue;
       tc_fence_after();
-      const int g = it / per_head, t0 = (tb0 + it - g * per_head) * 128;
-      // rows t0 + c see the key from c = first on; tokens end at c = last
-      const int first = key - seen0 - t0 + 1, last = q.n - t0;
-      const bool masked = __any_sync(0xffffffffu, first > 0) || last < 128;
+      // the tile's first token, and its columns that may be rows
+      const int t0 = kFlat ? 0 : (tb0 + it % per_head) * 128;
+      const int cols = kFlat ? min(a.group * a.T - it * 128, 128) : min(q.n - t0, 128);
+      const bool masked =
+          __any_sync(0xffffffffu, key >= seen0 + t0) || cols < 128 || (kFlat && q.n < a.T);
+      const int chunks = kFlat ? (cols + 31) / 32 : 4;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
+        if (c >= chunks) break;
         float v[32];
         tmem_ld_32x32b_x32(tmem + 128u * s + lanes + 32u * c, v);
         tmem_ld_wait_regs(v);
-        if (c == 3) {
+        if (c == chunks - 1) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&sh.tempty[s]));
@@ -224,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           for (int i = 0; i < 32; ++i) {
             const int col = 32 * c + i;
             const float e = ex2(fmaf(v[i], f, sh.z[s][col]));
-            sum[i & 1].x += col >= first && col < last ? e : 0.f;
+            sum[i & 1].x += sh.token[s][col] > key - seen0 ? e : 0.f;
           }
         }
       }
@@ -248,25 +262,27 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
-template <int D>
+template <int D, bool kFlat>
 bool run(const AttendArgs &p, cudaStream_t stream) {
   static int done[64];
   using Cfg = WCfg<D>;
   static_assert(Cfg::kSmem + sizeof(WShared) <= 113 * 1024, "two CTAs an SM");
-  if (!ensure_smem_limit(weights_tc_kernel<D>, Cfg::kSmem, done)) return false;
+  if (!ensure_smem_limit(weights_tc_kernel<D, kFlat>, Cfg::kSmem, done)) return false;
   CUtensorMap map;
   const unsigned long long rows =
       static_cast<unsigned long long>(p.a.n_seqs) * p.a.n_q_heads * p.a.T;
   if (!make_bf16_rows_map(&map, p.a.q, rows, 128, D)) return false;
   const dim3 grid(static_cast<unsigned>((p.a.max_len + kTile - 1) / kTile),
                   static_cast<unsigned>(p.a.n_seqs) * p.a.n_kv_heads);
-  return launch_programmatic(weights_tc_kernel<D>, grid, kThreads, Cfg::kSmem, 1, stream, p, map);
+  return launch_programmatic(weights_tc_kernel<D, kFlat>, grid, kThreads, Cfg::kSmem, 1, stream, p, map);
 }
 
 }  // namespace
 
 bool launch_weights_tc(const cache8::AttendArgs &p, cudaStream_t stream) {
-  return p.a.head_dim == 128 ? run<128>(p, stream) : run<64>(p, stream);
+  if (p.a.head_dim == 128)
+    return p.a.T < 128 ? run<128, true>(p, stream) : run<128, false>(p, stream);
+  return p.a.T < 128 ? run<64, true>(p, stream) : run<64, false>(p, stream);
 }
 
 }  // namespace bkv

@@ -1012,3 +1012,12 @@ def test_attend_nan_in_a_new_row_of_few():
                 hit[s, :, j - (lens[s] - T):, e] = True
         (o0, z0, w0), (o1, z1, w1) = nan_case("f32", 2, Hq, 1, 96, 16, T, lens, None, poke)
         assert same(o1, torch.where(hit, math.nan, o0)) and same(z1, z0) and same(w1, w0)
+
+
+@pytest.mark.parametrize("Hq,T,n_new", [
+    (4, 10, [10, 7, 0]), (3, 127, [127, 1, 60]), (3, 128, [128, 128, 5]), (7, 45, None),
+    (40, 1, None), (129, 1, None), (13, 20, [20, 0, 19]), (2, 100, [100, 64, 33])])
+def test_attend_weights_of_many_rows(Hq, T, n_new):
+    """Tiles of query rows that hold several heads' tokens, or end inside one."""
+    run_attend("bf16", 3, Hq, 1, 64, 32, T, [900, 129, 3001], n_new, True, 920, decay=0.5)
+    run_attend("bf16", 3, Hq, 1, 128, 16, T, [T, 200, 40], n_new, "fresh", 921)
