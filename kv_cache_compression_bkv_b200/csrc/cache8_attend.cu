@@ -908,10 +908,12 @@ __device__ __forceinline__ Parts parts_of(const Split &w, int first, int tiles) 
 }
 
 // The weights of keys j0 .. j1 - 1 from their kept logits, kQuad rows at a time.
+// nan_rows: the rows whose lse is NaN, which goes to the keys that they see alone (a
+// hidden key's logit is -infinity).
 template <int kQuad, int kBatch>
 __device__ __forceinline__ void weights_kept(const Cache8AttendArgs &a, const SeqInfo &q,
-                                             const float *xh, int x_cols, const float *s_z, int rows,
-                                             size_t head, int j0, int j1) {
+                                             const float *xh, int x_cols, const float *s_z,
+                                             unsigned nan_rows, int rows, size_t head, int j0, int j1) {
   for (int j = j0 + threadIdx.x; j < j1; j += kBatch * kSimtThreads) {
     float sum[kBatch] = {}, old[kBatch];
 #pragma unroll
@@ -932,10 +934,18 @@ __device__ __forceinline__ void weights_kept(const Cache8AttendArgs &a, const Se
       }
 #pragma unroll
       for (int k = 0; k < kQuad; ++k) {
-        const float z = s_z[r + k];  // infinity past the last row
+        const float z = s_z[r + k];  // infinity past the last row, and where it is NaN
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) sum[u] += ex2(v[u][k] - z);
       }
+    }
+    if (nan_rows != 0) {
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+        for (unsigned left = nan_rows; left != 0; left &= left - 1)
+          if (xh[static_cast<size_t>(min(j + u * kSimtThreads, j1 - 1)) * x_cols + __ffs(left) - 1] !=
+              -INFINITY)
+            sum[u] = __uint_as_float(0x7fc00000u);
     }
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
@@ -966,6 +976,7 @@ template <int kRows, typename T>
 __global__ void __launch_bounds__(kSimtThreads, 5) attend_finish_kernel(const AttendArgs p) {
   __shared__ float s_o[kSimtWarps][kMaxD];
   __shared__ float s_z[kMaxXRows];
+  __shared__ bool s_nan[kMaxXRows];
   const Cache8AttendArgs &a = p.a;
   const int D = a.head_dim;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -991,7 +1002,10 @@ __global__ void __launch_bounds__(kSimtThreads, 5) attend_finish_kernel(const At
     pdl_wait();
     if (none) return;
     const int rows = a.group * q.n;
-    if (threadIdx.x < kMaxXRows && threadIdx.x >= rows) s_z[threadIdx.x] = INFINITY;
+    if (threadIdx.x < kMaxXRows && threadIdx.x >= rows) {
+      s_z[threadIdx.x] = INFINITY;
+      s_nan[threadIdx.x] = false;
+    }
     for (int r = warp; r < rows; r += kSimtWarps) {
       const int unit = (head - seq * a.n_kv_heads) * p.row_blocks + r / kRows, row = r % kRows;
       const Parts x = parts_of(w, before + unit * (q.tiles + w.pad) + w.pad, q.tiles);
@@ -1005,16 +1019,21 @@ __global__ void __launch_bounds__(kSimtThreads, 5) attend_finish_kernel(const At
         const float M = ml.x, L = ml.y;
         z = L > 0.f || L != L ? M + log2f(L) : -INFINITY;
       }
-      if (lane == 0) s_z[r] = z == -INFINITY ? INFINITY : z;  // rows that see nothing add nothing
+      if (lane == 0) {
+        s_z[r] = z > -INFINITY ? z : INFINITY;  // rows that see nothing add nothing
+        s_nan[r] = z != z;
+      }
     }
     __syncthreads();
+    static_assert(kMaxXRows == 32, "a row a lane");
+    const unsigned nan_rows = __ballot_sync(0xffffffffu, s_nan[lane]);
     const int j1 = min(j0 + p.w_keys, q.len);
     const float *xh = p.x + static_cast<size_t>(head) * p.x_len * p.x_cols;
     // keys a thread has in flight: what the loads of one row pair take, or of a quad
     if ((p.x_cols & 3) == 0)
-      weights_kept<4, 2>(a, q, xh, p.x_cols, s_z, rows, head, j0, j1);
+      weights_kept<4, 2>(a, q, xh, p.x_cols, s_z, nan_rows, rows, head, j0, j1);
     else
-      weights_kept<2, 4>(a, q, xh, p.x_cols, s_z, rows, head, j0, j1);
+      weights_kept<2, 4>(a, q, xh, p.x_cols, s_z, nan_rows, rows, head, j0, j1);
     return;
   }
   const int u = blockIdx.x / per_unit;
