@@ -188,7 +188,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int r = it * 128 + row, g = kFlat ? r / a.T : it / per_head;
       const int t = kFlat ? r - g * a.T : (tb0 + it - g * per_head) * 128 + row;
       const bool there = g < a.group && t < q.n;
-      z_next = there ? -__ldg(lse2 + t * a.group + g) : 0.f;
+      const float z = there ? __ldg(lse2 + t * a.group + g) : 0.f;
+      z_next = z == -INFINITY ? z : -z;  // a row of logits of -infinity adds nothing
       t_next = there ? t : INT32_MIN;
     };
     bool ok = true;

@@ -1,5 +1,5 @@
-"""Queries and keys that are not a number: what they may reach of the outputs and of
-the attention weights, on every kernel."""
+"""Queries and keys that are not a number, and rows without a logit above -infinity:
+what they may reach of the outputs and of the attention weights, on every kernel."""
 import math
 
 import pytest
@@ -98,3 +98,42 @@ def test_nan_key_reaches_only_the_tokens_that_see_it(i):
     for s, L in enumerate(lens):
         assert bool(w[s, H - 1, :L].isnan().all())   # the last token sees every key
         assert same(w[s, :H - 1], want[2][s, :H - 1])
+
+
+@pytest.mark.parametrize("i", range(len(CASES)))
+def test_row_of_logits_below_the_range_adds_no_weight(i):
+    """A token whose every logit lies below f32's range counts as one that sees
+    nothing: zeros, an lse of -infinity, and nothing in the weights."""
+    dtype, Hq, H, d, block, T, lens, n_new = CASES[i]
+    S, G, cap = len(lens), Hq // H, (max(lens) + block - 1) // block * block
+    rc = ref.Cache(S, H, cap, d, block)
+    x = torch.randn(2, S, H, cap, d, generator=gen(680 + i))
+    x[0, ..., 0] = -1.0e12                           # every key's first element
+    rc.append([cap] * S, [cap] * S, x[0], x[1])
+    dev = Dev(S, Hq, H, cap, d, block, dtype)
+    dev.fill(rc, lens)
+    q = torch.randn(S, Hq, T, d, generator=gen(690 + i)).to(DT[dtype])
+    q[..., 0] = 0.0
+    hit = torch.zeros(S, Hq, T, dtype=torch.bool)
+    for s in range(S):
+        n = n_new[s] if n_new else T
+        h, t = (s + 1) % Hq, n - 1                   # the token that sees every key
+        q[s, h, t] = 0.0
+        q[s, h, t, 0] = 1.0e30                       # logits of -1e42 / sqrt(d)
+        hit[s, h, t] = True
+    out, lse, w = attend(dev, q, lens, n_new, T)
+    assert bool((out[hit] == 0).all()) and bool((lse[hit] == -math.inf).all())
+    for s, L in enumerate(lens):
+        n = n_new[s] if n_new else T
+        for h in range(H):
+            # every other row's probabilities sum to one
+            rows = int((~hit[s, h * G:(h + 1) * G, :n]).sum())
+            total = float(w[s, h, :L].sum())
+            assert math.isfinite(total)
+            # each is off by its logits' rounding alone: twice (d + 4) 2^-22 times the
+            # largest sum of magnitudes, and 2^-19, as derived in attend_bounds; the
+            # large elements of K meet zeros there, and cost nothing
+            mag = (q[s, h * G:(h + 1) * G, :n].double().abs()[..., 1:] @
+                   rc.values("k", s, h, L)[:, 1:].abs().T).amax() / math.sqrt(d)
+            tol = rows * (2 * (d + 4) * 2.0 ** -22 * float(mag) + 2.0 ** -19 + (L + G * n) * ref.U_F32)
+            assert abs(total - rows) <= tol, (s, h, total, rows, tol)
