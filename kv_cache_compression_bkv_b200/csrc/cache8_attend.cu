@@ -30,10 +30,12 @@
 //   The f16 product, not the 8-bit one: the e4m3 mma.sync took longer here (one
 // ragged batch 165 us against 147), and tcgen05 pads 8 rows to 128.
 //   The probabilities are rounded to f16 (2^-11, summed in f32 before that),
-// multiplied by the block's V scale over the largest one met so far.
-//   The softmax reference of a row is put 7 (in log2) under the largest logit and
-// moves only when a logit passes it by 15, so that probabilities stay under
-// 2^15: one vote per tile instead of a max over lanes.
+// multiplied by the block's V scale under a power of two of the row's own, so that
+// neither keys a row does not see nor such as get no probability cost it bits.
+//   The softmax reference of a row is put 7 (in log2) under the largest logit, that
+// of its outputs 7 under the largest logit plus V exponent, and they move only when
+// one of these is passed by 15, so that the f16 operands stay under 2^15: one vote
+// per tile instead of a max over lanes.
 //   Measured: 32 sequences of 517 .. 16384 rows, 32/8 heads of 128, one token, in
 // 109 us, 5.1 TB/s of codes, 79% of the measured copy rate.  What is left is the
 // GPU's memory channels, which serve its parts unevenly (CTAs of equal runs end
@@ -332,8 +334,9 @@ __global__ void __launch_bounds__(kThreads, 2) attend_mma_kernel(const AttendArg
   uint2 qf[NT == 1 ? KS : 1];
   float rs[NT][2];
   float o[MT][NT][4];
-  float m[NT][2], l[NT][2];
-  float vref = 0.f, ivref = 0.f;
+  // rows 8 nt + 2 c + i: a softmax reference m (log2) with the sum l of the
+  // probabilities under it, and outputs in units of 2^-lh under it (lh: a whole number)
+  float m[NT][2], l[NT][2], lh[NT][2];
   int kvh = 0, r0 = 0, seen0 = 0;
   bool fresh = true;
   int stage = 0, seg_tiles = 0;
@@ -372,12 +375,12 @@ __global__ void __launch_bounds__(kThreads, 2) attend_mma_kernel(const AttendArg
       for (int nt = 0; nt < NT; ++nt) {
         m[nt][0] = m[nt][1] = -INFINITY;
         l[nt][0] = l[nt][1] = 0.f;
+        lh[nt][0] = lh[nt][1] = 0.f;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int i = 0; i < 4; ++i) o[mt][nt][i] = 0.f;
       }
-      vref = ivref = 0.f;
     }
     // the stage read in the last round is free
     if (load.at < run) issue(stage == 0 ? Cfg::kStages - 1 : stage - 1);
@@ -390,7 +393,9 @@ __global__ void __launch_bounds__(kThreads, 2) attend_mma_kernel(const AttendArg
       const uint8_t *st = ring_ptr + stage * Cfg::kStageBytes;
       const float4 sc = *reinterpret_cast<const float4 *>(st + 2 * kKeys * D);
       const float ks[2] = {sc.x, sc.z};
-      const float vs[2] = {sc.y, there > 16 ? sc.w : 0.f};
+      // the V scales' exponents; a block that is not there has the lowest
+      const float lv[2] = {static_cast<float>(exp_of(sc.y)),
+                           there > 16 ? static_cast<float>(exp_of(sc.w)) : -127.f};
       // ---- logits, 16 keys (an m-tile) at a time; the rows are in the order
       // that leaves lane c the probabilities of keys 4c .. 4c+3 when transposed
       const bool masked = j0 + kKeys > seen0 + r0 / a.group;
@@ -437,8 +442,9 @@ __global__ void __launch_bounds__(kThreads, 2) attend_mma_kernel(const AttendArg
             if (j + 2 >= v0) y[2] = -INFINITY;
             if (j + 2 >= v1) y[3] = -INFINITY;
           }
-          grow |= fmaxf(y[0], y[2]) > m[nt][0] + 15.f;
-          grow |= fmaxf(y[1], y[3]) > m[nt][1] + 15.f;
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            grow |= fmaxf(y[i], y[i + 2]) > m[nt][i] + (15.f - fmaxf(lv[t] + lh[nt][i], 0.f));
           if (p.x_cols > 0) {
             const int col = r0 + nt * 8 + 2 * c;
             if (col < p.x_cols && t * 16 < there) {
@@ -450,21 +456,24 @@ __global__ void __launch_bounds__(kThreads, 2) attend_mma_kernel(const AttendArg
           }
         }
       }
-      // ---- a row's reference: 7 (in log2) under the largest logit when it was
-      // set, so that the probabilities are at most 2^15
+      // ---- a row's references: 7 (in log2) under the largest logit, and under the
+      // largest logit plus V exponent, when they were set (the second to a whole
+      // number), so that the probabilities and what the outputs add are at most 2^15
       if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            float t = fmaxf(fmaxf(x[0][nt][i], x[0][nt][i + 2]), fmaxf(x[1][nt][i], x[1][nt][i + 2]));
-            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
-            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
-            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16)) - 7.f;
-            if (t > m[nt][i]) {
-              const float f = ex2(m[nt][i] - t);
-              m[nt][i] = t;
-              l[nt][i] *= f;
+            const float t0 = fmaxf(x[0][nt][i], x[0][nt][i + 2]);
+            const float t1 = fmaxf(x[1][nt][i], x[1][nt][i + 2]);
+            float t = fmaxf(t0, t1), u = fmaxf(t0 + lv[0], t1 + lv[1]);
+#pragma unroll
+            for (int s = 4; s < 32; s <<= 1) {
+              t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, s));
+              u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, s));
+            }
+            float f;
+            if (move_reference(t - 7.f, u - 7.f, m[nt][i], l[nt][i], lh[nt][i], f)) {
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt) {
                 o[mt][nt][i] *= f;
@@ -473,18 +482,6 @@ __global__ void __launch_bounds__(kThreads, 2) attend_mma_kernel(const AttendArg
             }
           }
       }
-      const float vmax = fmaxf(vs[0], vs[1]);
-      if (vmax > vref) {  // the outputs are held in units of the largest V scale
-        const float f = vref / vmax;
-        vref = vmax;
-        ivref = 1.f / vmax;
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[mt][nt][i] *= f;
-      }
       uint32_t b[NT][2][2];  // B fragments of the two k-steps: keys 4c .. 4c+3 of each m-tile
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -492,13 +489,13 @@ __global__ void __launch_bounds__(kThreads, 2) attend_mma_kernel(const AttendArg
         const float m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          const float vr = vs[t] * ivref;
+          const float v0 = v_factor(lv[t], lh[nt][0]), v1 = v_factor(lv[t], lh[nt][1]);
           const float p0 = ex2(x[t][nt][0] - m0), p1 = ex2(x[t][nt][1] - m1);
           const float p2 = ex2(x[t][nt][2] - m0), p3 = ex2(x[t][nt][3] - m1);
           l[nt][0] += p0 + p2;
           l[nt][1] += p1 + p3;
-          b[nt][t][0] = transpose8x8(as_u32(__floats2half2_rn(p0 * vr, p1 * vr)));
-          b[nt][t][1] = transpose8x8(as_u32(__floats2half2_rn(p2 * vr, p3 * vr)));
+          b[nt][t][0] = transpose8x8(as_u32(__floats2half2_rn(p0 * v0, p1 * v1)));
+          b[nt][t][1] = transpose8x8(as_u32(__floats2half2_rn(p2 * v0, p3 * v1)));
         }
       }
       const int hidden = hidden_from(cur.q);
@@ -555,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_mma_kernel(const AttendArg
           }
         }
       __syncthreads();
-      // this warp's factor to the CTA's reference, with its V scale
+      // this warp's factor to the CTA's reference and the values' own units
       float f[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -566,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_mma_kernel(const AttendArg
 #pragma unroll
           for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w * Cfg::kRows + r]);
           f[nt][i] = (m[nt][i] != -INFINITY ? ex2(m[nt][i] - M)
-                                            : lsum[nt][i] != lsum[nt][i] ? 1.f : 0.f) * vref;
+                                            : lsum[nt][i] != lsum[nt][i] ? 1.f : 0.f) * ex2(-lh[nt][i]);
           if (warp == 0 && g == 0) {
             float L = 0.f;
 #pragma unroll

@@ -51,6 +51,31 @@ __device__ __forceinline__ bool elect_one() {
   return one != 0;
 }
 
+// ----------------------------------------------------- a row's two references
+//
+// A row sums its probabilities p = 2^(x - m) in l, and its outputs from f16 operands
+// p 2^(lv + lh) times codes, with lv the exponent of the key's V scale and lh a whole
+// number of the row's own: its outputs are in units of 2^(m - lh).
+
+// Moves them up to t (for p) and u (for the operands) where they lie below: true if
+// so, and then f is what the outputs are multiplied by.  Stays where t is -infinity or
+// NaN.
+__device__ __forceinline__ bool move_reference(float t, float u, float &m, float &l, float &lh,
+                                               float &f) {
+  if (!(t > m || u > m - lh)) return false;
+  const float to = fmaxf(m, t), up = to - m;       // from -infinity: infinity
+  const float h = floorf(fminf(to - u, lh + up));  // to - h: u, or the old one, and 1 above at most
+  const float g = ex2(-up);
+  f = m == -INFINITY ? 0.f : ex2(h - lh - up);
+  l *= g;
+  m = to;
+  lh = h;
+  return true;
+}
+
+// 2^(lv + lh), bounded so that a probability of zero times it is zero.
+__device__ __forceinline__ float v_factor(float lv, float lh) { return ex2(fminf(lv + lh, 126.f)); }
+
 // ------------------------------------------------------------ the work split
 
 struct SeqInfo {
