@@ -373,13 +373,10 @@ bkv_status bkv_cache8_append(const bkv_cache8_desc *desc, void *k8, void *v8,
  *   weights_in  device, like weights_out, optional (NULL: zeros); may be
  *               weights_out itself
  * Products are summed in f32, f32 queries on the CUDA cores.  On the tensor
- * cores the operands are f16 under powers of two: queries exact but for elements
- * 2^-32 under the largest of their row (of 32 rows, where a KV head has more);
- * codes exact for up to 32 rows, and above that but for parts under 2^-24 of the
- * largest scale, K's among 128 rows and V's among those that a CTA takes;
- * probabilities rounded, up to 32 rows under their V scale (2^-11, down to 2^-31
- * of the largest such product of the row), above that alone (2^-11, down to 2^-25
- * of the largest).  The weights and lse come from f32.  A logit above f32's range
+ * cores the operands are f16: codes exact; queries under a power of two of their
+ * row's own, exact but for elements 2^-32 under its largest; probabilities times
+ * their V scale under another, rounded (2^-11, down to 2^-31 of the row's largest
+ * such product).  The weights and lse come from f32.  A logit above f32's range
  * counts as NaN, one below it as that of a key that is not seen.
  * A NaN in K makes the outputs and lse of the tokens that see its row NaN, and
  * what they add to the weights; a NaN in V only its element of their outputs.

@@ -1272,16 +1272,14 @@ bool use_mma(int dtype, int head_dim) {
 
 namespace {
 struct PreSections {
-  size_t k, v, k_scale, v_scale, bytes;
+  size_t k, v, bytes;
 };
 PreSections pre_sections(int n_seqs, int n_kv_heads, int head_dim, long long max_len) {
   const size_t heads = static_cast<size_t>(n_seqs) * n_kv_heads, len = align_up(max_len, kTile);
   PreSections x;
   x.k = 0;
   x.v = align_up(heads * len * head_dim * 2, kAlign);
-  x.k_scale = 2 * x.v;
-  x.v_scale = x.k_scale + align_up(heads * (len / kTile) * 4, kAlign);
-  x.bytes = x.v_scale + align_up(heads * 4, kAlign);
+  x.bytes = 2 * x.v;
   return x;
 }
 }  // namespace
@@ -1349,8 +1347,6 @@ bkv_status launch_cache8_attend(const Cache8AttendArgs &a, const Cache8AttendPla
         align_up(reinterpret_cast<uintptr_t>(w + plan.pre_off), kAlign));
     p.pre_k = reinterpret_cast<uint16_t *>(e + x.k);
     p.pre_v = reinterpret_cast<uint16_t *>(e + x.v);
-    p.pre_k_scale = reinterpret_cast<float *>(e + x.k_scale);
-    p.pre_v_scale = reinterpret_cast<float *>(e + x.v_scale);
   }
   const bool mma = use_mma(dtype, a.head_dim);
   bool ok;

@@ -28,10 +28,9 @@ struct AttendArgs {
   float *part;
   float *lse2;       // [n_seqs][n_kv_heads][group * T], log2 units
   float *x;          // [n_seqs][n_kv_heads][x_len][x_cols], log2 units
-  // K and V as f16 tiles, [n_seqs][n_kv_heads][pre_len][head_dim], with a K
-  // scale per 128 keys and a V scale per head; NULL: the codes are read
+  // K's and V's codes as f16 tiles, [n_seqs][n_kv_heads][pre_len][head_dim]; NULL:
+  // the codes are read
   uint16_t *pre_k, *pre_v;
-  float *pre_k_scale, *pre_v_scale;
   long long pre_len;
 };
 

@@ -8,19 +8,21 @@
 //   O += P V    P f16 in TMEM over the columns S was read from, V f16 in shared
 //               memory as it is cached (keys x elements: MN-major)
 // e4m3 codes are exact in f16, so converter warps turn each tile's codes into
-// f16 once for all the CTA's rows, multiplied by the power of two between the
-// block's scale and the tile's largest (K) or the run's largest (V): exact down
-// to 2^-24 under it.  The f8f6f4 product would take the codes as they are, but
-// then the probabilities have to be split into 8-bit parts to keep f16's 11
-// bits, which costs the softmax warps more than the conversion costs others.
+// f16 once for all the CTA's rows.  The softmax warps multiply S by K's scales, 16
+// columns at a time, and the probabilities by V's under a power of two of the
+// row's own (move_reference), so no key costs another one's row any bits.  The
+// f8f6f4 product would take the codes as they are, but then the probabilities have
+// to be split into 8-bit parts to keep f16's 11 bits, which costs the softmax warps
+// more than the conversion costs others.
 //
 // Warps: 4 per row tile do the softmax, one thread a row (TMEM lane); the
 // converters load codes into registers ahead of need, half of them K, half V;
 // one warp issues the MMAs.  With two row tiles the tensor cores work on one
 // while the other's softmax runs; with one, S is double-buffered.
-// A row's reference is set 7 (in log2) under the largest logit and moves only
-// when a 32-column sum of probabilities passes 2^15, so the common path takes
-// no maxima; moving it rescales O in TMEM, after the MMAs that are under way.
+// A row's references are set 7 (in log2) under the largest logit (and logit plus V
+// exponent) and move only when a 16-column sum of probabilities (times their V
+// scale) passes 2^15, so the common path takes no maxima; moving them rescales O
+// in TMEM, after the MMAs that are under way.
 //
 // Bound by the tensor cores and exp (a 256 x 128 tile: 2 x 2 x 512 cycles of
 // MMA, 32768 exps at 16 a cycle, each 55% of the time in a long run); one row
@@ -146,18 +148,16 @@ struct TcShared {
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], drain;
   uint32_t tmem;
-  float k_scale[4];   // of the last tiles
-  float v_scale[4];   // of the last parts
 };
 
-// 16 codes as f16, times a power of two: elements 0..7 and 8..15.
-__device__ __forceinline__ void convert16(uint4 c, __half2 f, uint4 *lo, uint4 *hi) {
+// 16 codes as f16: elements 0..7 and 8..15.
+__device__ __forceinline__ void convert16(uint4 c, uint4 *lo, uint4 *hi) {
   const uint32_t w[4] = {c.x, c.y, c.z, c.w};
   uint32_t h[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    h[2 * i] = as_u32(__hmul2(as_half2(e4m3x2_to_f16x2(w[i])), f));
-    h[2 * i + 1] = as_u32(__hmul2(as_half2(e4m3x2_to_f16x2(w[i] >> 16)), f));
+    h[2 * i] = e4m3x2_to_f16x2(w[i]);
+    h[2 * i + 1] = e4m3x2_to_f16x2(w[i] >> 16);
   }
   *lo = make_uint4(h[0], h[1], h[2], h[3]);
   *hi = make_uint4(h[4], h[5], h[6], h[7]);
@@ -346,7 +346,6 @@ __global__ void __launch_bounds__((TcCfg<D, RT, kPre>::kThreads), 1)
     int lj = -1, cj = -1;  // tiles within the parts being loaded and converted
     bool more = true;
     uint4 c[NB][NP];
-    int ex[NB];  // lanes 0..7: exponent of the scale of keys 16 lane .. of the tile
     auto load = [&](int b) {
       if ((b & 1) == 0) {
         ++lj;
@@ -372,14 +371,10 @@ __global__ void __launch_bounds__((TcCfg<D, RT, kPre>::kThreads), 1)
           if (i * kThr < left) c[b][i] = __ldcs(src + i * kThr);
         }
       }
-      ex[b] = -127;
-      if (lane < 8 && j0 + lane * 16 < lx.len)
-        ex[b] = exp_of(__ldg((b & 1 ? a.v_scale : a.k_scale) + head * (a.cap >> p.log2_block) +
-                             ((j0 + lane * 16) >> p.log2_block)));
     };
 #pragma unroll
     for (int b = 0; b < NB; ++b) load(b);
-    int t = -1, seg = -1, ref = -127;
+    int t = -1;
     bool ok = true;
     while (ok) {
 #pragma unroll
@@ -391,17 +386,6 @@ __global__ void __launch_bounds__((TcCfg<D, RT, kPre>::kThreads), 1)
           while (ok && cj >= x.live) {
             ok = parts.next(p, w, units, &x);
             cj = 0;
-            if (!ok || x.live == 0) continue;
-            // a new part: its largest V scale
-            const float *sc = a.v_scale + (static_cast<size_t>(x.seq) * a.n_kv_heads + x.kvh) *
-                                              (a.cap >> p.log2_block);
-            const int b1 = (min((x.tile0 + x.live) * kTile, x.len) - 1) >> p.log2_block;
-            ref = -127;
-            for (int i = ((x.tile0 * kTile) >> p.log2_block) + lane; i <= b1; i += 32)
-              ref = max(ref, exp_of(__ldg(sc + i)));
-            ref = __reduce_max_sync(0xffffffffu, ref);
-            ++seg;
-            if (tid == 0) sh.v_scale[seg & 3] = pow2f(max(ref, -126));
           }
           if (!ok) break;
         }
@@ -409,9 +393,6 @@ __global__ void __launch_bounds__((TcCfg<D, RT, kPre>::kThreads), 1)
         if (!(ok = mbar_wait_warp(smem_u32(is_v ? &sh.v_empty[stage] : &sh.k_empty[stage]),
                                   ((t >> 1) & 1) ^ 1, kWhereConv)))
           break;
-        const int top = is_v ? ref : __reduce_max_sync(0xffffffffu, ex[b]);
-        // lanes 0..7: the factor of keys 16 lane ..
-        const uint32_t factor = as_u32(__float2half2_rn(pow2f(max(ex[b] - top, -24))));
         uint8_t *tile = (is_v ? s_v : s_k) + stage * Cfg::kTileBytes;
         const int hidden = x.len - x.n + 1 - (x.tile0 + cj) * kTile;  // row of the tile
         if (is_v && x.n > 1 && hidden < kTile) {
@@ -421,18 +402,14 @@ __global__ void __launch_bounds__((TcCfg<D, RT, kPre>::kThreads), 1)
         }
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-          const __half2 f =
-              as_half2(__shfl_sync(0xffffffffu, factor, ((row0 + i * kStep) >> 4) & 7));
-          if (128 * CH % kThr == 0 || i < NP - 1 || row0 + i * kStep < 128)
-          {
+          if (128 * CH % kThr == 0 || i < NP - 1 || row0 + i * kStep < 128) {
             uint4 lo, hi;
-            convert16(c[b][i], f, &lo, &hi);
+            convert16(c[b][i], &lo, &hi);
             const uint32_t to = (to0 ^ (kStep % 8 != 0 && (i & 1) ? swap4 : 0u)) + i * kStep * 128;
             *reinterpret_cast<uint4 *>(tile + to) = flip ? hi : lo;
             *reinterpret_cast<uint4 *>(tile + (to ^ 16u)) = flip ? lo : hi;
           }
         }
-        if (!is_v && tid == 0) sh.k_scale[t & 3] = pow2f(max(top, -126));
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(is_v ? &sh.v_full[stage] : &sh.k_full[stage]));
@@ -445,7 +422,7 @@ __global__ void __launch_bounds__((TcCfg<D, RT, kPre>::kThreads), 1)
     const int trow = (warp & 3) * 32 + lane;    // row in it, TMEM lane
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     Part x;
-    int t = 0, seg = 0;
+    int t = 0;
     bool ok = true;
     // Waits, once, until tile t - 1 of the part (its tile j - 1) is in O.  A phase
     // must not pass unwaited, or its parity would be taken for the next one's:
@@ -465,9 +442,10 @@ __global__ void __launch_bounds__((TcCfg<D, RT, kPre>::kThreads), 1)
       const int sees = x.len - x.n + 1 + r / a.group;  // keys this row sees
       const bool warp_rows = x.r0 + x_tile * 128 + (warp & 3) * 32 < x.rows;
       const bool whole = x.from_start && x.to_end;
-      float ref = -INFINITY, l = 0.f, vscale = 0.f;
+      float ref = -INFINITY, l = 0.f, lh = 0.f;
       if (x.live > 0) {
-        // queries: f16 under a power of two per 32 rows, largest in [2^14, 2^15)
+        float q_factor;  // of the logits
+        // queries: f16 under a power of two per row, largest in [2^14, 2^15)
         // (read twice: once in registers costs spills in the loop below, 112 -> 119 us
         // for 8 sequences to 8192 rows of 32/8 heads, 64 tokens)
         {
@@ -485,7 +463,6 @@ __global__ void __launch_bounds__((TcCfg<D, RT, kPre>::kThreads), 1)
               if (hi < 0x7f800000u) amax = max(amax, hi);
             }
           }
-          amax = __reduce_max_sync(0xffffffffu, amax);
           const int e = amax == 0 ? 0 : max(static_cast<int>(amax >> 23) - 127, -112);
           const float up = pow2f(14 - e);
           uint8_t *tile = s_q + x_tile * Cfg::kTileBytes;
@@ -501,26 +478,31 @@ __global__ void __launch_bounds__((TcCfg<D, RT, kPre>::kThreads), 1)
             *reinterpret_cast<uint4 *>(tile + (i >> 3) * kHalf + sw128_offset(trow, i & 7)) =
                 make_uint4(h[0], h[1], h[2], h[3]);
           }
-          vscale = pow2f(e - 14) * (a.scale * kLog2e);  // for now: the logits' factor
+          q_factor = pow2f(e - 14) * (a.scale * kLog2e);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&sh.q_full[x_tile]));
         }
-        const float q_factor = vscale;
-        const size_t head = static_cast<size_t>(x.seq) * a.n_kv_heads + x.kvh;
+        const size_t block0 = (static_cast<size_t>(x.seq) * a.n_kv_heads + x.kvh) * (a.cap >> p.log2_block);
         for (int j = 0; j < x.live; ++j, ++t) {
           const int buf = RT == 2 ? x_tile : t & 1;
-          float ks = 0.f;
-          if (kPre) ks = __ldg(p.pre_k_scale + head * (p.pre_len / kTile) + x.tile0 + j);
+          // lanes 8 i + b: K's scale and V's exponent for columns 16 b .. 16 b + 15
+          float ks = 0.f, lv = -127.f;
+          const int j0 = (x.tile0 + j) * kTile, jb = j0 + (lane & 7) * 16;
+          if (jb < x.len) {
+            ks = __ldg(a.k_scale + block0 + (jb >> p.log2_block));
+            lv = static_cast<float>(exp_of(__ldg(a.v_scale + block0 + (jb >> p.log2_block))));
+          }
           if (!(ok = mbar_wait_warp(smem_u32(&sh.s_full[buf]), RT == 2 ? t & 1 : (t >> 1) & 1,
                                     kWhereSoft)))
             break;
           tc_fence_after();
           if (warp_rows) {
             const uint32_t s_addr = s_col(buf) + lanes;
-            // not zero: -infinity has to stay
-            const float f = fmaxf(q_factor * (kPre ? ks : sh.k_scale[t & 3]), 1.17549435e-38f);
-            const int j0 = (x.tile0 + j) * kTile;
+            // the logits' factor in columns 16 b ..: not zero, as -infinity has to stay
+            auto k_factor = [&](int b) {
+              return fmaxf(q_factor * __shfl_sync(0xffffffffu, ks, b), 1.17549435e-38f);
+            };
             const int nvis = sees - j0;
             const bool masked = __any_sync(0xffffffffu, nvis < kTile);
             if (masked) {  // hidden keys' logits become -infinity where they stand
@@ -544,22 +526,24 @@ __global__ void __launch_bounds__((TcCfg<D, RT, kPre>::kThreads), 1)
             // first tile begins with the move
             for (int round = j > 0 ? 0 : 1;; ++round) {
               if (round > 0) {
-                float top = -INFINITY;
+                float top = -INFINITY, top_v = -INFINITY;
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
                   float v[32];
                   tmem_ld_32x32b_x32(s_addr + 32u * c, v);
                   tmem_ld_wait_regs(v);
 #pragma unroll
-                  for (int i = 0; i < 32; ++i) top = fmaxf(top, v[i]);
+                  for (int b = 0; b < 2; ++b) {
+                    float m = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) m = fmaxf(m, v[16 * b + i]);
+                    m *= k_factor(2 * c + b);
+                    top = fmaxf(top, m);
+                    top_v = fmaxf(top_v, m + __shfl_sync(0xffffffffu, lv, 2 * c + b));
+                  }
                 }
-                top = top * f - 7.f;
-                float corr = 1.f;
-                if (!fine && top > ref) {
-                  corr = ref == -INFINITY ? 0.f : ex2(ref - top);
-                  ref = top;
-                  l *= corr;
-                }
+                float corr = 1.f, f;
+                if (!fine && move_reference(top - 7.f, top_v - 7.f, ref, l, lh, f)) corr = f;
                 __syncwarp();
                 if (j > 0) {
                   // O, once the MMAs of the tile before have added to it
@@ -578,7 +562,7 @@ __global__ void __launch_bounds__((TcCfg<D, RT, kPre>::kThreads), 1)
                 }
               }
               const float ru = ref == -INFINITY ? 0.f : ref;
-              const float2 f2 = make_float2(f, f), r2 = make_float2(-ru, -ru);
+              const float2 r2 = make_float2(-ru, -ru);
               fine = true;
               sum = 0.f;
               float v[2][32];  // the next columns are on their way while these are used
@@ -587,24 +571,32 @@ __global__ void __launch_bounds__((TcCfg<D, RT, kPre>::kThreads), 1)
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
                 if (c < 3) tmem_ld_32x32b_x32(s_addr + 32u * (c + 1), v[(c + 1) & 1]);
-                float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  const float2 y =
-                      __ffma2_rn(make_float2(v[c & 1][2 * i], v[c & 1][2 * i + 1]), f2, r2);
-                  const float2 e = make_float2(ex2(y.x), ex2(y.y));
-                  part[i & 1] = __fadd2_rn(part[i & 1], e);
-                  ph[c * 16 + i] = as_u32(__floats2half2_rn(e.x, e.y));
+                for (int b = 0; b < 2; ++b) {
+                  const float f = k_factor(2 * c + b);
+                  const float g = v_factor(__shfl_sync(0xffffffffu, lv, 2 * c + b), lh);
+                  const float2 f2 = make_float2(f, f), g2 = make_float2(g, g);
+                  float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                  for (int i = 8 * b; i < 8 * b + 8; ++i) {
+                    const float2 y =
+                        __ffma2_rn(make_float2(v[c & 1][2 * i], v[c & 1][2 * i + 1]), f2, r2);
+                    const float2 e = make_float2(ex2(y.x), ex2(y.y));
+                    part[i & 1] = __fadd2_rn(part[i & 1], e);
+                    const float2 h = __fmul2_rn(e, g2);
+                    ph[c * 16 + i] = as_u32(__floats2half2_rn(h.x, h.y));
+                  }
+                  const float2 both = __fadd2_rn(part[0], part[1]);
+                  const float s16 = both.x + both.y;
+                  fine &= s16 <= 32768.f && s16 * g <= 32768.f;
+                  sum += s16;
                 }
-                const float2 both = __fadd2_rn(part[0], part[1]);
-                fine &= both.x + both.y <= 32768.f;
-                sum += both.x + both.y;
                 if (c < 3) tmem_ld_wait_regs(v[(c + 1) & 1]);
               }
               if (round > 0 || !__any_sync(0xffffffffu, !fine)) break;
             }
             if (!ok) break;
-            // still above the bound under its own largest logit: not a number
+            // still above a bound under its own largest logits: not a number
             if (!fine) sum = __uint_as_float(0x7fc00000u);
             l += sum;
             __syncwarp();  // tcgen05 loads and stores are the whole warp's
@@ -620,15 +612,14 @@ __global__ void __launch_bounds__((TcCfg<D, RT, kPre>::kThreads), 1)
         if (!ok) break;
         if (!(ok = mbar_wait_warp(smem_u32(&sh.pv_done[x_tile]), (t - 1) & 1, kWhereOut))) break;
         tc_fence_after();
-        vscale = kPre ? __ldg(p.pre_v_scale + head) : sh.v_scale[seg & 3];
-        ++seg;
       }
       if (!warp_rows) continue;
       // ---- the part's end: a whole segment goes out, a part to its slot
       float *part = p.part + (static_cast<size_t>(blockIdx.x) * 2 + (x.from_start ? 1 : 0)) *
                                  (kRows * (2 + D));
       const int pr = x_tile * 128 + trow;
-      const float mul = !whole ? vscale : l > 0.f || l != l ? vscale / l : 0.f;
+      const float unit = ex2(-lh);  // of the outputs
+      const float mul = !whole ? unit : l > 0.f || l != l ? unit / l : 0.f;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         float v[32];
@@ -685,9 +676,8 @@ __device__ __forceinline__ void store32(uint4 *to, uint4 lo, uint4 hi) {
 }
 
 // K and V of every sequence as f16 tiles of 128 keys (rows past the end zeros),
-// for calls whose row blocks would each convert them again: codes times the
-// power of two between the block's scale and the tile's largest (K) or the
-// head's largest (V).  A copy: 1 byte read, 2 written per element.
+// for calls whose row blocks would each convert them again.  A copy: 1 byte read, 2
+// written per element.
 template <int D>
 __global__ void __launch_bounds__(256) expand_kernel(const AttendArgs p) {
   constexpr int CH = D / 16, NP = 128 * CH / 256;
@@ -698,8 +688,6 @@ __global__ void __launch_bounds__(256) expand_kernel(const AttendArgs p) {
   const SeqInfo q = seq_info(a, static_cast<int>(head) / a.n_kv_heads);
   const int tile = blockIdx.x, j0 = tile * kTile;
   if (tile >= q.tiles) return;
-  const int lane = threadIdx.x & 31;
-  const size_t blk = head * (a.cap >> p.log2_block);
   const size_t src = (head * a.cap + j0) * D;
   uint4 c[2][NP];
 #pragma unroll
@@ -717,30 +705,14 @@ __global__ void __launch_bounds__(256) expand_kernel(const AttendArgs p) {
     for (int i = 0; i < NP; ++i)
       if (j0 + (i * 256 + threadIdx.x) / CH >= hidden) c[1][i] = without_nan16(c[1][i]);
   }
-  int ref = -127;  // the head's largest V scale
-  for (int i = lane; i <= (q.len - 1) >> p.log2_block; i += 32)
-    ref = max(ref, exp_of(__ldg(a.v_scale + blk + i)));
-  ref = __reduce_max_sync(0xffffffffu, ref);
 #pragma unroll
   for (int kv = 0; kv < 2; ++kv) {
-    int ex = -127;
-    if (lane < 8 && j0 + lane * 16 < q.len)
-      ex = exp_of(__ldg((kv ? a.v_scale : a.k_scale) + blk + ((j0 + lane * 16) >> p.log2_block)));
-    const int top = kv ? ref : __reduce_max_sync(0xffffffffu, ex);
-    const uint32_t factor = as_u32(__float2half2_rn(pow2f(max(ex - top, -24))));
-    uint4 *dst = reinterpret_cast<uint4 *>((kv ? p.pre_v : p.pre_k) +
-                                           (head * p.pre_len + j0) * D);
+    uint4 *dst = reinterpret_cast<uint4 *>((kv ? p.pre_v : p.pre_k) + (head * p.pre_len + j0) * D);
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      const int id = i * 256 + threadIdx.x;
-      const __half2 f = as_half2(__shfl_sync(0xffffffffu, factor, (id / CH) >> 4));
       uint4 lo, hi;
-      convert16(c[kv][i], f, &lo, &hi);
-      store32(&dst[2 * id], lo, hi);
-    }
-    if (threadIdx.x == 0) {
-      if (kv == 0) p.pre_k_scale[head * (p.pre_len / kTile) + tile] = pow2f(max(top, -126));
-      if (kv == 1 && tile == 0) p.pre_v_scale[head] = pow2f(max(top, -126));
+      convert16(c[kv][i], &lo, &hi);
+      store32(&dst[2 * (i * 256 + threadIdx.x)], lo, hi);
     }
   }
 }

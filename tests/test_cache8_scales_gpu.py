@@ -83,6 +83,16 @@ KERNELS = [
     ("f32", 4, 1, 96, 16, 5, [961, 97]),
 ]
 
+MANY = [
+    ("bf16", 40, 1, 128, 16, 1, [961, 97]),
+    ("bf16", 2, 1, 128, 16, 40, [961, 97]),
+    ("bf16", 4, 2, 64, 32, 50, [961, 97]),
+    ("bf16", 2, 1, 128, 16, 100, [961, 225]),
+    ("bf16", 1, 1, 64, 64, 200, [961, 321]),
+    ("bf16", 2, 1, 128, 16, 200, [961, 225]),
+    ("bf16", 3, 1, 64, 16, 120, [2001, 225]),
+]
+
 
 def cache_with_a_heavy_block(Hq, H, d, block, T, lens, dtype, r, seed, at):
     """Queries of which one block of keys, `at`, gets nearly all; its V lie 2^-r under
@@ -147,3 +157,15 @@ def test_heavy_block_of_small_v(i, r):
 @pytest.mark.parametrize("i", range(len(KERNELS)))
 def test_large_block_that_only_later_tokens_see(i, r):
     run_hidden(i, KERNELS[i], r)
+
+
+@pytest.mark.parametrize("r", [16, 20, 28, 40, 80])
+@pytest.mark.parametrize("i", range(len(MANY)))
+def test_heavy_block_of_small_v_many_rows(i, r):
+    run_heavy(20 + i, MANY[i], r)
+
+
+@pytest.mark.parametrize("r", [16, 20, 28, 40, 80])
+@pytest.mark.parametrize("i", range(len(MANY)))
+def test_large_block_that_only_later_tokens_see_many_rows(i, r):
+    run_hidden(20 + i, MANY[i], r)
