@@ -49,6 +49,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <type_traits>
 
 #include "bkv_device_status.cuh"
@@ -428,7 +429,8 @@ __global__ void __launch_bounds__(kThreads, 2) attend_mma_kernel(const AttendArg
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const float f0 = ks[t] * rs[nt][0], f1 = ks[t] * rs[nt][1];
+          // within f32's range, as logits of zero have to stay
+          const float f0 = fminf(ks[t] * rs[nt][0], FLT_MAX), f1 = fminf(ks[t] * rs[nt][1], FLT_MAX);
           float(&y)[4] = x[t][nt];
           y[0] *= f0;
           y[1] *= f1;
@@ -754,7 +756,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) attend_simt_kernel(const Atte
     if (j0 < cur.q.len) {
       const uint8_t *st = ring + stage * simt_stage_bytes(D);
       const float *sc = reinterpret_cast<const float *>(st + 2 * kSimtKeys * (D + 16));
-      const float f = sc[0] * a.scale * kLog2e, vs = sc[1];
+      const float f = fminf(sc[0] * (a.scale * kLog2e), FLT_MAX), vs = sc[1];
       const int j = j0 + (lane >> 1);
       float x[R];
       simt_logits<R>(st + (lane >> 1) * (D + 16), D, lane & 1, s_q, x);
@@ -1154,7 +1156,8 @@ __global__ void __launch_bounds__(kSimtThreads) weights_simt_kernel(const Attend
   const int j = j0 + (threadIdx.x >> 1), half = threadIdx.x & 1;
   const int jr = min(j, q.len - 1);
   const int rows = a.group * q.n;
-  const float f = __ldg(a.k_scale + head * (a.cap / a.block) + jr / a.block) * a.scale * kLog2e;
+  const float f =
+      fminf(__ldg(a.k_scale + head * (a.cap / a.block) + jr / a.block) * (a.scale * kLog2e), FLT_MAX);
   constexpr int kChunks = kMaxD / 32;  // 16-byte chunks a lane
   uint4 c[kChunks];
 #pragma unroll

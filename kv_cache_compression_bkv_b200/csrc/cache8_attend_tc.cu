@@ -33,6 +33,8 @@
 // 256 rows 113.
 #include <cuda_bf16.h>
 
+#include <cfloat>
+
 #include "bkv_device_status.cuh"
 #include "cache8_attend.cuh"
 #include "sm100.cuh"
@@ -421,6 +423,8 @@ __global__ void __launch_bounds__((TcCfg<D, RT, kPre>::kThreads), 1)
     const int x_tile = warp >> 2;               // row tile
     const int trow = (warp & 3) * 32 + lane;    // row in it, TMEM lane
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const float scale = fminf(fmaxf(a.scale * kLog2e, FLT_MIN), FLT_MAX);
+    const uint32_t scale_bits = (__float_as_uint(scale) & 0x7fffffu) | 0x800000u;
     Part x;
     int t = 0;
     bool ok = true;
@@ -444,7 +448,8 @@ __global__ void __launch_bounds__((TcCfg<D, RT, kPre>::kThreads), 1)
       const bool whole = x.from_start && x.to_end;
       float ref = -INFINITY, l = 0.f, lh = 0.f;
       if (x.live > 0) {
-        float q_factor;  // of the logits
+        int q_exp;       // of the logits' factor, see k_factor
+        int lh_exp = 0;  // lh
         // queries: f16 under a power of two per row, largest in [2^14, 2^15)
         // (read twice: once in registers costs spills in the loop below, 112 -> 119 us
         // for 8 sequences to 8192 rows of 32/8 heads, 64 tokens)
@@ -478,7 +483,7 @@ __global__ void __launch_bounds__((TcCfg<D, RT, kPre>::kThreads), 1)
             *reinterpret_cast<uint4 *>(tile + (i >> 3) * kHalf + sw128_offset(trow, i & 7)) =
                 make_uint4(h[0], h[1], h[2], h[3]);
           }
-          q_factor = pow2f(e - 14) * (a.scale * kLog2e);
+          q_exp = e - 14 + exp_of(scale) - 1;
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&sh.q_full[x_tile]));
@@ -486,23 +491,27 @@ __global__ void __launch_bounds__((TcCfg<D, RT, kPre>::kThreads), 1)
         const size_t block0 = (static_cast<size_t>(x.seq) * a.n_kv_heads + x.kvh) * (a.cap >> p.log2_block);
         for (int j = 0; j < x.live; ++j, ++t) {
           const int buf = RT == 2 ? x_tile : t & 1;
-          // lanes 8 i + b: K's scale and V's exponent for columns 16 b .. 16 b + 15
-          float ks = 0.f, lv = -127.f;
+          // lanes 8 i + b: the exponent fields of K's and V's scale in columns 16 b ..
+          uint32_t fields = 0;
           const int j0 = (x.tile0 + j) * kTile, jb = j0 + (lane & 7) * 16;
-          if (jb < x.len) {
-            ks = __ldg(a.k_scale + block0 + (jb >> p.log2_block));
-            lv = static_cast<float>(exp_of(__ldg(a.v_scale + block0 + (jb >> p.log2_block))));
-          }
+          if (jb < x.len)
+            fields = __float_as_uint(__ldg(a.k_scale + block0 + (jb >> p.log2_block))) >> 23 |
+                     __float_as_uint(__ldg(a.v_scale + block0 + (jb >> p.log2_block))) >> 23 << 16;
           if (!(ok = mbar_wait_warp(smem_u32(&sh.s_full[buf]), RT == 2 ? t & 1 : (t >> 1) & 1,
                                     kWhereSoft)))
             break;
           tc_fence_after();
           if (warp_rows) {
             const uint32_t s_addr = s_col(buf) + lanes;
-            // the logits' factor in columns 16 b ..: not zero, as -infinity has to stay
-            auto k_factor = [&](int b) {
-              return fmaxf(q_factor * __shfl_sync(0xffffffffu, ks, b), 1.17549435e-38f);
+            // the logits' factor under K's scale, row's power of two times `scale`,
+            // within f32's normal range, as -infinity and zero have to stay; and what the
+            // probabilities are multiplied by, 2^(lv + lh), bounded as in v_factor.  Put
+            // together from exponents, which leaves the exp unit to the exps
+            auto k_factor = [&](uint32_t fields) {
+              const int e = __viaddmin_s32_relu(static_cast<int>(fields & 0xffffu), q_exp, 253);
+              return __uint_as_float((static_cast<uint32_t>(e) << 23) + scale_bits);
             };
+            auto v_exp = [&](uint32_t fields) { return static_cast<int>(fields >> 16); };
             const int nvis = sees - j0;
             const bool masked = __any_sync(0xffffffffu, nvis < kTile);
             if (masked) {  // hidden keys' logits become -infinity where they stand
@@ -537,13 +546,17 @@ __global__ void __launch_bounds__((TcCfg<D, RT, kPre>::kThreads), 1)
                     float m = -INFINITY;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) m = fmaxf(m, v[16 * b + i]);
-                    m *= k_factor(2 * c + b);
+                    const uint32_t here = __shfl_sync(0xffffffffu, fields, 2 * c + b);
+                    m *= k_factor(here);
                     top = fmaxf(top, m);
-                    top_v = fmaxf(top_v, m + __shfl_sync(0xffffffffu, lv, 2 * c + b));
+                    top_v = fmaxf(top_v, m + static_cast<float>(v_exp(here) - 127));
                   }
                 }
                 float corr = 1.f, f;
-                if (!fine && move_reference(top - 7.f, top_v - 7.f, ref, l, lh, f)) corr = f;
+                if (!fine && move_reference(top - 7.f, top_v - 7.f, ref, l, lh, f)) {
+                  corr = f;
+                  lh_exp = static_cast<int>(fminf(fmaxf(lh, -300.f), 300.f));
+                }
                 __syncwarp();
                 if (j > 0) {
                   // O, once the MMAs of the tile before have added to it
@@ -573,8 +586,10 @@ __global__ void __launch_bounds__((TcCfg<D, RT, kPre>::kThreads), 1)
                 if (c < 3) tmem_ld_32x32b_x32(s_addr + 32u * (c + 1), v[(c + 1) & 1]);
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
-                  const float f = k_factor(2 * c + b);
-                  const float g = v_factor(__shfl_sync(0xffffffffu, lv, 2 * c + b), lh);
+                  const uint32_t here = __shfl_sync(0xffffffffu, fields, 2 * c + b);
+                  const float f = k_factor(here);
+                  const float g = __uint_as_float(
+                      static_cast<uint32_t>(__viaddmin_s32_relu(v_exp(here), lh_exp, 253)) << 23);
                   const float2 f2 = make_float2(f, f), g2 = make_float2(g, g);
                   float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll

@@ -20,6 +20,8 @@
 // 2 x 2.7 GB, 830 us at the measured copy rate.
 #include <cuda_bf16.h>
 
+#include <cfloat>
+
 #include "bkv_device_status.cuh"
 #include "cache8_attend.cuh"
 #include "sm100.cuh"
@@ -178,9 +180,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int s = warp >> 2, row = threadIdx.x & 127;  // accumulator, and tiles s, s + 2, ..
     const int key = j0 + row;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const float f =
+    const float f = fminf(
         __ldg(a.k_scale + head * (a.cap >> p.log2_block) + (min(key, q.len - 1) >> p.log2_block)) *
-        (a.scale * kLog2e);
+            (a.scale * kLog2e),
+        FLT_MAX);
     const float *lse2 = p.lse2 + head * a.group * a.T;
     float z_next = 0.f;
     int t_next = INT32_MIN;

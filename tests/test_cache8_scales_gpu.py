@@ -169,3 +169,23 @@ def test_heavy_block_of_small_v_many_rows(i, r):
 @pytest.mark.parametrize("i", range(len(MANY)))
 def test_large_block_that_only_later_tokens_see_many_rows(i, r):
     run_hidden(20 + i, MANY[i], r)
+
+
+@pytest.mark.parametrize("i", range(len(KERNELS + MANY)))
+def test_logits_of_zero_under_factors_past_the_range(i):
+    """K and queries whose scales multiply past f32's range, in elements that do not
+    meet: logits of zero, and the average of V."""
+    dtype, Hq, H, d, block, T, lens = (KERNELS + MANY)[i]
+    S, cap = len(lens), (max(lens) + block - 1) // block * block
+    g = gen(100 + i)
+    rc = ref.Cache(S, H, cap, d, block)
+    x = torch.randn(2, S, H, cap, d, generator=g)
+    x[0, ..., d // 2:] = 0.0
+    x[0] *= 2.0 ** 122
+    rc.append([cap] * S, [cap] * S, x[0], x[1])
+    dev = Dev(S, Hq, H, cap, d, block, dtype)
+    dev.fill(rc, lens)
+    q = torch.randn(S, Hq, T, d, generator=g) * 2.0 ** 90
+    q[..., :d // 2] = 0.0
+    q = q.to(DT[dtype])
+    check(rc, dtype, q, lens, None, T, attend(dev, q, lens, None, T))
