@@ -10,8 +10,7 @@
 // one per resident CTA, so a ragged batch leaves no CTA idle and a single long
 // sequence uses every SM.  A run can begin and end inside a (sequence, head,
 // row block), a "segment": a CTA that has a whole segment writes its output,
-// one that has a part writes (max, sum, unnormalised output) to its slot of
-// the workspace and attend_finish_kernel joins the parts in their order.  The
+// one that has a part writes (max, sum, output) to its slot of the workspace and attend_finish_kernel joins the parts in their order.  The
 // lengths are read on the device; the host needs only their upper bound.
 //
 // attend_mma_kernel (bf16, head_dim 64 or 128, up to 32 query rows a KV head):
@@ -70,15 +69,17 @@ constexpr int kSimtWarps = 8;            // the other kernels'
 constexpr int kSimtThreads = kSimtWarps * 32;
 constexpr int kSimtKeys = 16;
 
-// The end of a CTA's part of a segment: kBufs buffers of unnormalised outputs
-// (summed here; element (r, d) of a buffer at off(r, d)) and the row statistics
-// m, l.  A whole segment goes out, a part to the CTA's slot.  first[d]: the
+// The end of a CTA's part of a segment: kBufs buffers of its outputs (summed here;
+// element (r, d) of a buffer at off(r, d)) and the row statistics m, l.  The outputs
+// are averages already, as sums of values could pass f32's range: under l, or where
+// share is given under a sum of the buffer's own, whose share of l is share[buffer
+// kRows + r].  A whole segment goes out, a part to the CTA's slot.  first[d]: the
 // lowest key whose NaN in V was left out (hide_nan16), for the rows that see it,
 // where first[D] says that there are any; so does the result.  (With one token
 // every row sees every key, and first is not looked at.)
 template <int kRows, int kBufs, int kCta, typename T, typename Off>
 __device__ __forceinline__ bool write_segment(const AttendArgs &p, const float *buf, int buf_stride,
-                                              const float *m, const float *l, const int *first,
+                                              const float *share, const float *m, const float *l, const int *first,
                                               int seq, int unit, const SeqInfo &q, bool whole,
                                               int slot, Off &&off) {
   const Cache8AttendArgs &a = p.a;
@@ -92,12 +93,14 @@ __device__ __forceinline__ bool write_segment(const AttendArgs &p, const float *
     const int o = off(r, d);
     float v = 0.f;
 #pragma unroll
-    for (int b = 0; b < kBufs; ++b) v += buf[b * buf_stride + o];
+    for (int b = 0; b < kBufs; ++b) {
+      const float x = buf[b * buf_stride + o];
+      v = share ? fmaf(share[b * kRows + r], x, v) : v + x;
+    }
     if (!whole) {
       part[2 * kRows + e] = v;
     } else if (r0 + r < rows) {
-      store_out(static_cast<T *>(a.out) + q_row(a, seq, kvh, r0 + r) * D + d,
-                l[r] > 0.f || l[r] != l[r] ? v / l[r] : 0.f);
+      store_out(static_cast<T *>(a.out) + q_row(a, seq, kvh, r0 + r) * D + d, v);
     }
   }
   if (nans) {  // the same elements again
@@ -554,8 +557,8 @@ __global__ void __launch_bounds__(kThreads, 2) attend_mma_kernel(const AttendArg
           }
         }
       __syncthreads();
-      // this warp's factor to the CTA's reference and the values' own units
-      float f[NT][2];
+      // this warp's factors: to the CTA's average, and from its units to the values'
+      float f[NT][2], unit[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -564,15 +567,16 @@ __global__ void __launch_bounds__(kThreads, 2) attend_mma_kernel(const AttendArg
           float M = -INFINITY;
 #pragma unroll
           for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w * Cfg::kRows + r]);
-          f[nt][i] = (m[nt][i] != -INFINITY ? ex2(m[nt][i] - M)
-                                            : lsum[nt][i] != lsum[nt][i] ? 1.f : 0.f) * ex2(-lh[nt][i]);
-          if (warp == 0 && g == 0) {
-            float L = 0.f;
+          float L = 0.f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-              const float mw = s_m[w * Cfg::kRows + r], lw = s_l[w * Cfg::kRows + r];
-              L += mw == -INFINITY ? lw : ex2(mw - M) * lw;
-            }
+          for (int w = 0; w < kWarps; ++w) {
+            const float mw = s_m[w * Cfg::kRows + r], lw = s_l[w * Cfg::kRows + r];
+            L += mw == -INFINITY ? lw : ex2(mw - M) * lw;
+          }
+          f[nt][i] = (m[nt][i] != -INFINITY ? ex2(m[nt][i] - M)
+                                            : lsum[nt][i] != lsum[nt][i] ? 1.f : 0.f) * inverse(L);
+          unit[nt][i] = ex2(-lh[nt][i]);
+          if (warp == 0 && g == 0) {
             s_M[r] = M;
             s_L[r] = L;
           }
@@ -585,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_mma_kernel(const AttendArg
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) bf[at(mt, nt, i)] = o[mt][nt][i] * f[nt][i & 1];
+            for (int i = 0; i < 4; ++i) bf[at(mt, nt, i)] = o[mt][nt][i] * f[nt][i & 1] * unit[nt][i & 1];
       }
       __syncthreads();
       if (warp < 2) {
@@ -594,11 +598,12 @@ __global__ void __launch_bounds__(kThreads, 2) attend_mma_kernel(const AttendArg
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) bf[at(mt, nt, i)] += o[mt][nt][i] * f[nt][i & 1];
+            for (int i = 0; i < 4; ++i)
+              bf[at(mt, nt, i)] += o[mt][nt][i] * f[nt][i & 1] * unit[nt][i & 1];
       }
       __syncthreads();
       const bool nans = write_segment<Cfg::kRows, 2, kThreads, __nv_bfloat16>(
-          p, s_buf, Cfg::kBuf, s_M, s_L, s_first, cur.seq, cur.unit, cur.q, from_start && to_end,
+          p, s_buf, Cfg::kBuf, nullptr, s_M, s_L, s_first, cur.seq, cur.unit, cur.q, from_start && to_end,
           from_start ? 1 : 0, [](int r, int d) {
             return (((d >> 4) * NT + (r >> 3)) * 4 + ((d >> 3) & 1) * 2 + (r & 1)) * 32 +
                    (d & 7) * 4 + ((r & 7) >> 1);
@@ -671,7 +676,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) attend_simt_kernel(const Atte
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(16) float s_p[kSimtWarps][kSimtKeys][R];
   __shared__ float s_m[kSimtWarps][R], s_l[kSimtWarps][R];
-  __shared__ float s_M[R], s_L[R];
+  __shared__ float s_M[R], s_L[R], s_share[kSimtWarps][R];
   __shared__ int s_first[kMaxD + 1];  // see write_segment
   const Cache8AttendArgs &a = p.a;
   const int D = a.head_dim;
@@ -725,7 +730,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) attend_simt_kernel(const Atte
     __syncthreads();
   };
   if (a.T > 1) reset_first();
-  float o[R][4], m[R], l[R];
+  float o[R][4], m[R], l[R], lh[R];  // references and units: see move_reference
   bool fresh = true;
   int seg_tiles = 0, stage = 0;
   while (cur.at < run) {
@@ -745,7 +750,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) attend_simt_kernel(const Atte
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         m[r] = -INFINITY;
-        l[r] = 0.f;
+        l[r] = lh[r] = 0.f;
         o[r][0] = o[r][1] = o[r][2] = o[r][3] = 0.f;
       }
     }
@@ -756,28 +761,37 @@ __global__ void __launch_bounds__(kSimtThreads, 2) attend_simt_kernel(const Atte
     if (j0 < cur.q.len) {
       const uint8_t *st = ring + stage * simt_stage_bytes(D);
       const float *sc = reinterpret_cast<const float *>(st + 2 * kSimtKeys * (D + 16));
-      const float f = fminf(sc[0] * (a.scale * kLog2e), FLT_MAX), vs = sc[1];
+      const float f = fminf(sc[0] * (a.scale * kLog2e), FLT_MAX);
+      const float lv = static_cast<float>(exp_of(sc[1]));
       const int j = j0 + (lane >> 1);
       float x[R];
       simt_logits<R>(st + (lane >> 1) * (D + 16), D, lane & 1, s_q, x);
       const int seen0 = cur.q.len - cur.q.n + 1;
+      bool grow = false;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         x[r] = j < min(seen0 + (r0 + r) / a.group, cur.q.len) ? x[r] * f : -INFINITY;
         if (p.x_cols > r0 + r && (lane & 1) == 0 && j < cur.q.len)
           p.x[(head * p.x_len + j) * p.x_cols + r0 + r] = x[r];
-        float t = x[r];
+        grow |= x[r] > m[r] + (15.f - fmaxf(lv + lh[r], 0.f));
+      }
+      // references move where they are passed by 2^15, all of the row block's
+      if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-        for (int s = 2; s < 32; s <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, s));
-        if (t > m[r]) {
-          const float g = ex2(m[r] - t);
-          m[r] = t;
-          l[r] *= g;
-          o[r][0] *= g, o[r][1] *= g, o[r][2] *= g, o[r][3] *= g;
+        for (int r = 0; r < R; ++r) {
+          float t = x[r], g;
+#pragma unroll
+          for (int s = 2; s < 32; s <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, s));
+          if (move_reference(t, t + lv, m[r], l[r], lh[r], g)) {
+            o[r][0] *= g, o[r][1] *= g, o[r][2] *= g, o[r][3] *= g;
+          }
         }
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
         const float e = ex2(x[r] - (m[r] == -INFINITY ? 0.f : m[r]));
         if ((lane & 1) == 0) {
-          s_p[warp][lane >> 1][r] = e * vs;
+          s_p[warp][lane >> 1][r] = e * v_factor(lv, lh[r]);
           l[r] += e;
         }
       }
@@ -821,42 +835,41 @@ __global__ void __launch_bounds__(kSimtThreads, 2) attend_simt_kernel(const Atte
     ++seg_tiles;
     if (cur.tile + 1 == cur.q.tiles || cur.at + 1 == run) {
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        float t = l[r];
+      for (int r = 0; r < R; ++r) {  // the warp's averages
+        float t = l[r];  // odd lanes: zero
 #pragma unroll
-        for (int s = 2; s < 32; s <<= 1) t += __shfl_xor_sync(0xffffffffu, t, s);
+        for (int s = 1; s < 32; s <<= 1) t += __shfl_xor_sync(0xffffffffu, t, s);
         if (lane == 0) {
           s_m[warp][r] = m[r];
           s_l[warp][r] = t;
         }
-        l[r] = t;  // in the even lanes
+        const float f = inverse(t), unit = ex2(-lh[r]);
+        if (lane * 4 < D)
+          *reinterpret_cast<float4 *>(s_buf + (warp * R + r) * D + lane * 4) = make_float4(
+              o[r][0] * f * unit, o[r][1] * f * unit, o[r][2] * f * unit, o[r][3] * f * unit);
       }
       __syncthreads();
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        float M = -INFINITY;
-        for (int k = 0; k < kSimtWarps; ++k) M = fmaxf(M, s_m[k][r]);
-        // NaN logits leave no reference, and sums that have to stay
-        const float f = m[r] == -INFINITY ? (s_l[warp][r] != s_l[warp][r] ? 1.f : 0.f) : ex2(m[r] - M);
-        if (lane * 4 < D)
-          *reinterpret_cast<float4 *>(s_buf + (warp * R + r) * D + lane * 4) =
-              make_float4(o[r][0] * f, o[r][1] * f, o[r][2] * f, o[r][3] * f);
-      }
-      if (threadIdx.x < R) {
-        const int r = threadIdx.x;
+      if (threadIdx.x < kSimtWarps * R) {
+        const int k = threadIdx.x / R, r = threadIdx.x % R;
         float M = -INFINITY, L = 0.f;
         for (int k = 0; k < kSimtWarps; ++k) M = fmaxf(M, s_m[k][r]);
-        for (int k = 0; k < kSimtWarps; ++k)
-          L += s_m[k][r] == -INFINITY ? s_l[k][r] : ex2(s_m[k][r] - M) * s_l[k][r];
-        s_M[r] = M;
-        s_L[r] = L;
+        // NaN logits leave no reference, and sums that have to stay
+        auto part_of = [&](int k) {
+          return s_m[k][r] == -INFINITY ? s_l[k][r] : ex2(s_m[k][r] - M) * s_l[k][r];
+        };
+        for (int k = 0; k < kSimtWarps; ++k) L += part_of(k);
+        s_share[k][r] = part_of(k) * inverse(L);
+        if (k == 0) {
+          s_M[r] = M;
+          s_L[r] = L;
+        }
       }
       __syncthreads();
       const bool from_start = seg_tiles == cur.tile + 1;
       const bool to_end = cur.tile + 1 == cur.q.tiles;
       seg_tiles = 0;
       const bool nans = write_segment<R, kSimtWarps, kSimtThreads, T>(
-          p, s_buf, R * D, s_M, s_L, s_first, cur.seq, cur.unit, cur.q, from_start && to_end,
+          p, s_buf, R * D, s_share[0], s_M, s_L, s_first, cur.seq, cur.unit, cur.q, from_start && to_end,
           from_start ? 1 : 0, [D](int r, int d) { return r * D + d; });
       __syncthreads();
       if (nans) reset_first();
@@ -1076,22 +1089,26 @@ __global__ void __launch_bounds__(kSimtThreads, 5) attend_finish_kernel(const At
       }
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        float M = ml[k][0].x, l = 0.f;
+        float M = ml[k][0].x, l = 0.f, part_l[kFewParts];
 #pragma unroll
         for (int i = 1; i < kFewParts; ++i) M = fmaxf(M, ml[k][i].x);
+#pragma unroll
+        for (int i = 0; i < kFewParts; ++i) {
+          part_l[i] = (ml[k][i].x == -INFINITY ? 1.f : ex2(ml[k][i].x - M)) * ml[k][i].y;
+          l += part_l[i];
+        }
+        const float inv = inverse(l);
         float o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < kFewParts; ++i) {
-          const float f = ml[k][i].x == -INFINITY ? 1.f : ex2(ml[k][i].x - M);
-          l = fmaf(f, ml[k][i].y, l);
+          const float f = part_l[i] * inv;
           o[0] = fmaf(f, v[k][i].x, o[0]), o[1] = fmaf(f, v[k][i].y, o[1]);
           o[2] = fmaf(f, v[k][i].z, o[2]), o[3] = fmaf(f, v[k][i].w, o[3]);
         }
         if (i0 + k >= rows) break;
-        const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
         if (lane * 4 < D)
-          store_out4(static_cast<T *>(a.out) + q_row(a, seq, kvh, r0 + i0 + k) * D + lane * 4,
-                     o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
+          store_out4(static_cast<T *>(a.out) + q_row(a, seq, kvh, r0 + i0 + k) * D + lane * 4, o[0],
+                     o[1], o[2], o[3]);
         if (lane == 0) store_lse(p, seq, kvh, r0 + i0 + k, M, l);
       }
     }
@@ -1103,15 +1120,16 @@ __global__ void __launch_bounds__(kSimtThreads, 5) attend_finish_kernel(const At
     const float2 ml = join_row(x.n, [&](int i) {
       return *reinterpret_cast<const float2 *>(part(x, i) + 2 * row);
     });
-    const float M = ml.x, l = ml.y;
+    const float M = ml.x, l = ml.y, inv = inverse(l);
     float o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
     for (int i = warp % deal; i < x.n; i += deal) {
       const float *s = part(x, i);
-      const float mi = s[2 * row];
+      const float2 pair = *reinterpret_cast<const float2 *>(s + 2 * row);
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (lane * 4 < D) v = *reinterpret_cast<const float4 *>(s + 2 * kRows + row * D + lane * 4);
-      const float f = mi == -INFINITY ? 1.f : ex2(mi - M);  // no reference: zeros, or NaN
+      // no reference: no keys, or NaN
+      const float f = (pair.x == -INFINITY ? 1.f : ex2(pair.x - M)) * pair.y * inv;
       o[0] = fmaf(f, v.x, o[0]), o[1] = fmaf(f, v.y, o[1]);
       o[2] = fmaf(f, v.z, o[2]), o[3] = fmaf(f, v.w, o[3]);
     }
@@ -1127,10 +1145,9 @@ __global__ void __launch_bounds__(kSimtThreads, 5) attend_finish_kernel(const At
         }
       }
     }
-    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
     if (lane * 4 < D)
-      store_out4(static_cast<T *>(a.out) + q_row(a, seq, kvh, r0 + i0) * D + lane * 4, o[0] * inv,
-                 o[1] * inv, o[2] * inv, o[3] * inv);
+      store_out4(static_cast<T *>(a.out) + q_row(a, seq, kvh, r0 + i0) * D + lane * 4, o[0], o[1],
+                 o[2], o[3]);
     if (lane == 0) store_lse(p, seq, kvh, r0 + i0, M, l);
   }
 }

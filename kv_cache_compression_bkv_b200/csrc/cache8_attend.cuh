@@ -24,7 +24,7 @@ struct AttendArgs {
   int w_keys, w_chunks;  // keys per weights CTA, and its CTAs per (sequence, KV head)
   long long x_len;   // keys per (sequence, KV head) in x
   // [ctas][2]: the two ends' segments of a CTA's run, each (reference, sum)
-  // [rows], then unnormalised outputs [rows][head_dim]
+  // [rows], then outputs [rows][head_dim], averages under the sum
   float *part;
   float *lse2;       // [n_seqs][n_kv_heads][group * T], log2 units
   float *x;          // [n_seqs][n_kv_heads][x_len][x_cols], log2 units
@@ -74,6 +74,13 @@ __device__ __forceinline__ bool move_reference(float t, float u, float &m, float
 
 // 2^(lv + lh), bounded so that a probability of zero times it is zero.
 __device__ __forceinline__ float v_factor(float lv, float lh) { return ex2(fminf(lv + lh, 126.f)); }
+
+// 1 / l for a row's sum (to an ulp), 0 for one that sees nothing; NaN stays.
+__device__ __forceinline__ float inverse(float l) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(l));
+  return l > 0.f || l != l ? y : 0.f;
+}
 
 // ------------------------------------------------------------ the work split
 

@@ -634,7 +634,7 @@ __global__ void __launch_bounds__((TcCfg<D, RT, kPre>::kThreads), 1)
                                  (kRows * (2 + D));
       const int pr = x_tile * 128 + trow;
       const float unit = ex2(-lh);  // of the outputs
-      const float mul = !whole ? unit : l > 0.f || l != l ? unit / l : 0.f;
+      const float mul = inverse(l);
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         float v[32];
@@ -648,7 +648,7 @@ __global__ void __launch_bounds__((TcCfg<D, RT, kPre>::kThreads), 1)
         }
         // rows without a visible key so far hold zeros, whatever the scale
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = l != 0.f ? v[i] * mul : 0.f;
+        for (int i = 0; i < 32; ++i) v[i] = l != 0.f ? v[i] * mul * unit : 0.f;
         if (row && whole) {
           __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + q_row(a, x.seq, x.kvh, r) * D + 32 * c;
 #pragma unroll

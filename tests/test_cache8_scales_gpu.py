@@ -153,7 +153,7 @@ def test_heavy_block_of_small_v(i, r):
     run_heavy(i, KERNELS[i], r)
 
 
-@pytest.mark.parametrize("r", [16, 20, 28, 40, 80])
+@pytest.mark.parametrize("r", [16, 20, 28, 40, 80, 120])
 @pytest.mark.parametrize("i", range(len(KERNELS)))
 def test_large_block_that_only_later_tokens_see(i, r):
     run_hidden(i, KERNELS[i], r)
@@ -165,7 +165,7 @@ def test_heavy_block_of_small_v_many_rows(i, r):
     run_heavy(20 + i, MANY[i], r)
 
 
-@pytest.mark.parametrize("r", [16, 20, 28, 40, 80])
+@pytest.mark.parametrize("r", [16, 20, 28, 40, 80, 120])
 @pytest.mark.parametrize("i", range(len(MANY)))
 def test_large_block_that_only_later_tokens_see_many_rows(i, r):
     run_hidden(20 + i, MANY[i], r)
@@ -188,4 +188,22 @@ def test_logits_of_zero_under_factors_past_the_range(i):
     q = torch.randn(S, Hq, T, d, generator=g) * 2.0 ** 90
     q[..., :d // 2] = 0.0
     q = q.to(DT[dtype])
+    check(rc, dtype, q, lens, None, T, attend(dev, q, lens, None, T))
+
+
+@pytest.mark.parametrize("mag", [2.0e38, 1.0e-34])
+@pytest.mark.parametrize("i", range(len(KERNELS + MANY)))
+def test_values_at_the_ends_of_the_range(i, mag):
+    """Sums of many values of which a few pass f32's range, or lie at its lower end:
+    the outputs are averages, and lie within."""
+    dtype, Hq, H, d, block, T, lens = (KERNELS + MANY)[i]
+    S, cap = len(lens), (max(lens) + block - 1) // block * block
+    g = gen(80 + i)
+    rc = ref.Cache(S, H, cap, d, block)
+    x = torch.randn(2, S, H, cap, d, generator=g)
+    x[1] = mag * (0.5 + 0.5 * torch.rand(S, H, cap, d, generator=g))
+    rc.append([cap] * S, [cap] * S, x[0], x[1])
+    dev = Dev(S, Hq, H, cap, d, block, dtype)
+    dev.fill(rc, lens)
+    q = torch.randn(S, Hq, T, d, generator=g).to(DT[dtype])
     check(rc, dtype, q, lens, None, T, attend(dev, q, lens, None, T))
