@@ -660,29 +660,41 @@ __device__ __forceinline__ void simt_logits(const uint8_t *row, int D, int half,
   for (int r = 0; r < R; ++r) x[r] += __shfl_xor_sync(0xffffffffu, x[r], 1);
 }
 
-// Dynamic shared memory: queries, the warps' merge buffers, and per warp two
-// stages of 16 keys' codes (rows padded by 16 bytes against bank conflicts).
-inline __host__ __device__ int simt_stage_bytes(int D) { return 2 * kSimtKeys * (D + 16) + 16; }
-inline int simt_smem(int D, int R) {
+// Dynamic shared memory: queries, the warps' merge buffers (each with its
+// probabilities of a tile before), and per warp two stages of 16 keys' codes (rows
+// padded by 16 bytes against bank conflicts).
+constexpr int simt_stage_bytes(int D) { return 2 * kSimtKeys * (D + 16) + 16; }
+constexpr int simt_smem(int D, int R) {
   return (1 + kSimtWarps) * R * D * 4 + kSimtWarps * 2 * simt_stage_bytes(D);
 }
+template <int R>
+struct SimtShared {
+  float m[kSimtWarps][R], l[kSimtWarps][R], share[kSimtWarps][R];
+  float M[R], L[R];
+  int first[kMaxD + 1];  // see write_segment
+};
 
 // R: query rows a row block has room for, 2, 4 or 8: the least that holds a KV head's,
 // since empty ones cost as much as others.  f32, one token: 11 sequences of 1271
-// rows, 16/8 heads of 128, 20 us with 2 and 50 with 8; 3 of 24153 rows, 2/1 heads of
-// 96, 19 and 29.
+// rows, 16/8 heads of 128, 19 us with 2 and 35 with 8; 3 of 24153 rows, 2/1 heads of
+// 96, 18 and 28.
 template <typename T, int R>
 __global__ void __launch_bounds__(kSimtThreads, 2) attend_simt_kernel(const AttendArgs p) {
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(16) float s_p[kSimtWarps][kSimtKeys][R];
-  __shared__ float s_m[kSimtWarps][R], s_l[kSimtWarps][R];
-  __shared__ float s_M[R], s_L[R], s_share[kSimtWarps][R];
-  __shared__ int s_first[kMaxD + 1];  // see write_segment
+  __shared__ SimtShared<R> sh;
+  // what the plan's number of CTAs counts on: two an SM, of its 228 KB, 1 KB of each
+  // CTA's is the system's
+  static_assert(2 * (simt_smem(kMaxD, R) + sizeof(sh) + 1024) <= 228 * 1024, "two CTAs an SM");
+  auto &s_m = sh.m, &s_l = sh.l, &s_share = sh.share;
+  auto &s_M = sh.M, &s_L = sh.L;
+  auto &s_first = sh.first;
   const Cache8AttendArgs &a = p.a;
   const int D = a.head_dim;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float *s_q = reinterpret_cast<float *>(smem);
   float *s_buf = s_q + R * D;
+  // the probabilities of a tile, [key][R]: 16 R floats of the R D
+  float *s_p = s_buf + warp * R * D;
   uint8_t *ring = reinterpret_cast<uint8_t *>(s_buf + kSimtWarps * R * D) +
                   warp * 2 * simt_stage_bytes(D);
   const int units = a.n_kv_heads * p.row_blocks;
@@ -791,7 +803,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) attend_simt_kernel(const Atte
       for (int r = 0; r < R; ++r) {
         const float e = ex2(x[r] - (m[r] == -INFINITY ? 0.f : m[r]));
         if ((lane & 1) == 0) {
-          s_p[warp][lane >> 1][r] = e * v_factor(lv, lh[r]);
+          s_p[(lane >> 1) * R + r] = e * v_factor(lv, lh[r]);
           l[r] += e;
         }
       }
@@ -818,11 +830,11 @@ __global__ void __launch_bounds__(kSimtThreads, 2) attend_simt_kernel(const Atte
         values4(*reinterpret_cast<const uint32_t *>(vrow + k * (D + 16)), v);
         alignas(16) float e[R];
         if constexpr (R == 2) {
-          *reinterpret_cast<float2 *>(e) = *reinterpret_cast<const float2 *>(&s_p[warp][k][0]);
+          *reinterpret_cast<float2 *>(e) = *reinterpret_cast<const float2 *>(s_p + k * R);
         } else {
 #pragma unroll
           for (int r = 0; r < R; r += 4)
-            *reinterpret_cast<float4 *>(e + r) = *reinterpret_cast<const float4 *>(&s_p[warp][k][r]);
+            *reinterpret_cast<float4 *>(e + r) = *reinterpret_cast<const float4 *>(s_p + k * R + r);
         }
 #pragma unroll
         for (int r = 0; r < R; ++r)
