@@ -70,7 +70,11 @@ class StepArgs(ctypes.Structure):
                 ("ring_pos", ctypes.c_int64), ("aux_stream", ctypes.c_void_p)]
 
 STEP_EVENTS = 6
-_RAW_STREAM = torch._C._cuda_getCurrentRawStream
+try:  # not there in builds of torch without CUDA, where the module is imported all the same
+    from torch._C import _cuda_getCurrentRawStream as _RAW_STREAM
+except ImportError:
+    def _RAW_STREAM(device: int) -> int:
+        return torch.cuda.current_stream(device).cuda_stream
 
 
 def _load() -> ctypes.CDLL:
