@@ -17,6 +17,7 @@
 
 #include <algorithm>
 
+#include "bkv_check.cuh"
 #include "bkv_device_status.cuh"
 #include "bkv_internal.h"
 #include "cache8.cuh"
@@ -134,9 +135,10 @@ __global__ void __launch_bounds__(kMaxThreads) append_kernel(const Cache8AppendA
       if (p < pieces) v[i].load(src + static_cast<size_t>(p) * 16);
     }
   };
-  if (blk < blk_end) load(blk);
+  if (blk < blk_end && BKV_CHECK(blk >= 0 && blk < a.cap / a.block, 602)) load(blk);
 #pragma unroll 1
   for (int round = 0; blk < blk_end; ++blk, ++round) {
+    if (!BKV_CHECK(blk >= 0 && blk < a.cap / a.block, 602)) return;  // the whole CTA
     const int base = blk * a.block, r0 = max(base, first), r1 = min(base + a.block, len);
     const int pieces = (r1 - r0) * pr;
     uint8_t *codes = head_codes + static_cast<size_t>(base) * a.head_dim;

@@ -51,6 +51,7 @@
 #include <cfloat>
 #include <type_traits>
 
+#include "bkv_check.cuh"
 #include "bkv_device_status.cuh"
 #include "bkv_internal.h"
 #include "cache8_attend.cuh"
@@ -281,6 +282,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_mma_kernel(const AttendArg
   const uint32_t v_dst0 = kKeys * D + lrow * D + (D == 128 ? lch ^ lrow : lch ^ ((lrow >> 1) & 3)) * 16;
   Cursor load, cur;
   cur.seek(a, w, units, mine, t0);
+  if (!BKV_CHECK(cur.inside(a, units), 612)) return;  // the whole CTA
   load = cur;
   // the first segment's queries, ahead of the stream of codes
   RawQ<D> first_q;
@@ -707,6 +709,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) attend_simt_kernel(const Atte
   const int run = min(w.run, w.total - t0);
   Cursor cur, ahead;
   cur.seek(a, w, units, mine, t0);
+  if (!BKV_CHECK(cur.inside(a, units), 613)) return;  // the whole CTA
   ahead = cur;
   const uint64_t policy = evict_first();
   // the next tile's codes and scales of this warp
@@ -1032,7 +1035,8 @@ __global__ void __launch_bounds__(kSimtThreads, 5) attend_finish_kernel(const At
     }
     for (int r = warp; r < rows; r += kSimtWarps) {
       const int unit = (head - seq * a.n_kv_heads) * p.row_blocks + r / kRows, row = r % kRows;
-      const Parts x = parts_of(w, before + unit * (q.tiles + w.pad) + w.pad, q.tiles);
+      Parts x = parts_of(w, before + unit * (q.tiles + w.pad) + w.pad, q.tiles);
+      if (!BKV_CHECK(x.c0 >= 0 && x.n >= 1 && x.c0 + x.n <= p.ctas, 614)) x = {0, 1};
       float z;
       if (x.n == 1) {
         z = p.lse2[static_cast<size_t>(head) * a.group * a.T + r];
@@ -1070,6 +1074,7 @@ __global__ void __launch_bounds__(kSimtThreads, 5) attend_finish_kernel(const At
   Parts x = {0, 0};
   if (q.tiles > 0)
     x = parts_of(w, counted_before(a, w, units, mine, seq) + unit * (q.tiles + w.pad) + w.pad, q.tiles);
+  if (!BKV_CHECK(x.c0 >= 0 && x.n >= 0 && x.c0 + x.n <= p.ctas, 615)) x = {0, 0};
   pdl_wait();
   if (q.bad) {
     if (threadIdx.x == 0) record_device_status(BKV_DEV_ASSERT, 611);

@@ -175,6 +175,10 @@ struct Cursor {
     tile = max(pos, 0);
     at = max(-pos, 0);
   }
+  // Whether it names a tile of the call (for the debug build).
+  __device__ __forceinline__ bool inside(const Cache8AttendArgs &a, int units) const {
+    return seq >= 0 && seq < a.n_seqs && unit >= 0 && unit < units && tile >= 0 && tile < q.tiles;
+  }
   __device__ __forceinline__ void next(const Cache8AttendArgs &a, const Split &w, int units) {
     ++at;
     if (++tile < q.tiles) return;

@@ -35,6 +35,7 @@
 
 #include <cfloat>
 
+#include "bkv_check.cuh"
 #include "bkv_device_status.cuh"
 #include "cache8_attend.cuh"
 #include "sm100.cuh"
@@ -189,6 +190,7 @@ __global__ void __launch_bounds__((TcCfg<D, RT, kPre>::kThreads), 1)
   PartIter<kRows> parts;
   parts.run = min(w.run, w.total - t0);
   parts.c.seek(a, w, units, mine, t0);
+  if (!BKV_CHECK(parts.c.inside(a, units), 636)) return;  // the whole CTA
 
   constexpr int kMmaWarp = Cfg::kSoftWarps + Cfg::kConvWarps;
   if (warp == kMmaWarp) {
@@ -442,7 +444,7 @@ __global__ void __launch_bounds__((TcCfg<D, RT, kPre>::kThreads), 1)
     };
     while (ok && parts.next(p, w, units, &x)) {
       const int r = x.r0 + x_tile * 128 + trow;
-      const bool row = r < x.rows;
+      const bool row = r < x.rows && BKV_CHECK(r >= 0 && r < a.group * a.T, 638);
       const int sees = x.len - x.n + 1 + r / a.group;  // keys this row sees
       const bool warp_rows = x.r0 + x_tile * 128 + (warp & 3) * 32 < x.rows;
       const bool whole = x.from_start && x.to_end;
@@ -759,7 +761,9 @@ __global__ void __launch_bounds__(256) mark_nan_kernel(const AttendArgs p) {
     uint4 c = load(i);
     const int id = i * 256 + threadIdx.x, j = j0 + id / CH;
     hide_nan16(&c, [&](int e) {
-      for (int t = j - (q.len - q.n); t < q.n; ++t)
+      const int t0 = j - (q.len - q.n);  // the first token that sees row j
+      if (!BKV_CHECK(t0 >= 0 && j < q.len, 637)) return;
+      for (int t = t0; t < q.n; ++t)
         for (int g = 0; g < a.group; ++g)
           static_cast<__nv_bfloat16 *>(a.out)[q_row(a, seq, static_cast<int>(head) - seq * a.n_kv_heads,
                                                     t * a.group + g) * D + id % CH * 16 + e] =

@@ -33,6 +33,7 @@
 
 #include <algorithm>
 
+#include "bkv_check.cuh"
 #include "bkv_device_status.cuh"
 #include "bkv_internal.h"
 #include "cache8.cuh"
@@ -193,7 +194,9 @@ __global__ void __launch_bounds__(kSelThreads, 3) evict_select_kernel(const Cach
           while (bits) {
             const int t = __ffs(bits) - 1;
             bits &= bits - 1;
-            const uint32_t k = order_key(ranked(__ldg(w + j + 4 * kSelThreads * (t >> 2) + (t & 3))));
+            const unsigned at_w = j + 4 * kSelThreads * (t >> 2) + (t & 3);
+            if (!BKV_CHECK(at_w < static_cast<unsigned>(L), 623)) continue;
+            const uint32_t k = order_key(ranked(__ldg(w + at_w)));
             atomicAdd(&s_hist[(k >> 10) & 2047u], 1u);
             const uint32_t at = atomicAdd(&s_count, 1u);
             if (at < kListMax) s_list[at] = k;
@@ -308,7 +311,12 @@ __global__ void __launch_bounds__(kSelThreads, 3) evict_select_kernel(const Cach
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if ((n >> i) & 1u) idx[o++] = static_cast<int32_t>(j0 + 128 * t + i);
+        if ((n >> i) & 1u) {
+          const unsigned j = j0 + 128 * t + i;
+          if (BKV_CHECK(o < static_cast<uint32_t>(K) && j < static_cast<unsigned>(L), 622))
+            idx[o] = static_cast<int32_t>(j);
+          ++o;
+        }
     }
   }
 }
@@ -331,7 +339,8 @@ __global__ void __launch_bounds__(kThreads) evict_compact_kernel(const Cache8Evi
   // The next kernel starts when this one ends: its CTAs beside the last of these
   // cost more than they win (36 layers of 8192 rows 120 us, and 117)
   pdl_wait();
-  const int n = a.kept[seq];
+  int n = a.kept[seq];
+  if (!BKV_CHECK(n <= a.K && n <= a.dst_cap, 624)) n = -1;
   if (part == 0 && tid == 0 && head - seq * a.n_kv_heads == 0 && n >= 0 && a.new_lens)
     a.new_lens[seq] = n;
   const int pr = kPr ? kPr : a.head_dim >> 4;
@@ -356,7 +365,9 @@ __global__ void __launch_bounds__(kThreads) evict_compact_kernel(const Cache8Evi
     const int lr = tid & (kRows - 1);
     float wv = 0.f;
     if (lr < rows) {
-      const int j = idx[base + lr];
+      int j = idx[base + lr];
+      // ascending positions, so that no row is overwritten before it is read
+      if (!BKV_CHECK(j >= base + lr && j < a.cap, 625)) j = base + lr;
       const float *sc = (tid < kRows ? a.k_scale : a.v_scale) + ssc0 + (j >> lb);
       s_exp[tid >= kRows][lr] = exp_of(kInPlace ? __ldcg(sc) : __ldg(sc));
       if (tid < kRows) {

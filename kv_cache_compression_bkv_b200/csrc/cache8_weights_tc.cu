@@ -22,6 +22,7 @@
 
 #include <cfloat>
 
+#include "bkv_check.cuh"
 #include "bkv_device_status.cuh"
 #include "cache8_attend.cuh"
 #include "sm100.cuh"
@@ -191,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int r = it * 128 + row, g = kFlat ? r / a.T : it / per_head;
       const int t = kFlat ? r - g * a.T : (tb0 + it - g * per_head) * 128 + row;
       const bool there = g < a.group && t < q.n;
-      const float z = there ? __ldg(lse2 + t * a.group + g) : 0.f;
+      const float z = there && BKV_CHECK(t >= 0 && t < a.T, 645) ? __ldg(lse2 + t * a.group + g) : 0.f;
       z_next = z == -INFINITY ? z : -z;  // a row of logits of -infinity adds nothing
       t_next = there ? t : INT32_MIN;
     };
