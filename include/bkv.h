@@ -372,6 +372,9 @@ bkv_status bkv_cache8_append(const bkv_cache8_desc *desc, void *k8, void *v8,
  *               j >= lens[s] are left as they were
  *   weights_in  device, like weights_out, optional (NULL: zeros); may be
  *               weights_out itself
+ * The weights take every row of the call: drafted tokens that are then rejected
+ * have added theirs (call without weights_out to verify, or keep weights_in), and
+ * decay is applied once a call, whatever T is.
  * Products are summed in f32, f32 queries on the CUDA cores.  On the tensor
  * cores the operands are f16: codes exact; queries under a power of two of their
  * row's own, exact but for elements 2^-32 under its largest; probabilities times

@@ -3,7 +3,8 @@ entry point and with the same names.
 
 Argument marshalling only: each function turns torch tensors into device
 pointers and sizes, passes the current CUDA stream, and raises BkvError for a
-non-zero status.  Every step of the compression runs in the library's CUDA
+non-zero status (the calls of the 8-bit cache look at types and layouts first,
+TypeError and ValueError).  Every step of the compression runs in the library's CUDA
 kernels; there is no fallback of any kind, and importing this module fails
 loudly when the library has not been built.
 """

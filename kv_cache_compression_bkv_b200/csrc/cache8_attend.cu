@@ -36,7 +36,7 @@
 // one of these is passed by 15, so that the f16 operands stay under 2^15: one vote
 // per tile instead of a max over lanes.
 //   Measured: 32 sequences of 517 .. 16384 rows, 32/8 heads of 128, one token, in
-// 109 us, 5.1 TB/s of codes, 79% of the measured copy rate.  What is left is the
+// 109 to 114 us, 4.8 to 5.1 TB/s of codes, 75 to 79% of the measured copy rate.  What is left is the
 // GPU's memory channels, which serve its parts unevenly (CTAs of equal runs end
 // 40 to 58 us into a shorter call; 2 to 6 times as many, shorter runs were
 // slower, 131 us), and the join.
@@ -1085,7 +1085,7 @@ __global__ void __launch_bounds__(kSimtThreads, 5) attend_finish_kernel(const At
   if (p.join_rows > 1 && x.n >= 2 && x.n <= kFewParts) {
     // many rows in few parts: every lane has the parts' pairs of its row for
     // itself, two rows a warp at a time.  1024 tokens of 40/8 heads over 16384
-    // rows: 19 us, and 33 with a lane per part and the lanes joined
+    // rows: 20 us, and 33 with a lane per part and the lanes joined
     for (int i0 = 2 * warp; i0 < rows; i0 += 2 * kSimtWarps) {
       float2 ml[2][kFewParts];
       float4 v[2][kFewParts];
@@ -1331,7 +1331,7 @@ Cache8AttendPlan plan_cache8_attend(int n_seqs, int n_q_heads, int n_kv_heads, i
   // (115): 8 sequences of 8192 rows, 32/8 heads, 8 tokens
   p.nt = !mma || rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 24 ? 3 : head_dim == 128 ? 2 : 4;
   // Measured on both sides: 8 sequences to 8192 rows of 32/8 heads, 40 query rows
-  // a KV head 70 us on tcgen05 and 107 us on mma.sync, 128 rows 87 and 184; 24
+  // a KV head 69 us on tcgen05 and 107 us on mma.sync, 128 rows 89 and 184; 24
   // rows with weights (a key's logits are then kept) 109 and 48.
   p.row_tiles = mma && rows > 32 ? (rows <= 128 ? 1 : 2) : 0;
   p.block_rows = p.row_tiles ? 128 * p.row_tiles : 8 * p.nt;

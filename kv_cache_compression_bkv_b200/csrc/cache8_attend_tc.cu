@@ -25,12 +25,11 @@
 // in TMEM, after the MMAs that are under way.
 //
 // Bound by the tensor cores and exp (a 256 x 128 tile: 2 x 2 x 512 cycles of
-// MMA, 32768 exps at 16 a cycle, each 55% of the time in a long run); one row
-// tile with few rows by the converters.  Measured: 1024 tokens of 40/8 heads of 128
-// over 16384 rows, 320 us (1.04 PFLOP/s of what is visible, 63% of the
-// measured matrix rate); 8
-// sequences to 8192 rows of 32/8 heads, 40 query rows a KV head 72 us, 128 rows 90,
-// 256 rows 113.
+// MMA, 32768 exps at 16 a cycle, each 54% of the time in a long run, and waits for
+// TMEM between them); one row tile with few rows by the converters.  Measured: 1024
+// tokens of 40/8 heads of 128 over 16384 rows, 329 us (1.01 PFLOP/s of what is
+// visible, 61% of the measured matrix rate); 8 sequences to 8192 rows of 32/8 heads,
+// 40 query rows a KV head 69 us, 128 rows 89, 256 rows 113.
 #include <cuda_bf16.h>
 
 #include <cfloat>

@@ -14,7 +14,7 @@
 // beginning and waits lie under the other's exps.
 //
 // Bound by exp: 16384 of them a tile, 1024 cycles at 16 a cycle, against 512 of
-// MMA.  1024 tokens of 40/8 heads over 16384 rows: 235 us, exp's unit at work 78%
+// MMA.  1024 tokens of 40/8 heads over 16384 rows: 235 to 239 us, exp's unit at work 78%
 // of the time (271 us with four epilogue warps a CTA; the second product's own
 // floor is 101 us of MMA and 140 of exp).  Keeping the logits instead would move
 // 2 x 2.7 GB, 830 us at the measured copy rate.
