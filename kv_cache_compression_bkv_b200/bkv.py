@@ -72,14 +72,15 @@ class StepArgs(ctypes.Structure):
 
 STEP_EVENTS = 6
 try:
-    # the current stream's handle: a Stream object would cost 3 us to make
-    from torch._C import _cuda_getCurrentRawStream, _cuda_getDevice
-
-    def _current_stream() -> int:
-        return _cuda_getCurrentRawStream(_cuda_getDevice())
+    # by index and handle: a Stream object would cost 3 us to make
+    from torch._C import _cuda_getCurrentRawStream as _raw_stream
+    from torch._C import _cuda_getDevice as _current_device
 except ImportError:  # a torch without CUDA, where the module is imported all the same
-    def _current_stream() -> int:
-        return torch.cuda.current_stream(torch.cuda.current_device()).cuda_stream
+    def _raw_stream(device: int) -> int:
+        return torch.cuda.current_stream(device).cuda_stream
+
+    def _current_device() -> int:
+        return torch.cuda.current_device()
 
 
 def _load() -> ctypes.CDLL:
@@ -139,7 +140,7 @@ def _ptr(t: torch.Tensor | None):
 
 def _stream(stream) -> int:
     if stream is None:
-        return _current_stream()
+        return _raw_stream(_current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -334,14 +335,14 @@ def bkv_cache8_workspace_size(geom: Geometry8, max_len: int, T: int, K: int,
 
 # These calls are a decode step's, and their time on the host counts: pointers go
 # in as integers, the stream's handle is taken without a Stream object, and of the
-# tensors no more is looked at than the types and the layout that are easily mistaken
-# (lengths in 64 bits, rows that are a view of another order).
+# tensors no more is looked at than what is easily mistaken: types (lengths in 64 bits),
+# layout (rows that are a view of another order), and the device (lengths on the host).
 
 _I32, _F32 = torch.int32, torch.float32
 
 
-def _refuse8(where: str, ints, rows, dtype, floats=()) -> None:
-    """Say which tensor has another type or layout than the library reads."""
+def _refuse8(where: str, device: int, ints, rows, dtype, floats=()) -> None:
+    """Say which tensor has another type, layout or device than the library reads."""
     for group, want in ((ints, _I32), (rows, dtype), (floats, _F32)):
         for name, t in group:
             if t is None:
@@ -350,6 +351,9 @@ def _refuse8(where: str, ints, rows, dtype, floats=()) -> None:
                 raise TypeError(f"{where}: {name} is {t.dtype}, not {want}")
             if not t.is_contiguous():
                 raise ValueError(f"{where}: {name} has to be dense")
+            if t.get_device() != device:
+                raise ValueError(f"{where}: {name} is on {t.device}, not on the current device")
+    raise ValueError(f"{where}: the cache is not on the current device")
 
 
 def _nbytes(t: torch.Tensor | None) -> int:
@@ -359,15 +363,17 @@ def _nbytes(t: torch.Tensor | None) -> int:
 def bkv_cache8_append(geom: Geometry8, k8, v8, k_scale, v_scale, lens, k_new, v_new, T: int,
                       n_new=None, stream=None) -> None:
     """Quantise the newest rows of every sequence into the cache (lens counts them)."""
+    dev = _current_device()
     if not (lens.dtype is _I32 and (n_new is None or n_new.dtype is _I32)
             and k_new.dtype is geom.dtype is v_new.dtype
-            and k_new.is_contiguous() and v_new.is_contiguous()):
-        _refuse8("bkv_cache8_append", (("lens", lens), ("n_new", n_new)),
+            and k_new.is_contiguous() and v_new.is_contiguous()
+            and k8.get_device() == dev == lens.get_device() and k_new.get_device() == dev):
+        _refuse8("bkv_cache8_append", dev, (("lens", lens), ("n_new", n_new)),
                  (("k_new", k_new), ("v_new", v_new)), geom.dtype)
     st = _APPEND8(geom._ref, k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                   lens.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), T,
                   None if n_new is None else n_new.data_ptr(),
-                  _current_stream() if stream is None else _stream(stream))
+                  _raw_stream(dev) if stream is None else _stream(stream))
     if st:
         raise BkvError(st, "bkv_cache8_append")
 
@@ -377,18 +383,20 @@ def bkv_cache8_attend(geom: Geometry8, k8, v8, k_scale, v_scale, lens, max_len: 
                       workspace, stream=None) -> None:
     """Attention of the newest tokens over the cache, with the rows' attention
     weights where weights_out is given; lse, weights_in and weights_out may be None."""
+    dev = _current_device()
     if not (lens.dtype is _I32 and (n_new is None or n_new.dtype is _I32)
             and q.dtype is geom.dtype is out.dtype and q.is_contiguous() and out.is_contiguous()
+            and k8.get_device() == dev == lens.get_device() and q.get_device() == dev
             and (weights_out is None or weights_out.dtype is _F32)
             and (weights_in is None or weights_in.dtype is _F32)
             and (lse is None or lse.dtype is _F32)):
-        _refuse8("bkv_cache8_attend", (("lens", lens), ("n_new", n_new)), (("q", q), ("out", out)),
+        _refuse8("bkv_cache8_attend", dev, (("lens", lens), ("n_new", n_new)), (("q", q), ("out", out)),
                  geom.dtype, (("lse", lse), ("weights_in", weights_in),
                               ("weights_out", weights_out)))
     st = _ATTEND8(geom._ref, k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                   lens.data_ptr(), max_len, q.data_ptr(), T, _ptr(n_new), scale, out.data_ptr(),
                   _ptr(lse), _ptr(weights_in), _ptr(weights_out), decay, _ptr(workspace),
-                  _nbytes(workspace), _stream(stream))
+                  _nbytes(workspace), _raw_stream(dev) if stream is None else _stream(stream))
     if st:
         raise BkvError(st, "bkv_cache8_attend")
 
@@ -399,16 +407,19 @@ def bkv_cache8_evict(geom: Geometry8, k8, v8, k_scale, v_scale, weights, lens, m
                      stream=None) -> None:
     """Keep the first sink, the last recent and the heaviest other rows, K in all,
     in dst (in place when dst's buffers are the source's)."""
+    dev = _current_device()
     if not (lens.dtype is _I32 and weights.dtype is _F32
+            and k8.get_device() == dev == lens.get_device() and k8_dst.get_device() == dev
             and (idx is None or idx.dtype is _I32) and (new_lens is None or new_lens.dtype is _I32)
             and (weights_dst is None or weights_dst.dtype is _F32)):
-        _refuse8("bkv_cache8_evict", (("lens", lens), ("idx", idx), ("new_lens", new_lens)), (),
+        _refuse8("bkv_cache8_evict", dev, (("lens", lens), ("idx", idx), ("new_lens", new_lens)), (),
                  geom.dtype, (("weights", weights), ("weights_dst", weights_dst)))
     st = _EVICT8(geom._ref, k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                  weights.data_ptr(), lens.data_ptr(), max_len, K, sink, recent, dst._ref,
                  k8_dst.data_ptr(), v8_dst.data_ptr(), k_scale_dst.data_ptr(),
                  v_scale_dst.data_ptr(), _ptr(weights_dst), _ptr(idx), _ptr(new_lens),
-                 _ptr(workspace), _nbytes(workspace), _stream(stream))
+                 _ptr(workspace), _nbytes(workspace),
+                 _raw_stream(dev) if stream is None else _stream(stream))
     if st:
         raise BkvError(st, "bkv_cache8_evict")
 

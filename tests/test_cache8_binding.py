@@ -62,8 +62,10 @@ def evict(t):
 
 @pytest.fixture
 def passed(monkeypatch):
-    """The calls that get past the binding, which here end at a stand-in."""
+    """The calls that get past the binding, which here end at a stand-in; the host,
+    which tensors give as device -1, is the current device."""
     calls = []
+    monkeypatch.setattr(bkv, "_current_device", lambda: -1, raising=False)
     for name in ("_APPEND8", "_ATTEND8", "_EVICT8"):
         monkeypatch.setattr(bkv, name, lambda *a, name=name: calls.append(name) or 0)
     return calls
@@ -118,3 +120,18 @@ def test_geometry_of_scales_that_do_not_fit():
     for codes, scales in ((t["k8"].to(BF16), t["ks"]), (t["k8"], t["ks"].double())):
         with pytest.raises(TypeError):
             bkv.geometry8_of(codes, scales, HQ, BF16)
+
+
+@pytest.mark.parametrize("call,name", [
+    (append, "lens"), (append, "k_new"), (append, "k8"), (attend, "lens"), (attend, "q"),
+    (attend, "k8"), (evict, "lens"), (evict, "k8")])
+def test_refuses_another_device(call, name, passed):
+    class Elsewhere(torch.Tensor):
+        def get_device(self):
+            return 5
+
+    t = tensors()
+    t[name] = t[name].as_subclass(Elsewhere)
+    with pytest.raises(ValueError, match="the cache" if name == "k8" else name):
+        call(t)
+    assert not passed
