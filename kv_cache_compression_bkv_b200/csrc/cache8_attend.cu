@@ -10,8 +10,9 @@
 // one per resident CTA, so a ragged batch leaves no CTA idle and a single long
 // sequence uses every SM.  A run can begin and end inside a (sequence, head,
 // row block), a "segment": a CTA that has a whole segment writes its output,
-// one that has a part writes (max, sum, output) to its slot of the workspace and attend_finish_kernel joins the parts in their order.  The
-// lengths are read on the device; the host needs only their upper bound.
+// one that has a part writes (max, sum, output) to its slot of the workspace and
+// attend_finish_kernel joins the parts in their order.  The lengths are read on the
+// device; the host needs only their upper bound.
 //
 // attend_mma_kernel (bf16, head_dim 64 or 128, up to 32 query rows a KV head):
 // decode is bound by the codes' bytes, so each of the 4 warps streams its own 32
@@ -36,10 +37,10 @@
 // one of these is passed by 15, so that the f16 operands stay under 2^15: one vote
 // per tile instead of a max over lanes.
 //   Measured: 32 sequences of 517 .. 16384 rows, 32/8 heads of 128, one token, in
-// 109 to 114 us, 4.8 to 5.1 TB/s of codes, 75 to 79% of the measured copy rate.  What is left is the
-// GPU's memory channels, which serve its parts unevenly (CTAs of equal runs end
-// 40 to 58 us into a shorter call; 2 to 6 times as many, shorter runs were
-// slower, 131 us), and the join.
+// 109 to 114 us, 4.8 to 5.1 TB/s of codes, 75 to 79% of the measured copy rate.
+// What is left is the GPU's memory channels, which serve its parts unevenly (CTAs of
+// equal runs end 40 to 58 us into a shorter call; 2 to 6 times as many, shorter runs
+// were slower, 131 us), and the join.
 //
 // attend_simt_kernel (f32, and other head sizes): the same split with f32
 // products on the CUDA cores.
@@ -80,7 +81,8 @@ constexpr int kSimtKeys = 16;
 // every row sees every key, and first is not looked at.)
 template <int kRows, int kBufs, int kCta, typename T, typename Off>
 __device__ __forceinline__ bool write_segment(const AttendArgs &p, const float *buf, int buf_stride,
-                                              const float *share, const float *m, const float *l, const int *first,
+                                              const float *share, const float *m, const float *l,
+                                              const int *first,
                                               int seq, int unit, const SeqInfo &q, bool whole,
                                               int slot, Off &&off) {
   const Cache8AttendArgs &a = p.a;
@@ -591,7 +593,8 @@ __global__ void __launch_bounds__(kThreads, 2) attend_mma_kernel(const AttendArg
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) bf[at(mt, nt, i)] = o[mt][nt][i] * f[nt][i & 1] * unit[nt][i & 1];
+            for (int i = 0; i < 4; ++i)
+              bf[at(mt, nt, i)] = o[mt][nt][i] * f[nt][i & 1] * unit[nt][i & 1];
       }
       __syncthreads();
       if (warp < 2) {
@@ -605,8 +608,8 @@ __global__ void __launch_bounds__(kThreads, 2) attend_mma_kernel(const AttendArg
       }
       __syncthreads();
       const bool nans = write_segment<Cfg::kRows, 2, kThreads, __nv_bfloat16>(
-          p, s_buf, Cfg::kBuf, nullptr, s_M, s_L, s_first, cur.seq, cur.unit, cur.q, from_start && to_end,
-          from_start ? 1 : 0, [](int r, int d) {
+          p, s_buf, Cfg::kBuf, nullptr, s_M, s_L, s_first, cur.seq, cur.unit, cur.q,
+          from_start && to_end, from_start ? 1 : 0, [](int r, int d) {
             return (((d >> 4) * NT + (r >> 3)) * 4 + ((d >> 3) & 1) * 2 + (r & 1)) * 32 +
                    (d & 7) * 4 + ((r & 7) >> 1);
           });
@@ -884,8 +887,8 @@ __global__ void __launch_bounds__(kSimtThreads, 2) attend_simt_kernel(const Atte
       const bool to_end = cur.tile + 1 == cur.q.tiles;
       seg_tiles = 0;
       const bool nans = write_segment<R, kSimtWarps, kSimtThreads, T>(
-          p, s_buf, R * D, s_share[0], s_M, s_L, s_first, cur.seq, cur.unit, cur.q, from_start && to_end,
-          from_start ? 1 : 0, [D](int r, int d) { return r * D + d; });
+          p, s_buf, R * D, s_share[0], s_M, s_L, s_first, cur.seq, cur.unit, cur.q,
+          from_start && to_end, from_start ? 1 : 0, [D](int r, int d) { return r * D + d; });
       __syncthreads();
       if (nans) reset_first();
       fresh = true;

@@ -489,7 +489,8 @@ __global__ void __launch_bounds__((TcCfg<D, RT, kPre>::kThreads), 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&sh.q_full[x_tile]));
         }
-        const size_t block0 = (static_cast<size_t>(x.seq) * a.n_kv_heads + x.kvh) * (a.cap >> p.log2_block);
+        const size_t block0 =
+            (static_cast<size_t>(x.seq) * a.n_kv_heads + x.kvh) * (a.cap >> p.log2_block);
         for (int j = 0; j < x.live; ++j, ++t) {
           const int buf = RT == 2 ? x_tile : t & 1;
           // lanes 8 i + b: the exponent fields of K's and V's scale in columns 16 b ..

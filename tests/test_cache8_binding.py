@@ -110,7 +110,8 @@ def test_geometry_of_scales_that_do_not_fit():
     assert (g.n_seqs, g.n_q_heads, g.n_kv_heads, g.head_dim, g.capacity, g.block) == (
         S, HQ, H, D, CAP, BLOCK)
     # 15 scales for 256 rows: a floor division gives blocks of 17, 250 // 15 ones of 16
-    for codes, scales in ((t["k8"], torch.ones(S, H, 15)), (t["k8"][:, :, :250].contiguous(), torch.ones(S, H, 15)),
+    for codes, scales in ((t["k8"], torch.ones(S, H, 15)),
+                          (t["k8"][:, :, :250].contiguous(), torch.ones(S, H, 15)),
                           (t["k8"], torch.ones(S, H, 0)), (t["k8"], torch.ones(S, 1, 8)),
                           (t["k8"], torch.ones(1, H, 8)), (t["k8"], torch.ones(S * H, 8)),
                           (t["k8"], torch.ones(S, 8, H).transpose(1, 2)),

@@ -93,11 +93,14 @@ def test_as_many_heads_as_are_allowed(T):
     bkv.bkv_cache8_append(dev.geom, *dev.bufs, L, k.cuda(), v.cuda(), cap, L)
     q = torch.randn(S, Hq, T, d, generator=g).bfloat16()
     n = torch.minimum(lens, torch.tensor(T))
-    out, w = torch.zeros(S, Hq, T, d, dtype=torch.bfloat16, device="cuda"), torch.zeros(S, 1, cap, device="cuda")
-    ws = torch.empty(bkv.bkv_cache8_workspace_size(dev.geom, cap, T, 8, True), dtype=torch.uint8, device="cuda")
+    out = torch.zeros(S, Hq, T, d, dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros(S, 1, cap, device="cuda")
+    ws = torch.empty(bkv.bkv_cache8_workspace_size(dev.geom, cap, T, 8, True), dtype=torch.uint8,
+                     device="cuda")
     bkv.bkv_cache8_attend(dev.geom, *dev.bufs, L, cap, q.cuda(), T, n.int().cuda(), 0.0, out, None, None,
                           w, 1.0, ws)
-    idx, kept = torch.zeros(S, 1, 8, dtype=torch.int32, device="cuda"), torch.zeros(S, dtype=torch.int32, device="cuda")
+    idx = torch.zeros(S, 1, 8, dtype=torch.int32, device="cuda")
+    kept = torch.zeros(S, dtype=torch.int32, device="cuda")
     got_w = w.cpu()
     bkv.bkv_cache8_evict(dev.geom, *dev.bufs, w, L, cap, 8, 1, 2, dev.geom, *dev.bufs, w, idx, kept, ws)
     check_clean()
